@@ -24,9 +24,10 @@
  * Ownership and execution model (all entry points):
  *   - Every pointer is DEVICE memory owned by the caller (except the
  *     grouped call's descriptor array, a host array).  The library never
- *     allocates or frees device memory, keeps no pointer after returning,
- *     and needs no workspace; only the grouped call uses host memory of its
- *     own, for checking its descriptors during the call.
+ *     allocates or frees device memory and keeps no pointer after returning;
+ *     only the attention calls need a workspace, which the caller gives, and
+ *     only the grouped call uses host memory of its own, for checking its
+ *     descriptors during the call.
  *   - `stream` is a hipStream_t (NULL = the null stream).  Calls only enqueue
  *     work; they never synchronise the host.  Buffers must stay alive until
  *     the enqueued work completes.
@@ -71,6 +72,11 @@ typedef int32_t q4_status;
 #define Q4G128_MAX_BATCH 16
 #define Q4G128_MAX_N 0x7FFFFF00LL
 #define Q4G128_INT8_MAX_K 8192
+/* Limits of the cache and attention calls. */
+#define Q4G128_MAX_HEADS 1024
+#define Q4G128_MAX_GROUP 64
+#define Q4G128_MAX_TOKENS 1048576
+#define Q4G128_MAX_SEQUENCES 65536
 
 /*
  * q4g128_pack -- two codes per byte.
@@ -223,6 +229,123 @@ Q4_API q4_status q4g128_gemm_prefill(const uint8_t* packed, const uint16_t* scal
  */
 Q4_API q4_status q4g128_gemv_int8(const int8_t* q, const uint16_t* scales, const uint16_t* x,
                            float* y, int64_t n, int64_t k, void* stream);
+
+/*
+ * Attention between the fused projection and o_proj: three calls over one
+ * paged key-value cache.
+ *
+ * The cache is a pool of pages of `page` token positions each; page number
+ * table[s][i] holds positions i*page .. i*page + page-1 of sequence s.
+ *   k      fp16 [pages][kv_heads][page][dim]   one row per position.
+ *   v      fp16 [pages][kv_heads][dim][page]   one row per dimension: eight
+ *          positions of one dimension are one 16-byte load in the layout the
+ *          matrix cores take, so attention never transposes V.
+ * k_stride / v_stride are the elements from one page to the next (at least
+ * kv_heads*page*dim, a multiple of 8), so that a pool may hold several layers.
+ * A table entry outside [0, pages) is an absent page: nothing is read from or
+ * written to it, and its positions are masked.
+ *   dim in {64, 96, 128, 192, 256}; page a power of two in 16..256; heads a
+ *   multiple of kv_heads with at most 64 heads per kv head (head h reads kv
+ *   head h / (heads / kv_heads)); table_cols*page <= 2^31 - 256.
+ * Contents are device data and are not checked on the host: lengths below 0
+ * count as 0, lengths above max_length as max_length.
+ * The struct is host memory, read during the call and not kept.
+ */
+typedef struct q4g128_kv_cache {
+    uint16_t* k;
+    uint16_t* v;
+    const int32_t* table;  /* [sequences][table_cols] */
+    int64_t pages;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t sequences;
+    int64_t table_cols;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t page;
+} q4g128_kv_cache;
+
+/*
+ * q4g128_rope_append -- new tokens into the cache, and their queries.
+ * Row t of qkv (fp32, `ld` floats from row to row: the output of any product
+ * here, which may go on with other columns) holds `heads` query heads, then
+ * kv_heads key heads, then kv_heads value heads of `dim` columns.  For each
+ * query and key head:
+ *     x = row / sqrt(mean(row^2) + eps) * weight[dim]     (if its norm is given)
+ *     pair i < rot/2, angle a = positions[t] * inv_freq[i]:
+ *     (x_lo, x_hi) = mscale * (x_lo cos a - x_hi sin a, x_hi cos a + x_lo sin a)
+ * with lo, hi = 2i, 2i+1 if interleaved, else i, i + rot/2; dimensions from
+ * rot on are not turned.  Angles are formed in 64 bits, everything else in
+ * fp32, with one rounding to fp16.  Context scaling is the caller's choice of
+ * inv_freq and mscale.
+ *   q [tokens][heads][dim] fp16 is written in full; key and value heads go to
+ *   position positions[t] of sequence seq[t] (seq NULL: token t is of
+ *   sequence t).  A token whose sequence or position is outside the table, or
+ *   whose page is absent, writes no cache entry.  Two tokens of one call must
+ *   not share a position of a sequence.
+ *   rot a multiple of 4 with 0 <= rot <= dim (0: no rotation, inv_freq may be
+ *   NULL); ld a multiple of 4; q_norm / k_norm fp16 [dim] or NULL; eps >= 0.
+ */
+Q4_API q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens, int32_t heads,
+                             const q4g128_kv_cache* cache, const int32_t* seq,
+                             const int32_t* positions, const float* inv_freq, int32_t rot,
+                             int32_t interleaved, float mscale, const uint16_t* q_norm,
+                             const uint16_t* k_norm, float eps, uint16_t* q, void* stream);
+
+/*
+ * What the two attention calls compute for a query at position p of its
+ * sequence, over the positions j that it sees:
+ *     s_j = scale * (q . k_j);  if softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *     if slopes != NULL:        s_j += slopes[head] * (j - p)
+ *     out = sum_j softmax(s)_j v_j
+ * It sees j <= p, with window > 0 only j > p - window, and in the prompt call
+ * also every j < prefix[s].  Scores, softmax statistics and sums are fp32; the
+ * weights enter the second product as fp16 numbers in [0, 1], out is rounded
+ * once to fp16.  A query that sees nothing gives zeros.  What a masked
+ * position or an absent page holds never reaches a result, NaN included.
+ *   scale > 0; softcap >= 0 (0: none); window >= 0 (0: none).
+ */
+typedef struct q4g128_attn_options {
+    float scale;
+    float softcap;
+    int64_t window;
+    const float* slopes;   /* [heads], or NULL */
+    const int32_t* prefix; /* prompt call: [sequences], or NULL; needs window == 0 */
+} q4g128_attn_options;
+
+/*
+ * q4g128_attn_decode -- one new token per sequence.
+ *   q, out [batch][heads][dim] fp16; row b is position lengths[b] - 1 of
+ *   sequence b (table row b; cache->sequences >= batch), whose cache holds
+ *   lengths[b] positions, this token's among them.
+ *   max_length: an upper bound on the lengths, at most table_cols*page; it
+ *   sizes the launch.
+ *   workspace: q4g128_attn_decode_workspace() bytes, 16-byte aligned, contents
+ *   free before and after the call.
+ * The cache's length is split over workgroups and joined in a fixed order.
+ */
+Q4_API int64_t q4g128_attn_decode_workspace(int64_t batch, int32_t heads, int32_t dim);
+Q4_API q4_status q4g128_attn_decode(const uint16_t* q, const q4g128_kv_cache* cache,
+                             const int32_t* lengths, int64_t max_length, int64_t batch,
+                             int32_t heads, const q4g128_attn_options* options, uint16_t* out,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * q4g128_attn_prefill -- the prompt tokens of one or more sequences.
+ *   q, out [tokens][heads][dim] fp16; rows q_starts[s] .. q_starts[s+1]-1
+ *   (q_starts int32 [count + 1], ascending from 0 to tokens) are the last
+ *   positions of sequence s, whose cache holds lengths[s] positions, these
+ *   tokens among them.  A token before position 0 (more tokens than the length
+ *   says) sees nothing.  1 <= count <= 65536 and cache->sequences >= count.
+ *   max_length as above; workspace: q4g128_attn_prefill_workspace() bytes.
+ */
+Q4_API int64_t q4g128_attn_prefill_workspace(int64_t tokens, int64_t count, int32_t heads,
+                             int32_t kv_heads, int32_t dim, int64_t max_length);
+Q4_API q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache,
+                             const int32_t* q_starts, const int32_t* lengths, int64_t max_length,
+                             int64_t tokens, int64_t count, int32_t heads,
+                             const q4g128_attn_options* options, uint16_t* out,
+                             void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Static, NUL-terminated description of a status code. */
 Q4_API const char* q4g128_status_string(q4_status status);

@@ -38,6 +38,20 @@ class GemvDesc(ctypes.Structure):
     _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("mins", ctypes.c_void_p),
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
 
+class KvCache(ctypes.Structure):
+    """struct q4g128_kv_cache of include/q4g128.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("sequences", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("page", ctypes.c_int32)]
+
+
+class AttnOptions(ctypes.Structure):
+    """struct q4g128_attn_options of include/q4g128.h."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int64),
+                ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
 EXPORTED = (
     "q4g128_pack",
     "q4g128_quantize",
@@ -47,6 +61,11 @@ EXPORTED = (
     "q4g128_gemm_prefill",
     "q4g128_gemm_prefill_epilogue",
     "q4g128_gemv_int8",
+    "q4g128_rope_append",
+    "q4g128_attn_decode_workspace",
+    "q4g128_attn_decode",
+    "q4g128_attn_prefill_workspace",
+    "q4g128_attn_prefill",
     "q4g128_status_string",
     "q4g128_last_hip_error",
 )
@@ -77,10 +96,20 @@ def _load():
     lib.q4g128_gemm_prefill.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
     lib.q4g128_gemv_int8.argtypes = [vp, vp, vp, vp, i64, i64, vp]
     lib.q4g128_gemm_prefill_epilogue.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    cache, options = ctypes.POINTER(KvCache), ctypes.POINTER(AttnOptions)
+    lib.q4g128_rope_append.argtypes = [vp, i64, i64, i32, cache, vp, vp, vp, i32, i32, f32, vp, vp, f32, vp, vp]
+    lib.q4g128_attn_decode_workspace.argtypes = [i64, i32, i32]
+    lib.q4g128_attn_decode.argtypes = [vp, cache, vp, i64, i64, i32, options, vp, vp, i64, vp]
+    lib.q4g128_attn_prefill_workspace.argtypes = [i64, i64, i32, i32, i32, i64]
+    lib.q4g128_attn_prefill.argtypes = [vp, cache, vp, vp, i64, i64, i64, i32, options, vp, vp, i64, vp]
     for name in ("q4g128_pack", "q4g128_quantize", "q4g128_gemv", "q4g128_gemv_grouped", "q4g128_gemm_small_batch",
                  "q4g128_gemm_prefill",
-                 "q4g128_gemv_int8", "q4g128_gemm_prefill_epilogue"):
+                 "q4g128_gemv_int8", "q4g128_gemm_prefill_epilogue", "q4g128_rope_append", "q4g128_attn_decode",
+                 "q4g128_attn_prefill"):
         getattr(lib, name).restype = ctypes.c_int32
+    for name in ("q4g128_attn_decode_workspace", "q4g128_attn_prefill_workspace"):
+        getattr(lib, name).restype = ctypes.c_int64
     lib.q4g128_status_string.argtypes = [ctypes.c_int32]
     lib.q4g128_status_string.restype = ctypes.c_char_p
     lib.q4g128_last_hip_error.argtypes = []
@@ -291,6 +320,175 @@ def q4g128_gemv_int8(q, scales, x, y=None, stream=None) -> torch.Tensor:
         _check(_lib.q4g128_gemv_int8(q.data_ptr(), scales.data_ptr(), x.data_ptr(), y.data_ptr(), n, k,
                                      _stream(dev, stream)), "q4g128_gemv_int8")
     return y
+
+
+def _cache(k_cache, v_cache, table) -> KvCache:
+    """The cache descriptor; pages may be a strided slice of a larger pool, each page itself is contiguous."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must live on a GPU (got {t.device})")
+        if t.dtype != torch.float16:
+            raise TypeError(f"{name} must be torch.float16 (got {t.dtype})")
+        if t.dim() != 4:
+            raise ValueError("k_cache must be [pages][kv_heads][page][dim], v_cache [pages][kv_heads][dim][page]")
+    pages, kv_heads, page, dim = k_cache.shape
+    if tuple(v_cache.shape) != (pages, kv_heads, dim, page):
+        raise ValueError(f"v_cache must have shape {(pages, kv_heads, dim, page)} (got {tuple(v_cache.shape)})")
+    if k_cache.stride()[1:] != (page * dim, dim, 1) or v_cache.stride()[1:] != (page * dim, page, 1):
+        raise ValueError("each page of k_cache and v_cache must be contiguous")
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences][table_cols]")
+    _dev_tensor(table, "table", torch.int32, tuple(table.shape))
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), pages, k_cache.stride(0),
+                   v_cache.stride(0), table.shape[0], table.shape[1], kv_heads, dim, page)
+
+
+def _empty(shape, dtype, dev, stream):
+    """Memory of the stream that the call runs on, so that the allocator orders its reuse with the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _optional(t, name, dtype, shape):
+    if t is None:
+        return None
+    _dev_tensor(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq=None, q_norm=None, k_norm=None,
+                       eps=1e-6, interleaved=False, mscale=1.0, q=None, stream=None) -> torch.Tensor:
+    """Head norm, rotary position and cache write of new tokens; returns q fp16 [T][heads][dim].
+
+    qkv: fp32 [T][>= (heads + 2 kv_heads) dim], rows may be strided (a product's output: columns after the
+    value heads are left alone).  k_cache fp16 [pages][kv_heads][page][dim], v_cache fp16
+    [pages][kv_heads][dim][page], table int32 [sequences][cols].  positions int32 [T]; seq int32 [T] (None:
+    token t is of sequence t).  inv_freq fp32 [rot / 2] (None: no rotation).  q_norm, k_norm fp16 [dim] or None.
+    """
+    cache = _cache(k_cache, v_cache, table)
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
+        raise ValueError("qkv must be [T][columns]")
+    tokens, columns = qkv.shape
+    if qkv.device.type != "cuda":
+        raise ValueError(f"qkv must live on a GPU (got {qkv.device})")
+    if qkv.dtype != torch.float32:
+        raise TypeError(f"qkv must be torch.float32 (got {qkv.dtype})")
+    if columns < (heads + 2 * cache.kv_heads) * cache.dim:
+        raise ValueError(f"qkv has {columns} columns, fewer than (heads + 2 kv_heads) dim")
+    if qkv.stride(1) != 1:
+        raise ValueError("rows of qkv must be contiguous")
+    _dev_tensor(positions, "positions", torch.int32, (tokens,))
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    if q is None:
+        q = _empty((tokens, heads, cache.dim), torch.float16, qkv.device, stream)
+    _dev_tensor(q, "q", torch.float16, (tokens, heads, cache.dim))
+    freq = _optional(inv_freq, "inv_freq", torch.float32, (rot // 2,))
+    seqp = _optional(seq, "seq", torch.int32, (tokens,))
+    qn = _optional(q_norm, "q_norm", torch.float16, (cache.dim,))
+    kn = _optional(k_norm, "k_norm", torch.float16, (cache.dim,))
+    dev = _same_device(qkv, k_cache, v_cache, table, positions, q,
+                       *(t for t in (inv_freq, seq, q_norm, k_norm) if t is not None))
+    ld = qkv.stride(0) if tokens > 1 else max(qkv.stride(0), columns + -columns % 4)
+    with torch.cuda.device(dev):
+        _check(_lib.q4g128_rope_append(qkv.data_ptr(), ld, tokens, heads, ctypes.byref(cache), seqp,
+                                       positions.data_ptr(), freq, rot, int(bool(interleaved)), mscale, qn, kn, eps,
+                                       q.data_ptr(), _stream(dev, stream)), "q4g128_rope_append")
+    return q
+
+
+def _attn_args(q, k_cache, v_cache, table, lengths, count, scale, softcap, window, slopes, prefix, max_length, out, stream):
+    """Checks shared by the two attention calls -> (cache, options, max_length, out, device)."""
+    cache = _cache(k_cache, v_cache, table)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [rows][heads][dim]")
+    rows, heads, _ = q.shape
+    _dev_tensor(q, "q", torch.float16, (rows, heads, cache.dim))
+    _dev_tensor(lengths, "lengths", torch.int32, (count,))
+    if count > cache.sequences:
+        raise ValueError(f"table has {cache.sequences} sequences, fewer than {count}")
+    options = AttnOptions(cache.dim ** -0.5 if scale is None else scale, softcap, window,
+                          _optional(slopes, "slopes", torch.float32, (heads,)),
+                          _optional(prefix, "prefix", torch.int32, (count,)))
+    if max_length is None:
+        max_length = cache.table_cols * cache.page
+    if out is None:
+        out = _empty(tuple(q.shape), torch.float16, q.device, stream)
+    _dev_tensor(out, "out", torch.float16, tuple(q.shape))
+    dev = _same_device(q, k_cache, v_cache, table, lengths, out, *(t for t in (slopes, prefix) if t is not None))
+    return cache, options, max_length, out, dev
+
+
+def _workspace(workspace, need, dev, stream):
+    if need < 0:
+        raise Q4Error(need, "attention workspace")
+    if workspace is None:
+        return _empty((need,), torch.uint8, dev, stream)
+    if workspace.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 vector")
+    return workspace
+
+
+def q4g128_attn_decode_workspace(batch, heads, dim) -> int:
+    """Bytes of workspace that q4g128_attn_decode needs."""
+    return _lib.q4g128_attn_decode_workspace(batch, heads, dim)
+
+
+def q4g128_attn_prefill_workspace(tokens, count, heads, kv_heads, dim, max_length) -> int:
+    """Bytes of workspace that q4g128_attn_prefill needs (0: none)."""
+    return _lib.q4g128_attn_prefill_workspace(tokens, count, heads, kv_heads, dim, max_length)
+
+
+def q4g128_attn_decode(q, k_cache, v_cache, table, lengths, scale=None, softcap=0.0, window=0, slopes=None,
+                       max_length=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence: q fp16 [B][heads][dim] -> out fp16 [B][heads][dim].
+
+    lengths int32 [B] counts the cached positions of sequence b (row b of table), the new one included.
+    scale: dim ** -0.5 by default; softcap, window, slopes as in include/q4g128.h.  max_length: an upper bound on
+    the lengths (default: what the table holds).  workspace: uint8 of q4g128_attn_decode_workspace bytes (default:
+    from torch's allocator, per call).
+    """
+    cache, options, max_length, out, dev = _attn_args(q, k_cache, v_cache, table, lengths, q.shape[0], scale, softcap,
+                                                      window, slopes, None, max_length, out, stream)
+    b, heads, dim = q.shape
+    need = _lib.q4g128_attn_decode_workspace(b, heads, dim)
+    workspace = _workspace(workspace, need, dev, stream)
+    with torch.cuda.device(dev):
+        _check(_lib.q4g128_attn_decode(q.data_ptr(), ctypes.byref(cache), lengths.data_ptr(), max_length, b, heads,
+                                       ctypes.byref(options), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       _stream(dev, stream)), "q4g128_attn_decode")
+    return out
+
+
+def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=None, softcap=0.0, window=0, slopes=None,
+                        prefix=None, max_length=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Causal attention of prompt tokens packed over sequences: q fp16 [T][heads][dim] -> out, same shape.
+
+    Rows q_starts[s]..q_starts[s+1]-1 (int32 [S + 1]) are the last positions of sequence s, which holds lengths[s]
+    positions (int32 [S]), these included.  prefix int32 [S]: positions below prefix[s] are seen by every token of
+    the sequence (not together with a window).  Other arguments as q4g128_attn_decode.
+    """
+    cache, options, max_length, out, dev = _attn_args(q, k_cache, v_cache, table, lengths, lengths.shape[0], scale,
+                                                      softcap, window, slopes, prefix, max_length, out, stream)
+    tokens, heads, dim = q.shape
+    count = lengths.shape[0]
+    _dev_tensor(q_starts, "q_starts", torch.int32, (count + 1,))
+    _same_device(q, q_starts)
+    need = _lib.q4g128_attn_prefill_workspace(tokens, count, heads, cache.kv_heads, dim, max_length)
+    workspace = _workspace(workspace, need, dev, stream)
+    with torch.cuda.device(dev):
+        _check(_lib.q4g128_attn_prefill(q.data_ptr(), ctypes.byref(cache), q_starts.data_ptr(), lengths.data_ptr(),
+                                        max_length, tokens, count, heads, ctypes.byref(options), out.data_ptr(),
+                                        workspace.data_ptr(), workspace.numel(), _stream(dev, stream)),
+               "q4g128_attn_prefill")
+    return out
 
 
 def q4g128_status_string(status: int) -> str:

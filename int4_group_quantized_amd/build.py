@@ -28,7 +28,7 @@ DIAG_PATH = os.path.join(PKG_DIR, DIAG_NAME)
 DIAG_SOURCES = ["diag.hip"]
 
 SOURCES = ["api.cpp", "gemv.hip", "gemv_group.hip", "gemv_seg.hip", "prefill.hip", "prefill_split.hip", "prefill_pair.hip", "prefill_epilogue.hip", "pack.hip",
-           "quantize.hip", "head_int8.hip"]
+           "quantize.hip", "head_int8.hip", "rope_append.hip", "attn_decode.hip", "attn_prefill.hip"]
 ARCH = "gfx950"
 
 

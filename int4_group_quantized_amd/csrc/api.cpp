@@ -10,6 +10,7 @@
 #include <utility>
 #include <vector>
 
+#include "attn.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -104,6 +105,104 @@ q4::GemvArgs make_args(const uint8_t* packed, const uint16_t* scales, const uint
     a.n = (int)n;
     a.k = (int)k;
     return a;
+}
+
+// Checks the cache descriptor and fills the kernels' form of it.
+q4_status check_cache(const q4g128_kv_cache* c, int64_t heads, q4::KvCache* out) {
+    if (!c || !c->k || !c->v || !c->table) return Q4_EINVAL;
+    if (c->pages < 1 || c->sequences < 1 || c->table_cols < 1 || c->kv_heads < 1 || heads < 1) return Q4_EINVAL;
+    if (!q4::attn_dim_supported(c->dim)) return Q4_ESHAPE;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return Q4_ESHAPE;
+    if (heads > Q4G128_MAX_HEADS || heads % c->kv_heads != 0 || heads / c->kv_heads > Q4G128_MAX_GROUP)
+        return Q4_ESHAPE;
+    if (c->pages > Q4G128_MAX_N || c->sequences > Q4G128_MAX_N || c->table_cols > Q4G128_MAX_N / c->page)
+        return Q4_ESHAPE;
+    const int64_t per_page = (int64_t)c->kv_heads * c->page * c->dim;
+    if (c->k_stride < per_page || c->v_stride < per_page || c->k_stride % 8 != 0 || c->v_stride % 8 != 0 ||
+        c->k_stride > INT64_MAX / 4 / c->pages || c->v_stride > INT64_MAX / 4 / c->pages)
+        return Q4_ESHAPE;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4)) return Q4_EALIGN;
+    out->k = c->k;
+    out->v = c->v;
+    out->table = c->table;
+    out->k_stride = c->k_stride;
+    out->v_stride = c->v_stride;
+    out->pages = (int)c->pages;
+    out->sequences = (int)c->sequences;
+    out->cols = (int)c->table_cols;
+    out->kv_heads = c->kv_heads;
+    out->dim = c->dim;
+    out->shift = __builtin_ctz((unsigned)c->page);
+    return Q4_OK;
+}
+
+// Bytes from the first to past the last element of a pool.
+size_t pool_bytes(const q4::KvCache& c, long stride) {
+    return ((size_t)(c.pages - 1) * (size_t)stride + ((size_t)c.kv_heads * (size_t)c.dim << c.shift)) * 2;
+}
+
+// Whether the two pools share an element.  Pools whose pages interleave (parts
+// of one larger pool) overlap as ranges without sharing any.
+bool pools_meet(const q4::KvCache& c) {
+    if (!overlaps(c.k, pool_bytes(c, c.k_stride), c.v, pool_bytes(c, c.v_stride))) return false;
+    if (c.k_stride != c.v_stride) return true;
+    const uintptr_t k = (uintptr_t)c.k, v = (uintptr_t)c.v;
+    const uintptr_t stride = (uintptr_t)c.k_stride * 2, page = ((uintptr_t)c.kv_heads * c.dim << c.shift) * 2;
+    const uintptr_t apart = (k > v ? k - v : v - k) % stride;
+    return apart < page || apart > stride - page;
+}
+
+// Whether [p, p + bytes) meets one of the cache's pools or its table.
+bool hits_cache(const q4::KvCache& c, const void* p, size_t bytes) {
+    return overlaps(p, bytes, c.k, pool_bytes(c, c.k_stride)) || overlaps(p, bytes, c.v, pool_bytes(c, c.v_stride)) ||
+           overlaps(p, bytes, c.table, (size_t)c.sequences * (size_t)c.cols * 4);
+}
+
+// Shared checks of the two attention calls; `rows` = batch or tokens.
+q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* lengths, int64_t max_length,
+                          int64_t rows, int64_t sequences, int64_t heads, const q4g128_attn_options* o, uint16_t* out,
+                          void* workspace, int64_t workspace_bytes, int64_t workspace_needed, q4::AttnArgs* a) {
+    if (!q || !lengths || !o || !out || rows < 1 || sequences < 1 || max_length < 1) return Q4_EINVAL;
+    q4_status s = check_cache(cache, heads, &a->c);
+    if (s != Q4_OK) return s;
+    if (rows > Q4G128_MAX_TOKENS || sequences > Q4G128_MAX_SEQUENCES || sequences > cache->sequences ||
+        max_length > cache->table_cols * cache->page)
+        return Q4_ESHAPE;
+    // written so that NaN fails
+    if (!(o->scale > 0.0f) || !(o->softcap >= 0.0f) || o->window < 0 || (o->prefix && o->window > 0)) return Q4_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(o->slopes, 4) ||
+        !aligned(o->prefix, 4) || !aligned(workspace, 16))
+        return Q4_EALIGN;
+    if (workspace_needed > 0 && (!workspace || workspace_bytes < workspace_needed)) return Q4_EINVAL;
+    const size_t qbytes = (size_t)rows * (size_t)heads * (size_t)cache->dim * 2;
+    const size_t seqbytes = (size_t)sequences * 4, wsbytes = (size_t)workspace_needed;
+    if (hits_cache(a->c, out, qbytes) || overlaps(out, qbytes, q, qbytes) || overlaps(out, qbytes, lengths, seqbytes) ||
+        (o->slopes && overlaps(out, qbytes, o->slopes, (size_t)heads * 4)) ||
+        (o->prefix && overlaps(out, qbytes, o->prefix, seqbytes)))
+        return Q4_EINVAL;
+    if (wsbytes > 0 &&
+        (hits_cache(a->c, workspace, wsbytes) || overlaps(workspace, wsbytes, q, qbytes) ||
+         overlaps(workspace, wsbytes, out, qbytes) || overlaps(workspace, wsbytes, lengths, seqbytes) ||
+         (o->slopes && overlaps(workspace, wsbytes, o->slopes, (size_t)heads * 4)) ||
+         (o->prefix && overlaps(workspace, wsbytes, o->prefix, seqbytes))))
+        return Q4_EINVAL;
+    a->q = q;
+    a->lengths = lengths;
+    a->max_length = (int)max_length;
+    a->rows = (int)rows;
+    a->heads = (int)heads;
+    a->group = (int)(heads / cache->kv_heads);
+    a->scale = o->scale;
+    a->softcap = o->softcap;
+    // A window of max_length positions or more hides nothing.
+    a->window = o->window >= max_length ? 0 : (int)o->window;
+    a->slopes = o->slopes;
+    a->prefix = o->prefix;
+    a->out = out;
+    a->workspace = (float*)workspace;
+    a->q_starts = nullptr;
+    a->count = (int)sequences;
+    return Q4_OK;
 }
 
 }  // namespace
@@ -243,6 +342,106 @@ q4_status q4g128_gemv_int8(const int8_t* q, const uint16_t* scales, const uint16
     q4_status s = current_device(&dev);
     if (s != Q4_OK) return s;
     hipError_t e = q4::launch_head_int8(q, scales, x, y, n, k, dev, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens, int32_t heads,
+                             const q4g128_kv_cache* cache, const int32_t* seq, const int32_t* positions,
+                             const float* inv_freq, int32_t rot, int32_t interleaved, float mscale,
+                             const uint16_t* q_norm, const uint16_t* k_norm, float eps, uint16_t* q, void* stream) {
+    if (!qkv || !positions || !q || tokens < 1) return Q4_EINVAL;
+    q4::AppendArgs a;
+    q4_status s = check_cache(cache, heads, &a.c);
+    if (s != Q4_OK) return s;
+    const int64_t dim = cache->dim, columns = ((int64_t)heads + 2 * (int64_t)cache->kv_heads) * dim;
+    if (rot < 0 || rot > dim || rot % 4 != 0 || tokens > Q4G128_MAX_TOKENS || ld < columns || ld % 4 != 0 ||
+        ld > INT64_MAX / 8 / tokens)
+        return Q4_ESHAPE;
+    if ((rot > 0 && !inv_freq) || !(eps >= 0.0f)) return Q4_EINVAL;  // written so that NaN fails
+    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(seq, 4) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+        !aligned(q_norm, 2) || !aligned(k_norm, 2))
+        return Q4_EALIGN;
+    const size_t qbytes = (size_t)tokens * (size_t)heads * (size_t)dim * 2, nbytes = (size_t)dim * 2;
+    const void* in[] = {qkv, seq, positions, inv_freq, q_norm, k_norm};
+    const size_t inbytes[] = {((size_t)(tokens - 1) * (size_t)ld + (size_t)columns) * 4, (size_t)tokens * 4,
+                              (size_t)tokens * 4, (size_t)rot * 2, nbytes, nbytes};
+    if (pools_meet(a.c)) return Q4_EINVAL;
+    const size_t kbytes = pool_bytes(a.c, a.c.k_stride), vbytes = pool_bytes(a.c, a.c.v_stride);
+    const size_t tbytes = (size_t)a.c.sequences * (size_t)a.c.cols * 4;
+    if (hits_cache(a.c, q, qbytes) || overlaps(a.c.k, kbytes, a.c.table, tbytes) ||
+        overlaps(a.c.v, vbytes, a.c.table, tbytes))
+        return Q4_EINVAL;
+    for (int i = 0; i < 6; ++i)
+        if (in[i] && (overlaps(q, qbytes, in[i], inbytes[i]) || overlaps(a.c.k, kbytes, in[i], inbytes[i]) ||
+                      overlaps(a.c.v, vbytes, in[i], inbytes[i])))
+            return Q4_EINVAL;
+    a.qkv = qkv;
+    a.ld = ld;
+    a.tokens = (int)tokens;
+    a.heads = heads;
+    a.seq = seq;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.rot = rot;
+    a.interleaved = interleaved != 0;
+    a.mscale = mscale;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    a.q = q;
+    hipError_t e = q4::launch_rope_append(a, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+int64_t q4g128_attn_decode_workspace(int64_t batch, int32_t heads, int32_t dim) {
+    if (batch < 1 || heads < 1) return Q4_EINVAL;
+    if (batch > Q4G128_MAX_SEQUENCES || heads > Q4G128_MAX_HEADS || !q4::attn_dim_supported(dim)) return Q4_ESHAPE;
+    return q4::attn_decode_workspace(batch, heads, dim);
+}
+
+q4_status q4g128_attn_decode(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* lengths,
+                             int64_t max_length, int64_t batch, int32_t heads, const q4g128_attn_options* options,
+                             uint16_t* out, void* workspace, int64_t workspace_bytes, void* stream) {
+    q4::AttnArgs a;
+    const int64_t need = cache ? q4g128_attn_decode_workspace(batch, heads, cache->dim) : Q4_EINVAL;
+    if (need < 0) return (q4_status)need;
+    if (options && options->prefix) return Q4_EINVAL;
+    q4_status s = check_attention(q, cache, lengths, max_length, batch, batch, heads, options, out, workspace,
+                                  workspace_bytes, need, &a);
+    if (s != Q4_OK) return s;
+    hipError_t e = q4::launch_attn_decode(a, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+int64_t q4g128_attn_prefill_workspace(int64_t tokens, int64_t count, int32_t heads, int32_t kv_heads, int32_t dim,
+                                      int64_t max_length) {
+    if (tokens < 1 || count < 1 || heads < 1 || kv_heads < 1 || max_length < 1) return Q4_EINVAL;
+    if (tokens > Q4G128_MAX_TOKENS || count > Q4G128_MAX_SEQUENCES || heads > Q4G128_MAX_HEADS ||
+        heads % kv_heads != 0 || heads / kv_heads > Q4G128_MAX_GROUP || !q4::attn_dim_supported(dim) ||
+        max_length > Q4G128_MAX_N)
+        return Q4_ESHAPE;
+    return q4::attn_prefill_workspace(tokens, count, heads, kv_heads, dim, max_length);
+}
+
+q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* q_starts,
+                              const int32_t* lengths, int64_t max_length, int64_t tokens, int64_t count, int32_t heads,
+                              const q4g128_attn_options* options, uint16_t* out, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+    q4::AttnArgs a;
+    if (!q_starts) return Q4_EINVAL;
+    const int64_t need =
+        cache ? q4g128_attn_prefill_workspace(tokens, count, heads, cache->kv_heads, cache->dim, max_length) : Q4_EINVAL;
+    if (need < 0) return (q4_status)need;
+    q4_status s = check_attention(q, cache, lengths, max_length, tokens, count, heads, options, out, workspace,
+                                  workspace_bytes, need, &a);
+    if (s != Q4_OK) return s;
+    if (!aligned(q_starts, 4)) return Q4_EALIGN;
+    const size_t sbytes = (size_t)(count + 1) * 4;
+    if (overlaps(out, (size_t)tokens * (size_t)heads * (size_t)cache->dim * 2, q_starts, sbytes) ||
+        (need > 0 && overlaps(workspace, (size_t)need, q_starts, sbytes)))
+        return Q4_EINVAL;
+    a.q_starts = q_starts;
+    hipError_t e = q4::launch_attn_prefill(a, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

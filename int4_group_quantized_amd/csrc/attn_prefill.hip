@@ -1,0 +1,457 @@
+// Attention of prompt tokens over the paged cache (gfx950).
+//
+//   out[t][h] = sum_j softmax_j(s(q[t][h] . k_j)) v_j  over the positions j that
+//   token t sees: causal, its own sequence only, optionally within a window or
+//   with a prefix that every token sees.
+//
+// A workgroup of four waves serves 128 query rows of one kv head: the tokens
+// of one tile times the heads of the group (row = token * group + head), so
+// that every key and value read serves the whole group.  One pass over the
+// visible tiles of 64 positions keeps the running maximum and sum of the
+// softmax; scores and outputs stay in registers.
+//
+// Products with v_mfma_f32_32x32x16_f16, 32 rows per wave:
+//   S^T[key][row] = K Q^T     A = K rows from LDS, B = the query rows, in registers
+//   O^T[dim][row] = V^T P^T   A = V pages' rows from LDS, B = P^T
+// The result of the first (lane: row = lane & 31, h = lane >> 5, register r:
+// matrix row 4h + r%4 + 8(r/4)) is the operand of the second (k = 8h + j of
+// each 16) as it stands when matrix row m of a 32-key block loads key
+// 16(m/16) + 8(m/4%2) + 4(m/8%2) + m%4: register r then is key 16(r/8) + 8h + r%8.
+//
+// LDS rows are swizzled in 16-byte chunks (chunk ^ a function of the row) so
+// that the 32 rows of an operand load fall on different banks.  The next tile
+// is on its way from memory in registers while this one is computed.
+//
+// Few tokens on a long cache leave most CUs idle, so the visible tiles are
+// then cut into equal splits joined by a second launch.
+#include "attn_softmax.hpp"
+
+namespace q4 {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+constexpr int kPrefillWaves = 4;
+constexpr int kPrefillThreads = 64 * kPrefillWaves;
+constexpr int kPrefillRows = 32 * kPrefillWaves;
+constexpr int kPrefillBlocks = 512;     // workgroups below which the cache is split
+constexpr int kPrefillMinTiles = 4;     // tiles per split at least
+
+// Tokens per workgroup.
+__host__ __device__ inline int prefill_tokens(int group) { return kPrefillRows / group; }
+
+static long prefill_tiles(long tokens, long count, int group) {
+    const int tb = prefill_tokens(group);
+    const long a = tokens / tb + count;  // sum of ceil(n_s / tb) at most
+    return a < tokens ? a : tokens;      // each tile has a token
+}
+
+static int prefill_splits(long tokens, long count, int group, int kv_heads, long max_length) {
+    const long blocks = prefill_tiles(tokens, count, group) * kv_heads;
+    const long most = ((max_length + kTileKeys - 1) / kTileKeys + kPrefillMinTiles - 1) / kPrefillMinTiles;
+    const long want = kPrefillBlocks / blocks;
+    const long n = want < most ? want : most;
+    return n > 1 ? (int)n : 1;
+}
+
+int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length) {
+    const int splits = prefill_splits(tokens, count, heads / kv_heads, kv_heads, max_length);
+    return splits == 1 ? 0 : (int64_t)splits * tokens * heads * (dim + 2) * (int64_t)sizeof(float);
+}
+
+struct PrefillTile {
+    int s;      // sequence, or -1
+    int token;  // first token of the tile (row of q)
+    int n;      // tokens in the tile
+    int pos;    // position of the first token (may be negative)
+    int len;    // positions of the sequence
+};
+
+// Tile number `item`; a sequence's last tokens, which see the most positions, come first.
+__device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item) {
+    const int lane = threadIdx.x & 63;
+    const int tb = prefill_tokens(a.group);
+    PrefillTile r;
+    r.s = -1;
+    r.token = r.n = r.pos = r.len = 0;
+    int before = 0;
+    for (int s0 = 0; s0 < a.count; s0 += 64) {
+        int st = 0, en = 0;
+        if (s0 + lane < a.count) {
+            st = min(max(a.q_starts[s0 + lane], 0), a.rows);
+            en = min(max(a.q_starts[s0 + lane + 1], st), a.rows);
+        }
+        const int n = (en - st + tb - 1) / tb;
+        int upto = n;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += o;
+        }
+        const uint64_t hit = __ballot(n > 0 && item < before + upto && item >= before + upto - n);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const int first = __builtin_amdgcn_readlane(st, l), last = __builtin_amdgcn_readlane(en, l);
+            const int tiles = __builtin_amdgcn_readlane(n, l);
+            const int t = tiles - 1 - (item - (before + __builtin_amdgcn_readlane(upto, l) - tiles));
+            r.s = s0 + l;
+            r.token = first + t * tb;
+            r.n = min(tb, last - r.token);
+            r.len = min(max(a.lengths[r.s], 0), a.max_length);
+            r.pos = r.len - (last - first) + t * tb;
+            return r;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return r;
+}
+
+// Chunk of 16 bytes (eight halves) c of K row `key`, and of V row `dim`, in LDS.
+template <int D>
+__device__ __forceinline__ int k_chunk(int key, int c) {
+    constexpr int MASK = D % 64 == 0 ? 7 : 3;  // dim 96 has 12 chunks, which only two bits permute
+    const int f = (key & 3) | ((key >> 1) & 4);
+    return key * (D / 8) + (c ^ (f & MASK));
+}
+__device__ __forceinline__ int v_chunk(int dim, int c) { return dim * (kTileKeys / 8) + (c ^ (dim & 7)); }
+
+__device__ __forceinline__ h8 as_h8(u4 v) { return __builtin_bit_cast(h8, v); }
+
+// Halves of a dword whose exponent is all ones (infinite or NaN), as bits 0 and 16.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+    return (((w & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
+}
+
+// Eight halves split into their finite values (others zero) and two sets of
+// zeros and ones: +inf or NaN, and -inf or NaN.
+struct OddSplit {
+    h8 fine, up, down;
+};
+__device__ __forceinline__ OddSplit split_odd(u4 v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, up[4], down[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t odd = odd_halves(w[i]);
+        const uint32_t nan = (((w[i] & 0x03FF03FFu) + 0x03FF03FFu) >> 10) & odd;
+        const uint32_t neg = (w[i] >> 15) & odd;
+        up[i] = (nan | (odd & ~neg)) * 0x3C00u;  // fp16 1.0
+        down[i] = (nan | neg) * 0x3C00u;
+        w[i] &= ~(odd * 0xFFFFu);
+    }
+    return {as_h8((u4){w[0], w[1], w[2], w[3]}), as_h8((u4){up[0], up[1], up[2], up[3]}),
+            as_h8((u4){down[0], down[1], down[2], down[3]})};
+}
+
+template <int D, bool EXTRA>
+__global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefill_kernel(AttnArgs a, int tile0, int splits) {
+    constexpr int C = D / 8;             // 16-byte chunks of a K row
+    constexpr int STAGE = D / 32;        // chunks per thread and tile, for K and for V
+    __shared__ u4 k_lds[kTileKeys * C];
+    __shared__ u4 v_lds[D * (kTileKeys / 8)];
+    const int kvh = blockIdx.x % a.c.kv_heads;
+    const int rest = blockIdx.x / a.c.kv_heads;
+    const int split = rest % splits;
+    const PrefillTile it = prefill_tile(a, tile0 + rest / splits);
+    if (it.s < 0) return;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int n = lane & 31, h = lane >> 5;
+
+    // This lane's query row and the positions it sees: lo <= j < hi.
+    const int r = wave * 32 + n;
+    const int tok = r / a.group;
+    const bool live = tok < it.n;
+    const int head = kvh * a.group + (live ? r % a.group : 0);
+    const int token = it.token + (live ? tok : 0);
+    const int qpos = it.pos + tok;
+    const int prefix = a.prefix ? a.prefix[it.s] : 0;
+    int hi = 0, lo = 0;
+    if (live && qpos >= 0) {
+        hi = min(max(qpos + 1, prefix), it.len);
+        lo = a.window > 0 ? max(qpos + 1 - a.window, 0) : 0;
+    }
+    // The wave's rows: all see [all_lo, all_hi), none sees from any_hi on.
+    int all_hi = live ? hi : 0x7FFFFFFF, any_hi = hi, all_lo = lo;
+    for (int d = 16; d >= 1; d >>= 1) {
+        all_hi = min(all_hi, __shfl_xor(all_hi, d, 64));
+        any_hi = max(any_hi, __shfl_xor(any_hi, d, 64));
+        all_lo = max(all_lo, __shfl_xor(all_lo, d, 64));
+    }
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
+    all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+
+    // Tiles of the workgroup: the first token sees the lowest position, the last
+    // (or the prefix) the highest.
+    const int last = it.pos + it.n - 1;
+    const int wg_hi = last >= 0 ? min(max(last + 1, prefix), it.len) : 0;
+    const int wg_lo = a.window > 0 ? max(it.pos + 1 - a.window, 0) : 0;
+    const int first_tile = wg_lo / kTileKeys;
+    const int tiles = max((wg_hi + kTileKeys - 1) / kTileKeys - first_tile, 0);
+    const int per = (tiles + splits - 1) / splits;
+    const int t_begin = first_tile + split * per;
+    const int t_end = min(t_begin + per, first_tile + tiles);
+
+    h8 qf[D / 16];
+    {
+        const u4* qp = reinterpret_cast<const u4*>(a.q + ((size_t)token * a.heads + head) * D + 8 * h);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            qf[s] = as_h8(qp[2 * s]);
+            if (!live) qf[s] = (h8)(_Float16)0.0f;
+        }
+    }
+    const ScoreParams sp = score_params<EXTRA>(a, head);
+    const int pmask = (1 << a.c.shift) - 1;
+    const int* row = a.c.table + (size_t)it.s * a.c.cols;
+
+    u4 sk[STAGE], sv[STAGE];
+    int pages[4];  // of the tile's quarters
+    auto load = [&](int t) {
+        const int kb = t * kTileKeys;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pages[i] = page_of(a.c, row, min(kb + 16 * i, it.len - 1));
+        auto page = [&](int quarter) {
+            const int p = quarter < 2 ? (quarter == 0 ? pages[0] : pages[1]) : (quarter == 2 ? pages[2] : pages[3]);
+            return (size_t)max(p, 0);
+        };
+#pragma unroll
+        for (int j = 0; j < STAGE; ++j) {
+            const int idx = tid + kPrefillThreads * j;
+            const int key = idx / C, c = idx % C;
+            sk[j] = *reinterpret_cast<const u4*>(a.c.k + page(key >> 4) * a.c.k_stride +
+                                                 (((size_t)kvh << a.c.shift) + ((kb + key) & pmask)) * D + 8 * c);
+            const int dim = idx >> 3, vc = idx & 7;
+            sv[j] = *reinterpret_cast<const u4*>(a.c.v + page(vc >> 1) * a.c.v_stride +
+                                                 ((size_t)(kvh * D + dim) << a.c.shift) + ((kb + 8 * vc) & pmask));
+        }
+    };
+
+    f16v acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = (f16v)0.0f;
+    float m = Q4_NEG_INF, l = 0.0f;
+    const int km = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);  // key of this lane's K row
+
+    if (t_begin < t_end) load(t_begin);
+    for (int t = t_begin; t < t_end; ++t) {
+        const int kb = t * kTileKeys;
+        const bool absent = (pages[0] | pages[1] | pages[2] | pages[3]) < 0;  // of this tile
+        const bool gone[4] = {pages[0] < 0, pages[1] < 0, pages[2] < 0, pages[3] < 0};
+        if (t > t_begin) __syncthreads();  // the last tile's reads are done
+        if (absent || kb + kTileKeys > it.len) {
+            // Values past the end and of absent pages are cleared: their weight is
+            // zero, but zero times what an unwritten slot holds may be NaN.
+#pragma unroll
+            for (int j = 0; j < STAGE; ++j) {
+                const int vc = (tid + kPrefillThreads * j) & 7;
+                const bool dead = vc < 4 ? (vc < 2 ? gone[0] : gone[1]) : (vc < 6 ? gone[2] : gone[3]);
+                const int keep = dead ? 0 : min(max(it.len - (kb + 8 * vc), 0), 8);
+                uint32_t w[4] = {sv[j].x, sv[j].y, sv[j].z, sv[j].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e >= keep) w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                sv[j] = (u4){w[0], w[1], w[2], w[3]};
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < STAGE; ++j) {
+            const int idx = tid + kPrefillThreads * j;
+            k_lds[k_chunk<D>(idx / C, idx % C)] = sk[j];
+            v_lds[v_chunk(idx >> 3, idx & 7)] = sv[j];
+        }
+        __syncthreads();
+        if (t + 1 < t_end) load(t + 1);
+        if (kb >= any_hi) continue;  // nothing here for this wave (its barriers are above)
+
+        f16v s[2];
+        s[0] = s[1] = (f16v)0.0f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(k_lds[k_chunk<D>(32 * b + km, 2 * d + h)]), qf[d],
+                                                              s[b], 0, 0, 0);
+        }
+        const bool masked = absent || kb < all_lo || kb + kTileKeys > all_hi;
+        float top = Q4_NEG_INF;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int key = kb + 32 * b + 16 * (i >> 3) + 8 * h + (i & 7);
+                float x = score<EXTRA>(s[b][i], sp, key - qpos);
+                if (masked) x = key >= lo && key < hi && !gone[2 * b + (i >> 3)] ? x : Q4_NEG_INF;
+                s[b][i] = x;
+                top = fmaxf(top, x);
+            }
+        }
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float m_new = fmaxf(m, top);
+        const float base = m_new == Q4_NEG_INF ? 0.0f : m_new;
+        const float f = exp2_hw(m - base);
+        if (__any(m_new > m)) {
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) acc[d] *= f;
+        }
+        float sum = 0.0f;
+        h8 pf[4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float p = exp2_hw(s[b][i] - base);
+                sum += p;
+                pf[2 * b + (i >> 3)][i & 7] = (_Float16)p;
+            }
+        }
+        l = l * f + sum;
+        m = m_new;
+
+        bool dirty = false;
+        if (masked) {
+            // A weight of zero hides a masked value only if the value is finite.
+            uint32_t bad = 0;
+#pragma unroll 4
+            for (int i = lane; i < D * (kTileKeys / 8); i += 64) {
+                const u4 v = v_lds[i];
+                bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
+            }
+            dirty = __any(bad != 0);
+        }
+        if (!dirty) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d)
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(v_lds[v_chunk(32 * d + n, 2 * kk + h)]),
+                                                                    pf[kk], acc[d], 0, 0, 0);
+            }
+        } else {
+            // Finite values as above; infinities and NaN that a row sees are counted
+            // by two products of zeros and ones and added as what they are.
+#pragma unroll 1
+            for (int kk = 0; kk < 4; ++kk) {
+                const h8 p = kk < 2 ? (kk == 0 ? pf[0] : pf[1]) : (kk == 2 ? pf[2] : pf[3]);
+                const bool is_gone = kk < 2 ? (kk == 0 ? gone[0] : gone[1]) : (kk == 2 ? gone[2] : gone[3]);
+                const int k0 = kb + 16 * kk + 8 * h;
+                const int from = is_gone ? 8 : lo - k0, to = hi - k0;  // keys k0 + from .. k0 + to - 1 are seen
+                uint32_t sw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sw[e] = (2 * e >= from && 2 * e < to ? 0x3C00u : 0u) |
+                            (2 * e + 1 >= from && 2 * e + 1 < to ? 0x3C000000u : 0u);
+                const h8 seen = as_h8((u4){sw[0], sw[1], sw[2], sw[3]});
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) {
+                    const OddSplit v = split_odd(v_lds[v_chunk(32 * d + n, 2 * kk + h)]);
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v.fine, p, acc[d], 0, 0, 0);
+                    const f16v u = __builtin_amdgcn_mfma_f32_32x32x16_f16(v.up, seen, (f16v)0.0f, 0, 0, 0);
+                    const f16v w = __builtin_amdgcn_mfma_f32_32x32x16_f16(v.down, seen, (f16v)0.0f, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (u[i] > 0.0f) acc[d][i] += __builtin_inff();
+                        if (w[i] > 0.0f) acc[d][i] += Q4_NEG_INF;
+                    }
+                }
+            }
+        }
+    }
+    l += __shfl_xor(l, 32, 64);
+
+    if (!live) return;
+    if (splits == 1) {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        uint16_t* op = a.out + ((size_t)token * a.heads + head) * D;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint2 w;
+                w.x = as_u32((h2){(_Float16)(acc[d][4 * i] * inv), (_Float16)(acc[d][4 * i + 1] * inv)});
+                w.y = as_u32((h2){(_Float16)(acc[d][4 * i + 2] * inv), (_Float16)(acc[d][4 * i + 3] * inv)});
+                *reinterpret_cast<uint2*>(op + 32 * d + 8 * i + 4 * h) = w;
+            }
+        }
+    } else {
+        const long at = ((long)split * a.rows + token) * a.heads + head;
+        float* op = a.workspace + at * D;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f4*>(op + 32 * d + 8 * i + 4 * h) =
+                    (f4){acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        }
+        if (h == 0) {
+            float* ml = a.workspace + (long)splits * a.rows * a.heads * D + at * 2;
+            ml[0] = m;
+            ml[1] = l;
+        }
+    }
+}
+
+// Join of the splits of one query row, one wave each, in order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int splits) {
+    const int lane = threadIdx.x & 63;
+    const long rows = (long)a.rows * a.heads;
+    const long r = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r >= rows) return;
+    // Tokens outside every sequence have no parts.
+    const int token = (int)(r / a.heads);
+    if (token < a.q_starts[0] || token >= a.q_starts[a.count]) return;
+    const float* ml = a.workspace + (long)splits * rows * D;
+    float top = Q4_NEG_INF;
+    for (int s = lane; s < splits; s += 64) top = fmaxf(top, ml[(s * rows + r) * 2]);
+    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    constexpr int PER = (D + 63) / 64;
+    float o[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] = 0.0f;
+    float sum = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+        const float f = part_weight(ml[(s * rows + r) * 2], top);
+        sum += ml[(s * rows + r) * 2 + 1] * f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 64 * i < D) o[i] += a.workspace[(s * rows + r) * D + lane + 64 * i] * f;
+    }
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (lane + 64 * i < D)
+            a.out[r * D + lane + 64 * i] = __builtin_bit_cast(uint16_t, (_Float16)(o[i] * inv));
+}
+
+template <int D>
+static hipError_t launch_prefill_attn(const AttnArgs& a, hipStream_t st) {
+    const long tiles = prefill_tiles(a.rows, a.count, a.group);
+    const int splits = prefill_splits(a.rows, a.count, a.group, a.c.kv_heads, a.max_length);
+    const long per_tile = (long)a.c.kv_heads * splits;
+    const long most = ((1L << 24) - 1) / per_tile;  // tiles of one launch: at most 2^32 - 1 threads
+    const bool extra = a.softcap > 0.0f || a.slopes;
+    for (long t = 0; t < tiles; t += most) {
+        const dim3 grid((unsigned)((tiles - t < most ? tiles - t : most) * per_tile));
+        if (extra)
+            hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, dim3(kPrefillThreads), 0, st, a, (int)t, splits);
+        else
+            hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, dim3(kPrefillThreads), 0, st, a, (int)t, splits);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (splits == 1) return hipSuccess;
+    const long rows = (long)a.rows * a.heads;
+    hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a, splits);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t st) {
+    switch (a.c.dim) {
+        case 64: return launch_prefill_attn<64>(a, st);
+        case 96: return launch_prefill_attn<96>(a, st);
+        case 128: return launch_prefill_attn<128>(a, st);
+        case 192: return launch_prefill_attn<192>(a, st);
+        case 256: return launch_prefill_attn<256>(a, st);
+    }
+    return hipErrorInvalidValue;  // widths are validated before
+}
+
+}  // namespace q4
