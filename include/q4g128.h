@@ -34,7 +34,8 @@
  *   - Outputs are fully overwritten and must not overlap any input.
  *   - Arguments are validated on the host before any HIP call; an invalid
  *     call enqueues nothing.
- *   - Results are deterministic: no atomics, fixed reduction orders.
+ *   - Results are deterministic: fixed reduction orders; the only atomics
+ *     count finished workgroups.
  *
  * Limits: 1 <= N <= 2^31 - 256; K a multiple of 128 with 128 <= K <= 32768;
  * batch / prompt rows at most 2^31 - 256.
@@ -77,6 +78,7 @@ typedef int32_t q4_status;
 #define Q4G128_MAX_GROUP 64
 #define Q4G128_MAX_TOKENS 1048576
 #define Q4G128_MAX_SEQUENCES 65536
+#define Q4G128_ATTN_COUNTER_BYTES 2048
 
 /*
  * q4g128_pack -- two codes per byte.
@@ -320,9 +322,13 @@ typedef struct q4g128_attn_options {
  *   lengths[b] positions, this token's among them.
  *   max_length: an upper bound on the lengths, at most table_cols*page; it
  *   sizes the launch.
- *   workspace: q4g128_attn_decode_workspace() bytes, 16-byte aligned, contents
- *   free before and after the call.
- * The cache's length is split over workgroups and joined in a fixed order.
+ *   workspace: q4g128_attn_decode_workspace() bytes, 16-byte aligned.  Its
+ *   first Q4G128_ATTN_COUNTER_BYTES must be zero before its first use; every
+ *   call leaves them zero.  Calls that may run at the same time (on different
+ *   streams) need workspaces of their own; calls of any shape on one stream can
+ *   share one, which q4g128_attn_prefill may use too.
+ * The cache's length is split over workgroups; the last one of a sequence to
+ * finish joins their results, in the order of the positions whichever it is.
  */
 Q4_API int64_t q4g128_attn_decode_workspace(int64_t batch, int32_t heads, int32_t dim);
 Q4_API q4_status q4g128_attn_decode(const uint16_t* q, const q4g128_kv_cache* cache,
@@ -337,7 +343,9 @@ Q4_API q4_status q4g128_attn_decode(const uint16_t* q, const q4g128_kv_cache* ca
  *   positions of sequence s, whose cache holds lengths[s] positions, these
  *   tokens among them.  A token before position 0 (more tokens than the length
  *   says) sees nothing.  1 <= count <= 65536 and cache->sequences >= count.
- *   max_length as above; workspace: q4g128_attn_prefill_workspace() bytes.
+ *   max_length as above.  workspace: q4g128_attn_prefill_workspace() bytes (0:
+ *   none is needed, it may be NULL), 16-byte aligned; its first
+ *   Q4G128_ATTN_COUNTER_BYTES are left alone, the rest may hold anything.
  */
 Q4_API int64_t q4g128_attn_prefill_workspace(int64_t tokens, int64_t count, int32_t heads,
                              int32_t kv_heads, int32_t dim, int64_t max_length);

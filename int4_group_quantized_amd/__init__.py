@@ -31,6 +31,7 @@ MAX_K = 32768
 MAX_BATCH = 16
 INT8_MAX_K = 8192
 MAX_GROUPED = 65536
+ATTN_COUNTER_BYTES = 2048
 
 
 class GemvDesc(ctypes.Structure):
@@ -424,16 +425,32 @@ def _attn_args(q, k_cache, v_cache, table, lengths, count, scale, softcap, windo
     return cache, options, max_length, out, dev
 
 
+# The workspaces that the attention calls use when none is given: one per device
+# and stream (calls on one stream run one after the other), grown as needed,
+# with its counters zeroed once.
+_workspaces = {}
+
+
 def _workspace(workspace, need, dev, stream):
     if need < 0:
         raise Q4Error(need, "attention workspace")
-    if workspace is None:
-        return _empty((need,), torch.uint8, dev, stream)
-    if workspace.device != dev:
-        raise ValueError("all tensors must be on the same GPU")
-    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 vector")
-    return workspace
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 vector")
+        return workspace
+    on = torch.cuda.current_stream(dev) if stream is None else stream
+    with torch.cuda.stream(on):
+        # A graph may be replayed on any stream: calls in a capture get memory of their own.
+        capturing = torch.cuda.is_current_stream_capturing()
+        got = None if capturing else _workspaces.get((dev.index, on.cuda_stream))
+        if got is None or got.numel() < need:
+            got = torch.empty((need,), dtype=torch.uint8, device=dev)
+            got[:ATTN_COUNTER_BYTES].zero_()
+            if not capturing:
+                _workspaces[dev.index, on.cuda_stream] = got
+    return got
 
 
 def q4g128_attn_decode_workspace(batch, heads, dim) -> int:
@@ -452,8 +469,8 @@ def q4g128_attn_decode(q, k_cache, v_cache, table, lengths, scale=None, softcap=
 
     lengths int32 [B] counts the cached positions of sequence b (row b of table), the new one included.
     scale: dim ** -0.5 by default; softcap, window, slopes as in include/q4g128.h.  max_length: an upper bound on
-    the lengths (default: what the table holds).  workspace: uint8 of q4g128_attn_decode_workspace bytes (default:
-    from torch's allocator, per call).
+    the lengths (default: what the table holds).  workspace: uint8 of q4g128_attn_decode_workspace bytes, its first
+    ATTN_COUNTER_BYTES zero before its first use (default: one that the binding keeps for the stream).
     """
     cache, options, max_length, out, dev = _attn_args(q, k_cache, v_cache, table, lengths, q.shape[0], scale, softcap,
                                                       window, slopes, None, max_length, out, stream)

@@ -10,6 +10,8 @@ namespace q4 {
 
 // Attention's kernels treat 64 positions as one tile.
 constexpr int kTileKeys = 64;
+// Counters at the start of an attention workspace.
+constexpr int kAttnCounters = 512;
 
 struct KvCache {
     uint16_t* k;        // [pages][kv_heads][page][dim]
@@ -77,6 +79,21 @@ int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_
 __device__ __forceinline__ int page_of(const KvCache& c, const int* __restrict__ row, int pos) {
     const int id = row[pos >> c.shift];
     return (unsigned)id < (unsigned)c.pages ? id : -1;
+}
+
+// Inclusive prefix sum over the wave's 64 lanes, and its last value.
+struct LaneScan {
+    int upto;
+    int last;
+};
+__device__ __forceinline__ LaneScan lane_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 of a row to the next row, rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+    return {v, __builtin_amdgcn_readlane(v, 63)};
 }
 
 }  // namespace q4

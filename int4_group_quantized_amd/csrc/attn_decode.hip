@@ -17,11 +17,19 @@
 // subtile t's row r loads key 32 (t/2) + 8 (r/4) + 4 (t%2) + r%4.  A query row's
 // maximum and sum cross lanes twice per tile (lanes xor 16 and xor 32).
 //
+// Schedule: a wave has one tile's values and the next tile's keys on their way
+// while it computes (32 KB per wave, two waves per SIMD up to dim 128).  With
+// keys and values requested only when needed 64 sequences of 16,384 positions
+// (2.15 GB) took 499 us, with this 357 us (6.0 TB/s); its read-only twin, the
+// same loads without the arithmetic, takes 358 us.
+//
 // Split: the visible tiles of all sequences are cut into parts of one length,
 // computed on the device from the lengths so that uneven batches stay
-// balanced: every workgroup gets one part of one sequence and kv head (4 waves
-// take its tiles in turn), parts of a sequence are joined in order by a second
-// launch.  A sequence of one part is written directly.
+// balanced: every workgroup gets one part of one sequence and kv head, its four
+// waves take its tiles in turn.  512 parts (two workgroups per CU) measured
+// best: 256 ran 1.3 times as long, 768 and 1,024 2% longer on that case and 20%
+// on 16 uneven sequences.  The last part of a sequence to finish joins them in
+// order; a second launch for that cost 2 to 3 us more.
 #include "attn_softmax.hpp"
 
 namespace q4 {
@@ -29,6 +37,8 @@ namespace q4 {
 constexpr int kDecodeWaves = 4;
 constexpr int kDecodeThreads = 64 * kDecodeWaves;
 constexpr int kDecodeSlots = 512;   // workgroups wanted per launch: two per CU
+static_assert(kDecodeSlots <= kAttnCounters, "a counter for each sequence of several parts");
+constexpr int kJoin = 16;           // parts joined per round (a power of two)
 constexpr int kDecodeMinTiles = 4;  // tiles per part at least: one per wave
 
 // First visible tile and the number of tiles of sequence b.
@@ -43,31 +53,41 @@ struct DecodePart {
     int part;     // of the sequence
     int parts;    // parts of the sequence
     int slot;     // workspace slot of the sequence's first part
+    int split;    // sequences of several parts before this one
     int chunk;    // tiles per part
 };
 
-// Tiles per part; each wave computes it for itself.  target: parts wanted per
-// kv head and row block.
-__device__ __forceinline__ int decode_chunk(const AttnArgs& a, int target) {
-    const int lane = threadIdx.x & 63;
-    long total = 0;
-    for (int b0 = 0; b0 < a.rows; b0 += 64) {
-        int first, len;
-        int n = b0 + lane < a.rows ? decode_tiles(a, b0 + lane, first, len) : 0;
-        for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d, 64);
-        total += n;
-    }
-    const long want = (total + target - 1) / target;
-    return (int)(want > kDecodeMinTiles ? want : kDecodeMinTiles);
+// Tiles per part: the total over `target`, the parts wanted per kv head and row
+// block, rounded up, so that there are at most target + rows parts.
+__device__ __forceinline__ int decode_chunk(int64_t total, int target) {
+    int c = (int)((float)total / (float)target);  // within one of the quotient, up to 2^22 tiles per part
+    c = max(c - 1, kDecodeMinTiles);
+    while ((int64_t)c * target < total) ++c;
+    return c;
 }
 
-// The part with number `item`; parts are numbered sequence by sequence.
+// The part with number `item`; parts are numbered sequence by sequence.  Each
+// wave computes it for itself.
 __device__ __forceinline__ DecodePart decode_part(const AttnArgs& a, int item, int target) {
     const int lane = threadIdx.x & 63;
     DecodePart r;
-    r.chunk = decode_chunk(a, target);
     r.b = -1;
-    r.part = r.parts = r.slot = 0;
+    r.part = r.parts = r.slot = r.split = 0;
+    if (a.rows == 1) {
+        int first, len;
+        const int n = decode_tiles(a, 0, first, len);
+        r.chunk = decode_chunk(n, target);
+        r.parts = n > r.chunk ? (n + r.chunk - 1) / r.chunk : 1;
+        r.part = item;
+        if (item < r.parts) r.b = 0;
+        return r;
+    }
+    int64_t total = 0;
+    for (int b0 = 0; b0 < a.rows; b0 += 64) {
+        int first, len;
+        total += lane_scan(b0 + lane < a.rows ? decode_tiles(a, b0 + lane, first, len) : 0).last;
+    }
+    r.chunk = decode_chunk(total, target);
     int before = 0;  // parts of earlier sequences
     for (int b0 = 0; b0 < a.rows; b0 += 64) {
         int first, len, n = 0;
@@ -75,21 +95,19 @@ __device__ __forceinline__ DecodePart decode_part(const AttnArgs& a, int item, i
             n = (decode_tiles(a, b0 + lane, first, len) + r.chunk - 1) / r.chunk;
             n = n > 0 ? n : 1;  // an empty sequence has a part that writes zeros
         }
-        int upto = n;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(upto, d, 64);
-            if (lane >= d) upto += o;
-        }
-        const uint64_t hit = __ballot(n > 0 && item < before + upto && item >= before + upto - n);
+        const LaneScan s = lane_scan(n);
+        const uint64_t hit = __ballot(n > 0 && item < before + s.upto && item >= before + s.upto - n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
             r.b = b0 + l;
             r.parts = __builtin_amdgcn_readlane(n, l);
-            r.slot = before + __builtin_amdgcn_readlane(upto, l) - r.parts;
+            r.slot = before + __builtin_amdgcn_readlane(s.upto, l) - r.parts;
             r.part = item - r.slot;
+            r.split += __builtin_popcountll(__ballot(n > 1 && lane < l));
             return r;
         }
-        before += __builtin_amdgcn_readlane(upto, 63);
+        r.split += __builtin_popcountll(__ballot(n > 1));
+        before += s.last;
     }
     return r;
 }
@@ -99,20 +117,52 @@ __host__ __device__ inline int decode_target(int pairs) {
     return t > 0 ? t : 1;
 }
 
+// Counters of finished parts, then partial outputs [parts][heads][dim], their
+// maxima and sums [parts][heads][2].  A sequence of several parts has more than
+// total / target tiles, so there are fewer than `target` of them, and target
+// times the kv heads and row blocks is at most kDecodeSlots: the counters have
+// one place whatever the shape, so calls of all shapes can share a workspace.
+struct DecodeWorkspace {
+    float* o;
+    float* ml;
+    int* counters;
+};
+
+__device__ __forceinline__ DecodeWorkspace decode_workspace(const AttnArgs& a, int dim, int target) {
+    const long slots = (long)(target + a.rows) * a.heads;
+    DecodeWorkspace w;
+    w.counters = reinterpret_cast<int*>(a.workspace);
+    w.o = a.workspace + kAttnCounters;
+    w.ml = w.o + slots * dim;
+    return w;
+}
+
+// Four dimensions of an output row: o / sum in fp16, zeros where nothing was seen.
+__device__ __forceinline__ void store_row(uint16_t* p, f4 o, float sum) {
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    uint2 w;
+    w.x = as_u32((h2){(_Float16)(o[0] * inv), (_Float16)(o[1] * inv)});
+    w.y = as_u32((h2){(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)});
+    *reinterpret_cast<uint2*>(p) = w;
+}
+
 __device__ __forceinline__ h8 load_h8(const uint16_t* p) {
     return __builtin_bit_cast(h8, *reinterpret_cast<const u4*>(p));
 }
 
 template <int D, bool EXTRA>
-__global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(AttnArgs a, int target) {
+__global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_kernel(AttnArgs a, int target) {
     constexpr int OP = D + 4;  // pitch of a row of partial outputs in LDS
     __shared__ float part_o[kDecodeWaves][16][OP];
     __shared__ float part_m[kDecodeWaves][16], part_l[kDecodeWaves][16];
+    // Kv heads and row blocks first, so that neighbouring workgroups read
+    // neighbouring parts of the same pages at the same time.
     const int row_blocks = (a.group + 15) / 16;
-    const int kvh = blockIdx.y / row_blocks;
-    const int row0 = (blockIdx.y % row_blocks) * 16;   // first head of the group in this workgroup
+    const int pairs = a.c.kv_heads * row_blocks, pair = blockIdx.x % pairs;
+    const int kvh = row_blocks == 1 ? pair : pair / row_blocks;
+    const int row0 = (pair - kvh * row_blocks) * 16;   // first head of the group in this workgroup
     const int nrows = min(16, a.group - row0);
-    const DecodePart it = decode_part(a, blockIdx.x, target);
+    const DecodePart it = decode_part(a, blockIdx.x / pairs, target);
     if (it.b < 0) return;
     int first, len;
     const int tiles = decode_tiles(a, it.b, first, len);
@@ -142,30 +192,64 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(AttnArgs a,
     for (int i = 0; i < D / 16; ++i) acc[i] = (f4){0, 0, 0, 0};
     float m = Q4_NEG_INF, l = 0.0f;
 
-    for (int t = t_begin + wave; t < t_end; t += kDecodeWaves) {
+    // Operands of one tile: K as A of the first product, V as A of the second.
+    u4 kr[4][D / 32], vr[D / 16][2];
+    // Pages of the 8-key groups that this lane's values and scores belong to
+    // (vp) and that its keys belong to (kp), per 32-key block.  Positions past
+    // the end take the last one's page.
+    struct Ids {
+        int v[2], k[2];
+    };
+    auto ids = [&](int t) {
+        Ids r;
         const int kb = t * kTileKeys;
-        // Pages of the two 8-key groups this lane's values and scores belong to,
-        // and of its keys' groups.  Positions past the end read the last one's page.
-        int vp[2], kp[2];
-        bool whole = kb >= start && kb + kTileKeys <= len;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            vp[h] = page_of(a.c, row, min(kb + 32 * h + 8 * g, len - 1));
-            kp[h] = page_of(a.c, row, min(kb + 32 * h + 8 * (n >> 2), len - 1));
-            whole = whole && vp[h] >= 0;
+            r.v[h] = page_of(a.c, row, min(kb + 32 * h + 8 * g, len - 1));
+            r.k[h] = page_of(a.c, row, min(kb + 32 * h + 8 * (n >> 2), len - 1));
         }
-        whole = __all(whole);
+        return r;
+    };
+    auto load_k = [&](int t, const Ids& id) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int key = t * kTileKeys + 32 * (u >> 1) + 8 * (n >> 2) + 4 * (u & 1) + (n & 3);
+            const uint16_t* p = a.c.k + (size_t)max(id.k[u >> 1], 0) * a.c.k_stride +
+                                ((size_t)kvh * P + (key & pmask)) * D + 8 * g;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) kr[u][d] = *reinterpret_cast<const u4*>(p + 32 * d);
+        }
+    };
+    auto load_v = [&](int t, const Ids& id) {
+        // Both halves of a 128-byte line (a page of 64) are requested back to back.
+        const uint16_t* p[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            p[h] = a.c.v + (size_t)max(id.v[h], 0) * a.c.v_stride + ((size_t)(kvh * D + n) << a.c.shift) +
+                   ((t * kTileKeys + 32 * h + 8 * g) & pmask);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vr[d][h] = *reinterpret_cast<const u4*>(p[h] + ((size_t)(16 * d) << a.c.shift));
+        }
+    };
+    // One tile; K is in kr.  `next` requests the next tile's K as soon as kr is
+    // free, so that it travels during the softmax and the second product.
+    auto tile = [&](int t, const Ids& id, auto next) {
+        const int kb = t * kTileKeys;
+        load_v(t, id);
+        __builtin_amdgcn_sched_barrier(0);
         f4 s[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int key = kb + 32 * (u >> 1) + 8 * (n >> 2) + 4 * (u & 1) + (n & 3);
-            const int page = max(kp[u >> 1], 0);
-            const uint16_t* p = a.c.k + (size_t)page * a.c.k_stride + ((size_t)kvh * P + (key & pmask)) * D + 8 * g;
             s[u] = (f4){0, 0, 0, 0};
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
-                s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(load_h8(p + 32 * d), qf[d], s[u], 0, 0, 0);
+                s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, kr[u][d]), qf[d], s[u], 0, 0, 0);
         }
+        next();
+        __builtin_amdgcn_sched_barrier(0);
+        const bool whole = __all(kb >= start && kb + kTileKeys <= len && id.v[0] >= 0 && id.v[1] >= 0);
         // Scores; masked ones are -inf.
         float top = Q4_NEG_INF;
 #pragma unroll
@@ -174,7 +258,7 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(AttnArgs a,
             for (int i = 0; i < 4; ++i) {
                 const int key = kb + 32 * (u >> 1) + 8 * g + 4 * (u & 1) + i;
                 float x = score<EXTRA>(s[u][i], sp, key - (len - 1));
-                if (!whole) x = key >= start && key < len && vp[u >> 1] >= 0 ? x : Q4_NEG_INF;
+                if (!whole) x = key >= start && key < len && id.v[u >> 1] >= 0 ? x : Q4_NEG_INF;
                 s[u][i] = x;
                 top = fmaxf(top, x);
             }
@@ -197,29 +281,41 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(AttnArgs a,
         }
         l = l * f + sum;
         m = m_new;
+        if (!whole) {
+            // A masked position has weight zero, but zero times what an unwritten
+            // slot holds may be NaN: such values are cleared.
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k0 = kb + 32 * h + 8 * g;
+                const int from = id.v[h] < 0 ? 8 : start - k0, to = len - k0;
+                uint32_t keep[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    keep[e] = (2 * e >= from && 2 * e < to ? 0x0000FFFFu : 0u) |
+                              (2 * e + 1 >= from && 2 * e + 1 < to ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) vr[d][h] &= (u4){keep[0], keep[1], keep[2], keep[3]};
+            }
+        }
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
             acc[d] *= f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = kb + 32 * h + 8 * g;
-                const uint16_t* p = a.c.v + (size_t)max(vp[h], 0) * a.c.v_stride +
-                                    ((size_t)(kvh * D + 16 * d + n) << a.c.shift) + (key & pmask);
-                u4 v = *reinterpret_cast<const u4*>(p);
-                if (!whole) {
-                    // A masked position has weight zero, but zero times what an
-                    // unwritten slot holds may be NaN: such values are cleared.
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const bool seen = key + e >= start && key + e < len && vp[h] >= 0;
-                        if (!seen) w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                    }
-                    v = (u4){w[0], w[1], w[2], w[3]};
-                }
-                acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, v), pf[h], acc[d], 0, 0, 0);
-            }
+            for (int h = 0; h < 2; ++h)
+                acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, vr[d][h]), pf[h], acc[d], 0, 0, 0);
         }
+    };
+
+    int t = t_begin + wave;
+    if (t < t_end) {
+        Ids id = ids(t);
+        load_k(t, id);
+        for (; t + kDecodeWaves < t_end; t += kDecodeWaves) {
+            const Ids after = ids(t + kDecodeWaves);
+            tile(t, id, [&] { load_k(t + kDecodeWaves, after); });
+            id = after;
+        }
+        tile(t, id, [] {});
     }
     l += lane_swap16(l);
     l += __shfl_xor(l, 32, 64);
@@ -235,8 +331,7 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(AttnArgs a,
     }
     __syncthreads();
     const long slot = (long)it.slot + it.part;
-    float* ws_o = a.workspace;
-    float* ws_ml = a.workspace + (long)(target + a.rows) * a.heads * D;
+    const DecodeWorkspace ws = decode_workspace(a, D, target);
     for (int i = threadIdx.x; i < nrows * (D / 4); i += kDecodeThreads) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float top = part_m[0][r];
@@ -251,80 +346,78 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(AttnArgs a,
             o += *reinterpret_cast<const f4*>(&part_o[w][r][d]) * f;
         }
         if (it.parts == 1) {
-            const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-            uint2 w;
-            w.x = as_u32((h2){(_Float16)(o[0] * inv), (_Float16)(o[1] * inv)});
-            w.y = as_u32((h2){(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)});
-            *reinterpret_cast<uint2*>(a.out + ((size_t)it.b * a.heads + head0 + r) * D + d) = w;
+            store_row(a.out + ((size_t)it.b * a.heads + head0 + r) * D + d, o, sum);
         } else {
-            *reinterpret_cast<f4*>(ws_o + (slot * a.heads + head0 + r) * D + d) = o;
-            if (d == 0) {
-                ws_ml[(slot * a.heads + head0 + r) * 2] = top;
-                ws_ml[(slot * a.heads + head0 + r) * 2 + 1] = sum;
+            float* wo = ws.o + (slot * a.heads + head0 + r) * D + d;
+            share_store(wo, o[0], o[1]);
+            share_store(wo + 2, o[2], o[3]);
+            if (d == 0) share_store(ws.ml + (slot * a.heads + head0 + r) * 2, top, sum);
+        }
+    }
+    if (it.parts == 1) return;
+
+    // The last workgroup of a sequence and row block to finish joins its parts,
+    // in order, whichever it is.  It leaves the counter at zero for the next call.
+    if (!parts_done(ws.counters + it.split * pairs + pair, it.parts)) return;
+    for (int r = wave; r < nrows; r += kDecodeWaves) {
+        const float* ml = ws.ml + ((long)it.slot * a.heads + head0 + r) * 2;
+        const float* po = ws.o + ((long)it.slot * a.heads + head0 + r) * D;
+        // Rounds of up to kJoin parts: their outputs, maxima and sums are requested
+        // together, lane p holding part p's statistics.
+        constexpr int PER = (D + 127) / 128;  // pairs of dimensions per lane
+        float2 o[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) o[i] = {0.0f, 0.0f};
+        float top = Q4_NEG_INF, sum = 0.0f;
+        for (int p0 = 0; p0 < it.parts; p0 += kJoin) {
+            float2 v[kJoin][PER];
+            float2 st = {Q4_NEG_INF, 0.0f};
+            if (lane < kJoin && p0 + lane < it.parts) st = share_load(ml + (long)(p0 + lane) * a.heads * 2);
+#pragma unroll
+            for (int p = 0; p < kJoin; ++p) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int d = 2 * (lane + 64 * i);
+                    v[p][i] = {0.0f, 0.0f};
+                    if (p0 + p < it.parts && d < D) v[p][i] = share_load(po + (long)(p0 + p) * a.heads * D + d);
+                }
+            }
+            float t = st.x;
+#pragma unroll
+            for (int d = kJoin / 2; d >= 1; d >>= 1) t = fmaxf(t, __shfl_xor(t, d, 64));
+            t = fmaxf(top, __shfl(t, 0, 64));
+            const float f0 = part_weight(top, t), w = part_weight(st.x, t);
+            float s1 = st.y * w;
+#pragma unroll
+            for (int d = kJoin / 2; d >= 1; d >>= 1) s1 += __shfl_xor(s1, d, 64);
+            sum = sum * f0 + __shfl(s1, 0, 64);
+            top = t;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) o[i] = {o[i].x * f0, o[i].y * f0};
+#pragma unroll
+            for (int p = 0; p < kJoin; ++p) {
+                const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), p));
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    o[i].x += v[p][i].x * f;
+                    o[i].y += v[p][i].y * f;
+                }
             }
         }
-    }
-}
-
-// Join of the parts of one sequence and head: one workgroup, each wave sums
-// every fourth part, the waves are summed in order.
-template <int D>
-__global__ void __launch_bounds__(kDecodeThreads) attn_decode_join_kernel(AttnArgs a, int target) {
-    __shared__ float acc[kDecodeWaves][D];
-    __shared__ float sums[kDecodeWaves];
-    const int b = blockIdx.x, head = blockIdx.y;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    // The sequence's parts; those of earlier sequences have the lower numbers.
-    const int chunk = decode_chunk(a, target);
-    int slot = 0, parts = 1;
-    for (int b0 = 0; b0 <= b; b0 += 64) {
-        int first, len, n = 0;
-        if (b0 + lane <= b) {
-            n = (decode_tiles(a, b0 + lane, first, len) + chunk - 1) / chunk;
-            n = n > 0 ? n : 1;
-        }
-        if (b0 + 64 > b) parts = __shfl(n, b - b0, 64);
-        for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d, 64);
-        slot += n;
-    }
-    slot -= parts;
-    if (parts == 1) return;
-    const float* ws_o = a.workspace;
-    const float* ws_ml = a.workspace + (long)(target + a.rows) * a.heads * D;
-    float top = Q4_NEG_INF;
-    for (int p = lane; p < parts; p += 64) top = fmaxf(top, ws_ml[((long)(slot + p) * a.heads + head) * 2]);
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    constexpr int PER = (D + 63) / 64;
-    float o[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = 0.0f;
-    float sum = 0.0f;
-    for (int p = wave; p < parts; p += kDecodeWaves) {
-        const long at = (long)(slot + p) * a.heads + head;
-        const float f = part_weight(ws_ml[at * 2], top);
-        sum += ws_ml[at * 2 + 1] * f;
+        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+        uint16_t* op = a.out + ((size_t)it.b * a.heads + head0 + r) * D;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int d = lane + 64 * i;
-            if (d < D) o[i] += ws_o[at * D + d] * f;
+            const int d = 2 * (lane + 64 * i);
+            if (d < D)
+                *reinterpret_cast<uint32_t*>(op + d) = as_u32((h2){(_Float16)(o[i].x * inv), (_Float16)(o[i].y * inv)});
         }
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (lane + 64 * i < D) acc[wave][lane + 64 * i] = o[i];
-    if (lane == 0) sums[wave] = sum;
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kDecodeThreads) {
-        const float all = sums[0] + sums[1] + sums[2] + sums[3];
-        const float inv = all > 0.0f || all != all ? 1.0f / all : 0.0f;
-        const float v = (acc[0][d] + acc[1][d] + acc[2][d] + acc[3][d]) * inv;
-        a.out[((size_t)b * a.heads + head) * D + d] = __builtin_bit_cast(uint16_t, (_Float16)v);
     }
 }
 
 int64_t attn_decode_workspace(int64_t batch, int heads, int dim) {
     // Parts: at most the wanted number and one more per sequence.
-    return ((int64_t)kDecodeSlots + batch) * heads * (dim + 2) * (int64_t)sizeof(float);
+    return (((int64_t)kDecodeSlots + batch) * heads * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
 
 template <int D>
@@ -335,15 +428,11 @@ static hipError_t launch_decode(const AttnArgs& a, hipStream_t st) {
     const long grid = (long)target + a.rows < most * a.rows ? (long)target + a.rows : most * a.rows;
     const bool extra = a.softcap > 0.0f || a.slopes;
     if (extra)
-        hipLaunchKernelGGL((attn_decode_kernel<D, true>), dim3((unsigned)grid, pairs), dim3(kDecodeThreads), 0, st, a,
+        hipLaunchKernelGGL((attn_decode_kernel<D, true>), dim3((unsigned)(grid * pairs)), dim3(kDecodeThreads), 0, st, a,
                            target);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<D, false>), dim3((unsigned)grid, pairs), dim3(kDecodeThreads), 0, st, a,
+        hipLaunchKernelGGL((attn_decode_kernel<D, false>), dim3((unsigned)(grid * pairs)), dim3(kDecodeThreads), 0, st, a,
                            target);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || most == 1) return e;
-    hipLaunchKernelGGL((attn_decode_join_kernel<D>), dim3((unsigned)a.rows, a.heads), dim3(kDecodeThreads), 0, st, a,
-                       target);
     return hipGetLastError();
 }
 

@@ -55,7 +55,8 @@ static int prefill_splits(long tokens, long count, int group, int kv_heads, long
 
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length) {
     const int splits = prefill_splits(tokens, count, heads / kv_heads, kv_heads, max_length);
-    return splits == 1 ? 0 : (int64_t)splits * tokens * heads * (dim + 2) * (int64_t)sizeof(float);
+    // The counters of the decode call come first, so that both can share one.
+    return splits == 1 ? 0 : ((int64_t)splits * tokens * heads * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
 
 struct PrefillTile {
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
         }
     } else {
         const long at = ((long)split * a.rows + token) * a.heads + head;
-        float* op = a.workspace + at * D;
+        float* op = a.workspace + kAttnCounters + at * D;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) {
 #pragma unroll
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                     (f4){acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
         }
         if (h == 0) {
-            float* ml = a.workspace + (long)splits * a.rows * a.heads * D + at * 2;
+            float* ml = a.workspace + kAttnCounters + (long)splits * a.rows * a.heads * D + at * 2;
             ml[0] = m;
             ml[1] = l;
         }
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
     // Tokens outside every sequence have no parts.
     const int token = (int)(r / a.heads);
     if (token < a.q_starts[0] || token >= a.q_starts[a.count]) return;
-    const float* ml = a.workspace + (long)splits * rows * D;
+    const float* part = a.workspace + kAttnCounters;
+    const float* ml = part + (long)splits * rows * D;
     float top = Q4_NEG_INF;
     for (int s = lane; s < splits; s += 64) top = fmaxf(top, ml[(s * rows + r) * 2]);
     for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
         sum += ml[(s * rows + r) * 2 + 1] * f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (lane + 64 * i < D) o[i] += a.workspace[(s * rows + r) * D + lane + 64 * i] * f;
+            if (lane + 64 * i < D) o[i] += part[(s * rows + r) * D + lane + 64 * i] * f;
     }
     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
 #pragma unroll

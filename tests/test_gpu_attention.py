@@ -333,6 +333,25 @@ def test_decode_masked_positions_stay_out(dev, junk):
     check_attention(out, q, pool, range(3), lengths, 0.2, f"junk {junk}", window=window)
 
 
+def test_decode_shapes_share_a_workspace(dev):
+    """Calls of different shapes on one workspace, with prompt calls between them, leave its counters at zero."""
+    rng = np.random.default_rng(15)
+    cases = [([3000, 5], 4, 1, 64), ([700] * 9, 12, 3, 128), ([9000], 40, 1, 64), ([1, 0], 2, 2, 256)]
+    need = max(max(q4.q4g128_attn_decode_workspace(len(n), h, d),
+                   q4.q4g128_attn_prefill_workspace(len(n), len(n), h, kv, d, max(n))) for n, h, kv, d in cases)
+    ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+    ws[q4.ATTN_COUNTER_BYTES:] = 0xFF
+    for lengths, heads, kv, dim in cases + cases[::-1]:
+        pool = Pool(rng, lengths, kv, 64, dim)
+        c = pool.on(dev)
+        q = rng.standard_normal((len(lengths), heads, dim)).astype(np.float16)
+        qd, n, starts = torch.from_numpy(q).to(dev), i32(lengths, dev), i32(range(len(lengths) + 1), dev)
+        for out in (q4.q4g128_attn_decode(qd, *c, n, scale=0.1, max_length=max(lengths), workspace=ws),
+                    q4.q4g128_attn_prefill(qd, *c, starts, n, scale=0.1, max_length=max(lengths), workspace=ws)):
+            check_attention(out, q, pool, range(len(lengths) + 1), lengths, 0.1, f"shared workspace {lengths}")
+        assert not ws[:q4.ATTN_COUNTER_BYTES].any()
+
+
 def test_decode_repeats_bit_for_bit_and_on_another_stream(dev):
     rng = np.random.default_rng(14)
     lengths = [5000, 17, 1200]
@@ -481,7 +500,7 @@ def test_step_in_a_graph(dev):
     starts = i32([0, 1, 2, 3], dev)
     q = torch.empty((b, heads, dim), dtype=torch.float16, device=dev)
     out, out2 = torch.empty_like(q), torch.empty_like(q)
-    ws = torch.empty(q4.q4g128_attn_decode_workspace(b, heads, dim), dtype=torch.uint8, device=dev)
+    ws = torch.zeros(q4.q4g128_attn_decode_workspace(b, heads, dim), dtype=torch.uint8, device=dev)
     ws2 = torch.empty(q4.q4g128_attn_prefill_workspace(b, 3, heads, kv, dim, 900), dtype=torch.uint8, device=dev)
 
     def step():
