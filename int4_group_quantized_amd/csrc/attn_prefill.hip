@@ -20,7 +20,7 @@
 //
 // LDS rows are swizzled in 16-byte chunks (chunk ^ a function of the row) so
 // that the 32 rows of an operand load fall on different banks.  The next tile
-// is on its way from memory in registers while this one is computed.
+// goes straight from memory into a second LDS image while this one is computed.
 //
 // Few tokens on a long cache leave most CUs idle, so the visible tiles are
 // then cut into equal splits joined by a second launch.
@@ -105,14 +105,18 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
     return r;
 }
 
-// Chunk of 16 bytes (eight halves) c of K row `key`, and of V row `dim`, in LDS.
+// Chunk of 16 bytes (eight halves) c of K row `key`, and of V row `dim`, in a
+// tile's LDS image: K [64][D / 8], V [D][8] behind it.
 template <int D>
 __device__ __forceinline__ int k_chunk(int key, int c) {
     constexpr int MASK = D % 64 == 0 ? 7 : 3;  // dim 96 has 12 chunks, which only two bits permute
     const int f = (key & 3) | ((key >> 1) & 4);
     return key * (D / 8) + (c ^ (f & MASK));
 }
-__device__ __forceinline__ int v_chunk(int dim, int c) { return dim * (kTileKeys / 8) + (c ^ (dim & 7)); }
+template <int D>
+__device__ __forceinline__ int v_chunk(int dim, int c) {
+    return kTileKeys * (D / 8) + dim * (kTileKeys / 8) + (c ^ (dim & 7));
+}
 
 __device__ __forceinline__ h8 as_h8(u4 v) { return __builtin_bit_cast(h8, v); }
 
@@ -121,45 +125,46 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
     return (((w & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
 }
 
-// Eight halves split into their finite values (others zero) and two sets of
-// zeros and ones: +inf or NaN, and -inf or NaN.
-struct OddSplit {
-    h8 fine, up, down;
-};
-__device__ __forceinline__ OddSplit split_odd(u4 v) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w}, up[4], down[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t odd = odd_halves(w[i]);
-        const uint32_t nan = (((w[i] & 0x03FF03FFu) + 0x03FF03FFu) >> 10) & odd;
-        const uint32_t neg = (w[i] >> 15) & odd;
-        up[i] = (nan | (odd & ~neg)) * 0x3C00u;  // fp16 1.0
-        down[i] = (nan | neg) * 0x3C00u;
-        w[i] &= ~(odd * 0xFFFFu);
-    }
-    return {as_h8((u4){w[0], w[1], w[2], w[3]}), as_h8((u4){up[0], up[1], up[2], up[3]}),
-            as_h8((u4){down[0], down[1], down[2], down[3]})};
+// Eight halves with infinities and NaN set to zero.
+__device__ __forceinline__ u4 finite_halves(u4 v) {
+    return (u4){v.x & ~(odd_halves(v.x) * 0xFFFFu), v.y & ~(odd_halves(v.y) * 0xFFFFu),
+                v.z & ~(odd_halves(v.z) * 0xFFFFu), v.w & ~(odd_halves(v.w) * 0xFFFFu)};
+}
+
+// 16 bytes per lane from memory into LDS: lane i's to base + 16 i.
+__device__ __forceinline__ void load_lds(const uint16_t* p, u4* base) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)p,
+                                     (__attribute__((address_space(3))) uint32_t*)base, 16, 0, 0);
+}
+
+__device__ __forceinline__ void images_ready() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);  // the loads into LDS count as vector memory operations
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
 template <int D, bool EXTRA>
 __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefill_kernel(AttnArgs a, int tile0, int splits) {
     constexpr int C = D / 8;             // 16-byte chunks of a K row
     constexpr int STAGE = D / 32;        // chunks per thread and tile, for K and for V
-    __shared__ u4 k_lds[kTileKeys * C];
-    __shared__ u4 v_lds[D * (kTileKeys / 8)];
+    constexpr int IMAGE = 2 * kTileKeys * C;  // chunks of a tile's image
+    // Two images as two arrays: the compiler then knows that reads of one do not
+    // wait for the loads under way into the other.
+    __shared__ u4 image0[IMAGE], image1[IMAGE];
     const int kvh = blockIdx.x % a.c.kv_heads;
     const int rest = blockIdx.x / a.c.kv_heads;
-    const int split = rest % splits;
-    const PrefillTile it = prefill_tile(a, tile0 + rest / splits);
+    const int split = splits == 1 ? 0 : rest % splits;
+    const PrefillTile it = prefill_tile(a, tile0 + (splits == 1 ? rest : rest / splits));
     if (it.s < 0) return;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
 
     // This lane's query row and the positions it sees: lo <= j < hi.
     const int r = wave * 32 + n;
     const int tok = r / a.group;
     const bool live = tok < it.n;
-    const int head = kvh * a.group + (live ? r % a.group : 0);
+    const int head = kvh * a.group + (live ? r - tok * a.group : 0);
     const int token = it.token + (live ? tok : 0);
     const int qpos = it.pos + tok;
     const int prefix = a.prefix ? a.prefix[it.s] : 0;
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     const int wg_lo = a.window > 0 ? max(it.pos + 1 - a.window, 0) : 0;
     const int first_tile = wg_lo / kTileKeys;
     const int tiles = max((wg_hi + kTileKeys - 1) / kTileKeys - first_tile, 0);
-    const int per = (tiles + splits - 1) / splits;
+    const int per = splits == 1 ? tiles : (tiles + splits - 1) / splits;
     const int t_begin = first_tile + split * per;
     const int t_end = min(t_begin + per, first_tile + tiles);
 
@@ -203,26 +208,47 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     const int pmask = (1 << a.c.shift) - 1;
     const int* row = a.c.table + (size_t)it.s * a.c.cols;
 
-    u4 sk[STAGE], sv[STAGE];
-    int pages[4];  // of the tile's quarters
-    auto load = [&](int t) {
-        const int kb = t * kTileKeys;
+    // Pages of a tile's four quarters (16 positions each); positions past the end
+    // take the last one's.  Uniform over the workgroup.
+    struct Pages {
+        int p[4];
+        __device__ int gone() const {  // bit i: quarter i has no page
+            return (p[0] < 0 ? 1 : 0) | (p[1] < 0 ? 2 : 0) | (p[2] < 0 ? 4 : 0) | (p[3] < 0 ? 8 : 0);
+        }
+    };
+    auto pages_of = [&](int t) {
+        Pages r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pages[i] = page_of(a.c, row, min(kb + 16 * i, it.len - 1));
-        auto page = [&](int quarter) {
-            const int p = quarter < 2 ? (quarter == 0 ? pages[0] : pages[1]) : (quarter == 2 ? pages[2] : pages[3]);
-            return (size_t)max(p, 0);
-        };
+        for (int i = 0; i < 4; ++i)
+            r.p[i] = __builtin_amdgcn_readfirstlane(page_of(a.c, row, min(t * kTileKeys + 16 * i, it.len - 1)));
+        return r;
+    };
+    // A tile straight into an image, 16 bytes per lane: LDS takes a wave's lanes
+    // in order, so each lane fetches the chunk that the swizzle puts at its place.
+    auto load = [&](int t, const Pages& pg, u4* im) {
+        const int kb = t * kTileKeys;
+        const uint16_t *kp[4], *vp[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t p = (size_t)max(pg.p[i], 0);
+            const int off = (kb + 16 * i) & pmask;
+            kp[i] = a.c.k + p * a.c.k_stride + (((size_t)kvh << a.c.shift) + off) * D;
+            vp[i] = a.c.v + p * a.c.v_stride + ((size_t)(kvh * D) << a.c.shift) + off;
+        }
 #pragma unroll
         for (int j = 0; j < STAGE; ++j) {
-            const int idx = tid + kPrefillThreads * j;
-            const int key = idx / C, c = idx % C;
-            sk[j] = *reinterpret_cast<const u4*>(a.c.k + page(key >> 4) * a.c.k_stride +
-                                                 (((size_t)kvh << a.c.shift) + ((kb + key) & pmask)) * D + 8 * c);
-            const int dim = idx >> 3, vc = idx & 7;
-            sv[j] = *reinterpret_cast<const u4*>(a.c.v + page(vc >> 1) * a.c.v_stride +
-                                                 ((size_t)(kvh * D + dim) << a.c.shift) + ((kb + 8 * vc) & pmask));
+            const int x = kPrefillThreads * j + tid;
+            const int key = x / C, c = k_chunk<D>(key, x % C) - key * C, quarter = key >> 4;
+            const uint16_t* k0 = quarter < 2 ? (quarter == 0 ? kp[0] : kp[1]) : (quarter == 2 ? kp[2] : kp[3]);
+            load_lds(k0 + (unsigned)((key & 15) * D + 8 * c), im + kPrefillThreads * j + 64 * wave);
         }
+        // x = 256 j + tid: dimension 32 j + tid / 8, whose swizzle is the same for all j
+        const int vc = (tid & 7) ^ ((tid >> 3) & 7);
+        const uint16_t* v0 = (vc < 4 ? (vc < 2 ? vp[0] : vp[1]) : (vc < 6 ? vp[2] : vp[3])) + 8 * (vc & 1);
+#pragma unroll
+        for (int j = 0; j < STAGE; ++j)
+            load_lds(v0 + ((unsigned)(32 * j + (tid >> 3)) << a.c.shift),
+                     im + kTileKeys * C + kPrefillThreads * j + 64 * wave);
     };
 
     f16v acc[D / 32];
@@ -231,128 +257,152 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     float m = Q4_NEG_INF, l = 0.0f;
     const int km = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);  // key of this lane's K row
 
-    if (t_begin < t_end) load(t_begin);
-    for (int t = t_begin; t < t_end; ++t) {
+    // One tile from image `im`, while the next one goes to `other`.
+    Pages pg = {};
+    int gone = 0;
+    auto tile = [&](int t, u4* im, u4* other) {
         const int kb = t * kTileKeys;
-        const bool absent = (pages[0] | pages[1] | pages[2] | pages[3]) < 0;  // of this tile
-        const bool gone[4] = {pages[0] < 0, pages[1] < 0, pages[2] < 0, pages[3] < 0};
-        if (t > t_begin) __syncthreads();  // the last tile's reads are done
-        if (absent || kb + kTileKeys > it.len) {
+        // This wave's loads and LDS reads are done; after the barrier everyone's:
+        // the image is complete, and the other one is free.
+        images_ready();
+        const int gone_next = t + 1 < t_end ? pg.gone() : 0;
+        if (t + 1 < t_end) {
+            load(t + 1, pg, other);
+            if (t + 2 < t_end) pg = pages_of(t + 2);
+        }
+        if (gone || kb + kTileKeys > it.len) {
             // Values past the end and of absent pages are cleared: their weight is
             // zero, but zero times what an unwritten slot holds may be NaN.
-#pragma unroll
-            for (int j = 0; j < STAGE; ++j) {
-                const int vc = (tid + kPrefillThreads * j) & 7;
-                const bool dead = vc < 4 ? (vc < 2 ? gone[0] : gone[1]) : (vc < 6 ? gone[2] : gone[3]);
-                const int keep = dead ? 0 : min(max(it.len - (kb + 8 * vc), 0), 8);
-                uint32_t w[4] = {sv[j].x, sv[j].y, sv[j].z, sv[j].w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e >= keep) w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                sv[j] = (u4){w[0], w[1], w[2], w[3]};
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < STAGE; ++j) {
-            const int idx = tid + kPrefillThreads * j;
-            k_lds[k_chunk<D>(idx / C, idx % C)] = sk[j];
-            v_lds[v_chunk(idx >> 3, idx & 7)] = sv[j];
-        }
-        __syncthreads();
-        if (t + 1 < t_end) load(t + 1);
-        if (kb >= any_hi) continue;  // nothing here for this wave (its barriers are above)
-
-        f16v s[2];
-        s[0] = s[1] = (f16v)0.0f;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(k_lds[k_chunk<D>(32 * b + km, 2 * d + h)]), qf[d],
-                                                              s[b], 0, 0, 0);
-        }
-        const bool masked = absent || kb < all_lo || kb + kTileKeys > all_hi;
-        float top = Q4_NEG_INF;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int key = kb + 32 * b + 16 * (i >> 3) + 8 * h + (i & 7);
-                float x = score<EXTRA>(s[b][i], sp, key - qpos);
-                if (masked) x = key >= lo && key < hi && !gone[2 * b + (i >> 3)] ? x : Q4_NEG_INF;
-                s[b][i] = x;
-                top = fmaxf(top, x);
-            }
-        }
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m_new = fmaxf(m, top);
-        const float base = m_new == Q4_NEG_INF ? 0.0f : m_new;
-        const float f = exp2_hw(m - base);
-        if (__any(m_new > m)) {
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) acc[d] *= f;
-        }
-        float sum = 0.0f;
-        h8 pf[4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float p = exp2_hw(s[b][i] - base);
-                sum += p;
-                pf[2 * b + (i >> 3)][i & 7] = (_Float16)p;
-            }
-        }
-        l = l * f + sum;
-        m = m_new;
-
-        bool dirty = false;
-        if (masked) {
-            // A weight of zero hides a masked value only if the value is finite.
-            uint32_t bad = 0;
-#pragma unroll 4
-            for (int i = lane; i < D * (kTileKeys / 8); i += 64) {
-                const u4 v = v_lds[i];
-                bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
-            }
-            dirty = __any(bad != 0);
-        }
-        if (!dirty) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(v_lds[v_chunk(32 * d + n, 2 * kk + h)]),
-                                                                    pf[kk], acc[d], 0, 0, 0);
-            }
-        } else {
-            // Finite values as above; infinities and NaN that a row sees are counted
-            // by two products of zeros and ones and added as what they are.
-#pragma unroll 1
-            for (int kk = 0; kk < 4; ++kk) {
-                const h8 p = kk < 2 ? (kk == 0 ? pf[0] : pf[1]) : (kk == 2 ? pf[2] : pf[3]);
-                const bool is_gone = kk < 2 ? (kk == 0 ? gone[0] : gone[1]) : (kk == 2 ? gone[2] : gone[3]);
-                const int k0 = kb + 16 * kk + 8 * h;
-                const int from = is_gone ? 8 : lo - k0, to = hi - k0;  // keys k0 + from .. k0 + to - 1 are seen
-                uint32_t sw[4];
+            for (int i = tid; i < D * (kTileKeys / 8); i += kPrefillThreads) {
+                const int dim = i >> 3, vc = i & 7;
+                const int keep = (gone >> (vc >> 1)) & 1 ? 0 : min(max(it.len - (kb + 8 * vc), 0), 8);
+                u4 mask;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    sw[e] = (2 * e >= from && 2 * e < to ? 0x3C00u : 0u) |
-                            (2 * e + 1 >= from && 2 * e + 1 < to ? 0x3C000000u : 0u);
-                const h8 seen = as_h8((u4){sw[0], sw[1], sw[2], sw[3]});
+                    mask[e] = (2 * e < keep ? 0x0000FFFFu : 0u) | (2 * e + 1 < keep ? 0xFFFF0000u : 0u);
+                im[v_chunk<D>(dim, vc)] &= mask;
+            }
+            lds_barrier();
+        }
+        if (kb < any_hi) {
+            f16v s[2];
+            s[0] = s[1] = (f16v)0.0f;
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d) {
-                    const OddSplit v = split_odd(v_lds[v_chunk(32 * d + n, 2 * kk + h)]);
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v.fine, p, acc[d], 0, 0, 0);
-                    const f16v u = __builtin_amdgcn_mfma_f32_32x32x16_f16(v.up, seen, (f16v)0.0f, 0, 0, 0);
-                    const f16v w = __builtin_amdgcn_mfma_f32_32x32x16_f16(v.down, seen, (f16v)0.0f, 0, 0, 0);
+            for (int d = 0; d < D / 16; ++d) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(im[k_chunk<D>(32 * b + km, 2 * d + h)]), qf[d],
+                                                                  s[b], 0, 0, 0);
+            }
+            const bool masked = gone || kb < all_lo || kb + kTileKeys > all_hi;
+            // Without options the running maximum is that of the plain products
+            // (scale > 0), and scale and maximum enter the exponent in one
+            // multiply-add.
+            if constexpr (EXTRA) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[b][i] = score<true>(s[b][i], sp, kb + 32 * b + 16 * (i >> 3) + 8 * h + (i & 7) - qpos);
+                }
+            }
+            if (masked) {
+                const int from = lo - kb - 8 * h, to = hi - kb - 8 * h;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        if (u[i] > 0.0f) acc[d][i] += __builtin_inff();
-                        if (w[i] > 0.0f) acc[d][i] += Q4_NEG_INF;
+                        const int key = 32 * b + 16 * (i >> 3) + (i & 7);
+                        const bool seen = key >= from && key < to && !((gone >> (2 * b + (i >> 3))) & 1);
+                        s[b][i] = seen ? s[b][i] : Q4_NEG_INF;
                     }
                 }
             }
+            float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float m_new = fmaxf(m, EXTRA ? top : top * sp.scale2);
+            const float base = m_new == Q4_NEG_INF ? 0.0f : m_new;
+            if (__any(m_new > m)) {
+                const float f = exp2_hw(m - base);
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) acc[d] *= f;
+                m = m_new;
+            }
+            h8 pf[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p = exp2_hw(EXTRA ? s[b][i] - base : __builtin_fmaf(s[b][i], sp.scale2, -base));
+                    l += p;
+                    pf[2 * b + (i >> 3)][i & 7] = (_Float16)p;
+                }
+            }
+
+            bool dirty = false;
+            if (masked) {
+                // A weight of zero hides a masked value only if the value is finite.
+                uint32_t bad = 0;
+#pragma unroll 4
+                for (int i = lane; i < D * (kTileKeys / 8); i += 64) {
+                    const u4 v = im[kTileKeys * C + i];
+                    bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
+                }
+                dirty = __any(bad != 0);
+            }
+            if (!dirty) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d)
+                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(im[v_chunk<D>(32 * d + n, 2 * kk + h)]),
+                                                                        pf[kk], acc[d], 0, 0, 0);
+                }
+            } else {
+                // The finite values as above, then every other one by itself to the
+                // rows that see its position: rare, so written for few registers.
+#pragma unroll 1
+                for (int kk = 0; kk < 4; ++kk) {
+                    const h8 p = kk < 2 ? (kk == 0 ? pf[0] : pf[1]) : (kk == 2 ? pf[2] : pf[3]);
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d)
+                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            as_h8(finite_halves(im[v_chunk<D>(32 * d + n, 2 * kk + h)])), p, acc[d], 0, 0, 0);
+                }
+                const uint16_t* values = reinterpret_cast<const uint16_t*>(im);
+#pragma unroll 1
+                for (int i = 0; i < D * kTileKeys; ++i) {
+                    const int dim = i / kTileKeys, key = i % kTileKeys;
+                    const uint16_t bits = values[8 * v_chunk<D>(dim, key >> 3) + (key & 7)];
+                    if ((bits & 0x7C00) != 0x7C00) continue;
+                    const bool seen = kb + key >= lo && kb + key < hi && !((gone >> (key >> 4)) & 1);
+                    const float x = seen ? f16_bits_to_f32(bits) : 0.0f;
+                    // acc[d][i] of lane half h is dimension 32 d + 8 (i / 4) + 4 h + i % 4
+                    const bool mine = ((dim >> 2) & 1) == h;
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (mine && 32 * d + 8 * (e >> 2) + (e & 3) == (dim & ~4)) acc[d][e] += x;
+                    }
+                }
+            }
+        }
+        gone = gone_next;
+    };
+    if (t_begin < t_end) {
+        pg = pages_of(t_begin);
+        load(t_begin, pg, image0);
+        gone = pg.gone();
+        if (t_begin + 1 < t_end) pg = pages_of(t_begin + 1);
+        for (int t = t_begin;;) {
+            tile(t, image0, image1);
+            if (++t == t_end) break;
+            tile(t, image1, image0);
+            if (++t == t_end) break;
         }
     }
     l += __shfl_xor(l, 32, 64);
