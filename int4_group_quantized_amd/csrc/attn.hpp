@@ -63,6 +63,7 @@ struct AttnArgs {
     const int* q_starts;
     const int* prefix;     // or NULL
     int count;             // sequences
+    int splits;            // parts that the positions are cut into
 };
 
 // Widths the attention kernels are compiled for.

@@ -125,10 +125,85 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
     return (((w & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
 }
 
-// Eight halves with infinities and NaN set to zero.
-__device__ __forceinline__ u4 finite_halves(u4 v) {
-    return (u4){v.x & ~(odd_halves(v.x) * 0xFFFFu), v.y & ~(odd_halves(v.y) * 0xFFFFu),
-                v.z & ~(odd_halves(v.z) * 0xFFFFu), v.w & ~(odd_halves(v.w) * 0xFFFFu)};
+// Row r of a tile: the positions it sees are lo <= j < hi.  Rows that the tile
+// does not have are not live and see nothing.
+struct PrefillRow {
+    int token, head, pos, lo, hi;
+    bool live;
+};
+
+__device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const PrefillTile& it, int kvh, int r) {
+    PrefillRow q;
+    const int tok = r / a.group;
+    q.live = tok < it.n;
+    q.head = kvh * a.group + (q.live ? r - tok * a.group : 0);
+    q.token = it.token + (q.live ? tok : 0);
+    q.pos = it.pos + tok;
+    q.hi = q.lo = 0;
+    if (q.live && q.pos >= 0) {
+        const int prefix = a.prefix ? a.prefix[it.s] : 0;
+        q.hi = min(max(q.pos + 1, prefix), it.len);
+        q.lo = a.window > 0 ? max(q.pos + 1 - a.window, 0) : 0;
+    }
+    return q;
+}
+
+// A wave's 32 rows over positions [k_begin, k_end), one position after the
+// other, never touching what a row does not see: for tiles that hold infinities
+// or NaN in masked places, where the matrix products would multiply them by
+// zero.  Lanes n and n + 32 share row n, half the dimensions each.  Far slower;
+// the wave starts its rows again here, after the fast loop and with nothing of it
+// live, because the same handling inside that loop cost it 100 registers
+// (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
+template <int D, bool EXTRA>
+__device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int split,
+                                                                  int kvh, int wave, int k_begin, int k_end) {
+    const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
+    const PrefillRow q = prefill_row(a, it, kvh, wave * 32 + n);
+    const ScoreParams sp = score_params<EXTRA>(a, q.head);
+    const _Float16* qp = reinterpret_cast<const _Float16*>(a.q) + ((size_t)q.token * a.heads + q.head) * D + d0;
+    const int* row = a.c.table + (size_t)it.s * a.c.cols;
+    const int pmask = (1 << a.c.shift) - 1;
+    float acc[D / 2];
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) acc[i] = 0.0f;
+    float m = Q4_NEG_INF, l = 0.0f;
+    for (int key = k_begin; key < min(k_end, it.len); ++key) {
+        const int page = page_of(a.c, row, key);
+        if (page < 0) continue;
+        const _Float16* kp = reinterpret_cast<const _Float16*>(a.c.k) + (size_t)page * a.c.k_stride +
+                             (((size_t)kvh << a.c.shift) + (key & pmask)) * D + d0;
+        const _Float16* vp = reinterpret_cast<const _Float16*>(a.c.v) + (size_t)page * a.c.v_stride +
+                             ((size_t)(kvh * D + d0) << a.c.shift) + (key & pmask);
+        float dot = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < D / 2; ++i) dot = __builtin_fmaf((float)qp[i], (float)kp[i], dot);
+        dot += __shfl_xor(dot, 32, 64);
+        if (key < q.lo || key >= q.hi) continue;
+        const float s = score<EXTRA>(dot, sp, key - q.pos);
+        const float m_new = fmaxf(m, s), base = m_new == Q4_NEG_INF ? 0.0f : m_new;
+        const float f = exp2_hw(m - base), p = exp2_hw(s - base);
+        l = l * f + p;
+        m = m_new;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) acc[i] = acc[i] * f + p * (float)vp[(size_t)i << a.c.shift];
+    }
+    if (!q.live) return;
+    const long at = ((long)split * a.rows + q.token) * a.heads + q.head;
+    float* po = a.workspace + kAttnCounters + at * D + d0;
+    _Float16* op = reinterpret_cast<_Float16*>(a.out) + ((size_t)q.token * a.heads + q.head) * D + d0;
+    const bool partial = a.splits > 1;
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) {
+        if (partial) po[i] = acc[i];
+        else op[i] = (_Float16)(acc[i] * inv);
+    }
+    if (partial && d0 == 0) {
+        float* ml = a.workspace + kAttnCounters + (long)a.splits * a.rows * a.heads * D + at * 2;
+        ml[0] = m;
+        ml[1] = l;
+    }
 }
 
 // 16 bytes per lane from memory into LDS: lane i's to base + 16 i.
@@ -145,7 +220,8 @@ __device__ __forceinline__ void images_ready() {
 }
 
 template <int D, bool EXTRA>
-__global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefill_kernel(AttnArgs a, int tile0, int splits) {
+__global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefill_kernel(AttnArgs a, int tile0) {
+    const int splits = a.splits;
     constexpr int C = D / 8;             // 16-byte chunks of a K row
     constexpr int STAGE = D / 32;        // chunks per thread and tile, for K and for V
     constexpr int IMAGE = 2 * kTileKeys * C;  // chunks of a tile's image
@@ -160,19 +236,10 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
 
-    // This lane's query row and the positions it sees: lo <= j < hi.
-    const int r = wave * 32 + n;
-    const int tok = r / a.group;
-    const bool live = tok < it.n;
-    const int head = kvh * a.group + (live ? r - tok * a.group : 0);
-    const int token = it.token + (live ? tok : 0);
-    const int qpos = it.pos + tok;
+    const PrefillRow q = prefill_row(a, it, kvh, wave * 32 + n);
+    const int head = q.head, token = q.token, qpos = q.pos, hi = q.hi, lo = q.lo;
+    const bool live = q.live;
     const int prefix = a.prefix ? a.prefix[it.s] : 0;
-    int hi = 0, lo = 0;
-    if (live && qpos >= 0) {
-        hi = min(max(qpos + 1, prefix), it.len);
-        lo = a.window > 0 ? max(qpos + 1 - a.window, 0) : 0;
-    }
     // The wave's rows: all see [all_lo, all_hi), none sees from any_hi on.
     int all_hi = live ? hi : 0x7FFFFFFF, any_hi = hi, all_lo = lo;
     for (int d = 16; d >= 1; d >>= 1) {
@@ -260,6 +327,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     // One tile from image `im`, while the next one goes to `other`.
     Pages pg = {};
     int gone = 0;
+    uint32_t bad = 0;  // nonzero: a tile with masked positions holds infinities or NaN
     auto tile = [&](int t, u4* im, u4* other) {
         const int kb = t * kTileKeys;
         // This wave's loads and LDS reads are done; after the barrier everyone's:
@@ -342,53 +410,20 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                 }
             }
 
-            bool dirty = false;
             if (masked) {
                 // A weight of zero hides a masked value only if the value is finite.
-                uint32_t bad = 0;
 #pragma unroll 4
                 for (int i = lane; i < D * (kTileKeys / 8); i += 64) {
                     const u4 v = im[kTileKeys * C + i];
                     bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
                 }
-                dirty = __any(bad != 0);
             }
-            if (!dirty) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
+            for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-                    for (int d = 0; d < D / 32; ++d)
-                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(im[v_chunk<D>(32 * d + n, 2 * kk + h)]),
-                                                                        pf[kk], acc[d], 0, 0, 0);
-                }
-            } else {
-                // The finite values as above, then every other one by itself to the
-                // rows that see its position: rare, so written for few registers.
-#pragma unroll 1
-                for (int kk = 0; kk < 4; ++kk) {
-                    const h8 p = kk < 2 ? (kk == 0 ? pf[0] : pf[1]) : (kk == 2 ? pf[2] : pf[3]);
-#pragma unroll
-                    for (int d = 0; d < D / 32; ++d)
-                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            as_h8(finite_halves(im[v_chunk<D>(32 * d + n, 2 * kk + h)])), p, acc[d], 0, 0, 0);
-                }
-                const uint16_t* values = reinterpret_cast<const uint16_t*>(im);
-#pragma unroll 1
-                for (int i = 0; i < D * kTileKeys; ++i) {
-                    const int dim = i / kTileKeys, key = i % kTileKeys;
-                    const uint16_t bits = values[8 * v_chunk<D>(dim, key >> 3) + (key & 7)];
-                    if ((bits & 0x7C00) != 0x7C00) continue;
-                    const bool seen = kb + key >= lo && kb + key < hi && !((gone >> (key >> 4)) & 1);
-                    const float x = seen ? f16_bits_to_f32(bits) : 0.0f;
-                    // acc[d][i] of lane half h is dimension 32 d + 8 (i / 4) + 4 h + i % 4
-                    const bool mine = ((dim >> 2) & 1) == h;
-#pragma unroll
-                    for (int d = 0; d < D / 32; ++d) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (mine && 32 * d + 8 * (e >> 2) + (e & 3) == (dim & ~4)) acc[d][e] += x;
-                    }
-                }
+                for (int d = 0; d < D / 32; ++d)
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(im[v_chunk<D>(32 * d + n, 2 * kk + h)]),
+                                                                    pf[kk], acc[d], 0, 0, 0);
             }
         }
         gone = gone_next;
@@ -404,6 +439,10 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             tile(t, image1, image0);
             if (++t == t_end) break;
         }
+    }
+    if (__any(bad != 0)) {
+        prefill_rows_one_by_one<D, EXTRA>(a, it, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
+        return;
     }
     l += __shfl_xor(l, 32, 64);
 
@@ -441,7 +480,8 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
 
 // Join of the splits of one query row, one wave each, in order.
 template <int D>
-__global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int splits) {
+__global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
+    const int splits = a.splits;
     const int lane = threadIdx.x & 63;
     const long rows = (long)a.rows * a.heads;
     const long r = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -474,24 +514,24 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
 }
 
 template <int D>
-static hipError_t launch_prefill_attn(const AttnArgs& a, hipStream_t st) {
+static hipError_t launch_prefill_attn(AttnArgs a, hipStream_t st) {
     const long tiles = prefill_tiles(a.rows, a.count, a.group);
-    const int splits = prefill_splits(a.rows, a.count, a.group, a.c.kv_heads, a.max_length);
-    const long per_tile = (long)a.c.kv_heads * splits;
+    a.splits = prefill_splits(a.rows, a.count, a.group, a.c.kv_heads, a.max_length);
+    const long per_tile = (long)a.c.kv_heads * a.splits;
     const long most = ((1L << 24) - 1) / per_tile;  // tiles of one launch: at most 2^32 - 1 threads
     const bool extra = a.softcap > 0.0f || a.slopes;
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid((unsigned)((tiles - t < most ? tiles - t : most) * per_tile));
         if (extra)
-            hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, dim3(kPrefillThreads), 0, st, a, (int)t, splits);
+            hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, dim3(kPrefillThreads), 0, st, a, (int)t);
         else
-            hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, dim3(kPrefillThreads), 0, st, a, (int)t, splits);
+            hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, dim3(kPrefillThreads), 0, st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (splits == 1) return hipSuccess;
+    if (a.splits == 1) return hipSuccess;
     const long rows = (long)a.rows * a.heads;
-    hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a, splits);
+    hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
