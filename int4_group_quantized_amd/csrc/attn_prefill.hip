@@ -18,9 +18,8 @@
 // each 16) as it stands when matrix row m of a 32-key block loads key
 // 16(m/16) + 8(m/4%2) + 4(m/8%2) + m%4: register r then is key 16(r/8) + 8h + r%8.
 //
-// LDS rows are swizzled in 16-byte chunks (chunk ^ a function of the row) so
-// that the 32 rows of an operand load fall on different banks.  The next tile
-// goes straight from memory into a second LDS image while this one is computed.
+// LDS rows are swizzled in 16-byte chunks so that the rows of an operand load
+// fall on different banks (k_chunk).  The next tile goes straight from memory into a second LDS image while this one is computed.
 //
 // Few tokens on a long cache leave most CUs idle, so the visible tiles are
 // then cut into equal splits joined by a second launch.
@@ -106,16 +105,21 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
 }
 
 // Chunk of 16 bytes (eight halves) c of K row `key`, and of V row `dim`, in a
-// tile's LDS image: K [64][D / 8], V [D][8] behind it.
+// tile's LDS image: K [64][D / 8], V [D][8] behind it.  LDS serves 16 lanes of a
+// 16-byte read at a time from 64 banks, so the 16 rows n .. n + 15 of an operand
+// (n: matrix row, see above) have to fall on different sixteenths of 256 bytes:
+// the part of n that the row pitch does not already spread is exclusive-ored
+// into the chunk.  With the permutation over 128 bytes only, half of the LDS
+// cycles were conflicts.
 template <int D>
 __device__ __forceinline__ int k_chunk(int key, int c) {
-    constexpr int MASK = D % 64 == 0 ? 7 : 3;  // dim 96 has 12 chunks, which only two bits permute
-    const int f = (key & 3) | ((key >> 1) & 4);
-    return key * (D / 8) + (c ^ (f & MASK));
+    const int n = (key & 3) | ((key >> 1) & 4) | ((key << 1) & 8);  // matrix row, low four bits
+    constexpr int SHIFT = D % 128 == 0 ? 0 : D % 64 == 0 ? 1 : 2;   // pitch 256 or 512, 128 or 384, 192 bytes
+    return key * (D / 8) + (c ^ (n >> SHIFT));
 }
 template <int D>
 __device__ __forceinline__ int v_chunk(int dim, int c) {
-    return kTileKeys * (D / 8) + dim * (kTileKeys / 8) + (c ^ (dim & 7));
+    return kTileKeys * (D / 8) + dim * (kTileKeys / 8) + (c ^ ((dim >> 1) & 7));
 }
 
 __device__ __forceinline__ h8 as_h8(u4 v) { return __builtin_bit_cast(h8, v); }
@@ -204,6 +208,12 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
         ml[0] = m;
         ml[1] = l;
     }
+}
+
+// max(a, b) of two matrix results: the median with +inf.  fmaxf would first pass
+// each of them through an instruction of its own to quieten signalling NaN.
+__device__ __forceinline__ float max_of(float a, float b) {
+    return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
 }
 
 // 16 bytes per lane from memory into LDS: lane i's to base + 16 i.
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             load_lds(k0 + (unsigned)((key & 15) * D + 8 * c), im + kPrefillThreads * j + 64 * wave);
         }
         // x = 256 j + tid: dimension 32 j + tid / 8, whose swizzle is the same for all j
-        const int vc = (tid & 7) ^ ((tid >> 3) & 7);
+        const int vc = v_chunk<D>(tid >> 3, tid & 7) & 7;
         const uint16_t* v0 = (vc < 4 ? (vc < 2 ? vp[0] : vp[1]) : (vc < 6 ? vp[2] : vp[3])) + 8 * (vc & 1);
 #pragma unroll
         for (int j = 0; j < STAGE; ++j)
@@ -353,15 +363,32 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             lds_barrier();
         }
         if (kb < any_hi) {
+            // Operand reads run ahead of the products: half of K's, the rest of K's,
+            // half of V's before the softmax.
+            constexpr int KH = D / 32;  // of D / 16 steps
+            u4 kf[2][KH][2];
+#pragma unroll
+            for (int d = 0; d < KH; ++d)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) kf[0][d][b] = im[k_chunk<D>(32 * b + km, 2 * d + h)];
+#pragma unroll
+            for (int d = 0; d < KH; ++d)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) kf[1][d][b] = im[k_chunk<D>(32 * b + km, 2 * (KH + d) + h)];
+            __builtin_amdgcn_sched_barrier(0);
             f16v s[2];
             s[0] = s[1] = (f16v)0.0f;
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
+            for (int d = 0; d < 2 * KH; ++d)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(im[k_chunk<D>(32 * b + km, 2 * d + h)]), qf[d],
-                                                                  s[b], 0, 0, 0);
-            }
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(kf[d / KH][d % KH][b]), qf[d], s[b], 0, 0, 0);
+            u4 vf[2][D / 32];
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) vf[0][d] = im[v_chunk<D>(32 * d + n, h)];
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) vf[1][d] = im[v_chunk<D>(32 * d + n, 2 + h)];
+            __builtin_amdgcn_sched_barrier(0);
             const bool masked = gone || kb < all_lo || kb + kTileKeys > all_hi;
             // Without options the running maximum is that of the plain products
             // (scale > 0), and scale and maximum enter the exponent in one
@@ -386,30 +413,39 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                     }
                 }
             }
-            float top = fmaxf(s[0][0], s[1][0]);
+            float tops[16];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float m_new = fmaxf(m, EXTRA ? top : top * sp.scale2);
-            const float base = m_new == Q4_NEG_INF ? 0.0f : m_new;
-            if (__any(m_new > m)) {
-                const float f = exp2_hw(m - base);
+            for (int i = 0; i < 16; ++i) tops[i] = max_of(s[0][i], s[1][i]);
+#pragma unroll
+            for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                for (int i = 0; i < w; ++i) tops[i] = fmaxf(tops[i], tops[i + w]);
+            float top = fmaxf(tops[0], __shfl_xor(tops[0], 32, 64));
+            if constexpr (!EXTRA) top *= sp.scale2;
+            // The maximum that the exponents are taken from follows the true one only
+            // when it is more than 2^8 behind: weights then stay below 2^8, and the
+            // outputs are rarely rescaled after the first tiles.
+            if (__any(top > m + 8.0f)) {
+                const float m_new = fmaxf(m, top);
+                const float f = part_weight(m, m_new);
                 l *= f;
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d) acc[d] *= f;
                 m = m_new;
             }
+            const float base = m == Q4_NEG_INF ? 0.0f : m;
+            float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             h8 pf[4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float p = exp2_hw(EXTRA ? s[b][i] - base : __builtin_fmaf(s[b][i], sp.scale2, -base));
-                    l += p;
+                    sums[i & 3] += p;
                     pf[2 * b + (i >> 3)][i & 7] = (_Float16)p;
                 }
             }
-
+            l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             if (masked) {
                 // A weight of zero hides a masked value only if the value is finite.
 #pragma unroll 4
@@ -421,9 +457,10 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(im[v_chunk<D>(32 * d + n, 2 * kk + h)]),
-                                                                    pf[kk], acc[d], 0, 0, 0);
+                for (int d = 0; d < D / 32; ++d) {
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(vf[kk & 1][d]), pf[kk], acc[d], 0, 0, 0);
+                    if (kk < 2) vf[kk][d] = im[v_chunk<D>(32 * d + n, 2 * (kk + 2) + h)];
+                }
             }
         }
         gone = gone_next;
