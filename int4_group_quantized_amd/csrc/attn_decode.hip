@@ -38,7 +38,6 @@ constexpr int kDecodeWaves = 4;
 constexpr int kDecodeThreads = 64 * kDecodeWaves;
 constexpr int kDecodeSlots = 512;   // workgroups wanted per launch: two per CU
 static_assert(kDecodeSlots <= kAttnCounters, "a counter for each sequence of several parts");
-constexpr int kJoin = 16;           // parts joined per round (a power of two)
 constexpr int kDecodeMinTiles = 4;  // tiles per part at least: one per wave
 
 // First visible tile and the number of tiles of sequence b.
@@ -360,58 +359,9 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
     // in order, whichever it is.  It leaves the counter at zero for the next call.
     if (!parts_done(ws.counters + it.split * pairs + pair, it.parts)) return;
     for (int r = wave; r < nrows; r += kDecodeWaves) {
-        const float* ml = ws.ml + ((long)it.slot * a.heads + head0 + r) * 2;
-        const float* po = ws.o + ((long)it.slot * a.heads + head0 + r) * D;
-        // Rounds of up to kJoin parts: their outputs, maxima and sums are requested
-        // together, lane p holding part p's statistics.
-        constexpr int PER = (D + 127) / 128;  // pairs of dimensions per lane
-        float2 o[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) o[i] = {0.0f, 0.0f};
-        float top = Q4_NEG_INF, sum = 0.0f;
-        for (int p0 = 0; p0 < it.parts; p0 += kJoin) {
-            float2 v[kJoin][PER];
-            float2 st = {Q4_NEG_INF, 0.0f};
-            if (lane < kJoin && p0 + lane < it.parts) st = share_load(ml + (long)(p0 + lane) * a.heads * 2);
-#pragma unroll
-            for (int p = 0; p < kJoin; ++p) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int d = 2 * (lane + 64 * i);
-                    v[p][i] = {0.0f, 0.0f};
-                    if (p0 + p < it.parts && d < D) v[p][i] = share_load(po + (long)(p0 + p) * a.heads * D + d);
-                }
-            }
-            float t = st.x;
-#pragma unroll
-            for (int d = kJoin / 2; d >= 1; d >>= 1) t = fmaxf(t, __shfl_xor(t, d, 64));
-            t = fmaxf(top, __shfl(t, 0, 64));
-            const float f0 = part_weight(top, t), w = part_weight(st.x, t);
-            float s1 = st.y * w;
-#pragma unroll
-            for (int d = kJoin / 2; d >= 1; d >>= 1) s1 += __shfl_xor(s1, d, 64);
-            sum = sum * f0 + __shfl(s1, 0, 64);
-            top = t;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) o[i] = {o[i].x * f0, o[i].y * f0};
-#pragma unroll
-            for (int p = 0; p < kJoin; ++p) {
-                const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), p));
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    o[i].x += v[p][i].x * f;
-                    o[i].y += v[p][i].y * f;
-                }
-            }
-        }
-        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-        uint16_t* op = a.out + ((size_t)it.b * a.heads + head0 + r) * D;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int d = 2 * (lane + 64 * i);
-            if (d < D)
-                *reinterpret_cast<uint32_t*>(op + d) = as_u32((h2){(_Float16)(o[i].x * inv), (_Float16)(o[i].y * inv)});
-        }
+        const long at = (long)it.slot * a.heads + head0 + r;
+        join_parts<D, true>(ws.o + at * D, ws.ml + at * 2, a.heads, it.parts,
+                            a.out + ((size_t)it.b * a.heads + head0 + r) * D);
     }
 }
 

@@ -33,7 +33,11 @@ constexpr int kPrefillWaves = 4;
 constexpr int kPrefillThreads = 64 * kPrefillWaves;
 constexpr int kPrefillRows = 32 * kPrefillWaves;
 constexpr int kPrefillBlocks = 512;     // workgroups below which the cache is split
-constexpr int kPrefillMinTiles = 4;     // tiles per split at least
+// Tiles per split at least (34 tokens on 8,000 positions: 4 tiles 20.7 us, 2
+// tiles 23.9, 8 tiles 25.1), and tiles below which the second launch costs more
+// than it saves (five prompts of up to 473 tokens: 23.4 us whole, 25.8 halved).
+constexpr int kPrefillMinTiles = 4;
+constexpr int kPrefillSplitTiles = 16;
 
 // Tokens per workgroup.
 __host__ __device__ inline int prefill_tokens(int group) { return kPrefillRows / group; }
@@ -46,7 +50,9 @@ static long prefill_tiles(long tokens, long count, int group) {
 
 static int prefill_splits(long tokens, long count, int group, int kv_heads, long max_length) {
     const long blocks = prefill_tiles(tokens, count, group) * kv_heads;
-    const long most = ((max_length + kTileKeys - 1) / kTileKeys + kPrefillMinTiles - 1) / kPrefillMinTiles;
+    const long length = (max_length + kTileKeys - 1) / kTileKeys;
+    if (length < kPrefillSplitTiles) return 1;
+    const long most = (length + kPrefillMinTiles - 1) / kPrefillMinTiles;
     const long want = kPrefillBlocks / blocks;
     const long n = want < most ? want : most;
     return n > 1 ? (int)n : 1;
@@ -519,7 +525,6 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
 template <int D>
 __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     const int splits = a.splits;
-    const int lane = threadIdx.x & 63;
     const long rows = (long)a.rows * a.heads;
     const long r = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (r >= rows) return;
@@ -527,27 +532,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     const int token = (int)(r / a.heads);
     if (token < a.q_starts[0] || token >= a.q_starts[a.count]) return;
     const float* part = a.workspace + kAttnCounters;
-    const float* ml = part + (long)splits * rows * D;
-    float top = Q4_NEG_INF;
-    for (int s = lane; s < splits; s += 64) top = fmaxf(top, ml[(s * rows + r) * 2]);
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    constexpr int PER = (D + 63) / 64;
-    float o[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = 0.0f;
-    float sum = 0.0f;
-    for (int s = 0; s < splits; ++s) {
-        const float f = part_weight(ml[(s * rows + r) * 2], top);
-        sum += ml[(s * rows + r) * 2 + 1] * f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 64 * i < D) o[i] += part[(s * rows + r) * D + lane + 64 * i] * f;
-    }
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (lane + 64 * i < D)
-            a.out[r * D + lane + 64 * i] = __builtin_bit_cast(uint16_t, (_Float16)(o[i] * inv));
+    join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits, a.out + r * D);
 }
 
 template <int D>

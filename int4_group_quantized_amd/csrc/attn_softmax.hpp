@@ -55,6 +55,64 @@ __device__ __forceinline__ bool parts_done(int* counter, int parts) {
     return last != 0;
 }
 
+// One wave joins the parts of one query row in order and writes the row: part p
+// has its output at po + p * stride * D and (m, l) at ml + p * stride * 2.  Up
+// to kJoin parts at a time are requested together, lane p holding part p's
+// statistics; part after part waited for each time took 3.3 us for 8 parts.
+// AGENT: the parts come from workgroups of the same launch.
+constexpr int kJoin = 16;
+template <int D, bool AGENT>
+__device__ __forceinline__ void join_parts(const float* po, const float* ml, long stride, int parts, uint16_t* out) {
+    const int lane = threadIdx.x & 63;
+    auto get = [](const float* p) { return AGENT ? share_load(p) : *reinterpret_cast<const float2*>(p); };
+    constexpr int PER = (D + 127) / 128;  // pairs of dimensions per lane
+    float2 o[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] = {0.0f, 0.0f};
+    float top = Q4_NEG_INF, sum = 0.0f;
+    for (int p0 = 0; p0 < parts; p0 += kJoin) {
+        float2 v[kJoin][PER];
+        float2 st = {Q4_NEG_INF, 0.0f};
+        if (lane < kJoin && p0 + lane < parts) st = get(ml + (long)(p0 + lane) * stride * 2);
+#pragma unroll
+        for (int p = 0; p < kJoin; ++p) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int d = 2 * (lane + 64 * i);
+                v[p][i] = {0.0f, 0.0f};
+                if (p0 + p < parts && d < D) v[p][i] = get(po + (long)(p0 + p) * stride * D + d);
+            }
+        }
+        float t = st.x;
+#pragma unroll
+        for (int d = kJoin / 2; d >= 1; d >>= 1) t = fmaxf(t, __shfl_xor(t, d, 64));
+        t = fmaxf(top, __shfl(t, 0, 64));
+        const float f0 = part_weight(top, t), w = part_weight(st.x, t);
+        float s1 = st.y * w;
+#pragma unroll
+        for (int d = kJoin / 2; d >= 1; d >>= 1) s1 += __shfl_xor(s1, d, 64);
+        sum = sum * f0 + __shfl(s1, 0, 64);
+        top = t;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) o[i] = {o[i].x * f0, o[i].y * f0};
+#pragma unroll
+        for (int p = 0; p < kJoin; ++p) {
+            const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), p));
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                o[i].x += v[p][i].x * f;
+                o[i].y += v[p][i].y * f;
+            }
+        }
+    }
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int d = 2 * (lane + 64 * i);
+        if (d < D) *reinterpret_cast<uint32_t*>(out + d) = as_u32((h2){(_Float16)(o[i].x * inv), (_Float16)(o[i].y * inv)});
+    }
+}
+
 // A dot product as a base-2 score.  EXTRA: with the options' cap and bias;
 // tanh(x) = 1 - 2 / (e^(2x) + 1), absolute error about 2^-23, so the score's
 // is about softcap * 2^-23.
