@@ -20,7 +20,7 @@
 //    one token and HB consecutive heads.  A lane holds four dimensions: two
 //    pairs with either pair layout, so that no value crosses lanes except for
 //    the norm's sum.
-//  * values: 64 tokens of one kv head go through LDS and leave transposed,
+//  * values: up to 64 tokens of one kv head go through LDS and leave transposed,
 //    eight positions of one dimension per 16-byte store where the eight tokens
 //    sit on an aligned run of one page.
 #include "attn.hpp"
@@ -29,7 +29,18 @@ namespace q4 {
 
 constexpr int kAppendThreads = 256;
 constexpr int kValueTokens = 64;
-constexpr int kValuePitch = kValueTokens + 2;  // halves; 33 dwords, so a column's dimensions fall on different banks
+constexpr int kAppendAhead = 4;      // heads whose rows a team requests together
+// Teams beyond which a team serves more heads (2, 4, 8, ... of one token), so
+// that sines and cosines are formed less often.  8,192 tokens of 40 query and key
+// heads (302 MB): one head per team 100 us, 4 heads 66 us, 8 heads 64 us, 16
+// heads 68 us, 32 heads 82 us; fewer teams than this gain nothing from it.
+constexpr long kAppendTeams = 65536;
+constexpr int kValuePitch = kValueTokens + 10;  // halves; 37 dwords, so a token's dimensions fall on different banks
+// Tokens per workgroup of values: kValueTokens where that gives kValueBlocks
+// workgroups, else kValueFew (one token of each of 64
+// sequences: 3.7 us with 8, 5.2 with 16, 9.0 with 64).
+constexpr int kValueFew = 8;
+constexpr long kValueBlocks = 512;
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -46,62 +57,68 @@ __device__ __forceinline__ int append_slot(const AppendArgs& a, int t, int& off)
     return page_of(a.c, a.c.table + (size_t)s * a.c.cols, pos);
 }
 
+// `vt` tokens (a multiple of 8 up to kValueTokens) of one kv head.
 template <int D>
-__device__ __forceinline__ void append_values(const AppendArgs& a, int tile, int head, uint16_t* lds) {
+__device__ __forceinline__ void append_values(const AppendArgs& a, int tile, int vt, int head, uint16_t* lds) {
     __shared__ int slot_page[kValueTokens];
     __shared__ int slot_off[kValueTokens];
-    __shared__ int run[kValueTokens / 8];
+    __shared__ int run[kValueTokens / 8 + 1];
     const int tid = threadIdx.x;
-    const int t0 = tile * kValueTokens;
-    const int nt = min(kValueTokens, a.tokens - t0);
+    const int t0 = tile * vt;
+    const int nt = min(vt, a.tokens - t0);
     if (tid < nt) {
         int off;
         slot_page[tid] = append_slot(a, t0 + tid, off);
         slot_off[tid] = off;
     }
+    // Columns are shifted by the first position's place in its run of eight, so
+    // that a prompt's aligned runs start at multiples of eight columns wherever
+    // it starts.
+    const int shift = a.positions[t0] & 7;
     const float* src = a.qkv + (size_t)t0 * a.ld + (size_t)(a.heads + a.c.kv_heads + head) * D;
     for (int i = tid; i < nt * (D / 4); i += kAppendThreads) {
         const int t = i / (D / 4), d = i % (D / 4) * 4;
         const f4 v = *reinterpret_cast<const f4*>(src + (size_t)t * a.ld + d);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            lds[(d + e) * kValuePitch + t] = __builtin_bit_cast(uint16_t, (_Float16)v[e]);
+            lds[(d + e) * kValuePitch + t + shift] = __builtin_bit_cast(uint16_t, (_Float16)v[e]);
     }
     __syncthreads();
-    const int groups = (nt + 7) / 8;
+    const int groups = (nt + shift + 7) / 8;
     if (tid < groups) {
-        int ok = 8 * tid + 8 <= nt;
+        const int t = 8 * tid - shift;  // token of the group's first column
+        int ok = t >= 0 && t + 8 <= nt;
         if (ok) {
-            const int p = slot_page[8 * tid], o = slot_off[8 * tid];
+            const int p = slot_page[t], o = slot_off[t];
             ok = p >= 0 && (o & 7) == 0;
-            for (int e = 1; e < 8; ++e) ok = ok && slot_page[8 * tid + e] == p && slot_off[8 * tid + e] == o + e;
+            for (int e = 1; e < 8; ++e) ok = ok && slot_page[t + e] == p && slot_off[t + e] == o + e;
         }
         run[tid] = ok;
     }
     __syncthreads();
     const int P = 1 << a.c.shift;
     for (int i = tid; i < groups * D; i += kAppendThreads) {
-        const int g = i % groups, d = i / groups;
+        const int g = i % groups, d = i / groups, t = 8 * g - shift;
         const uint16_t* col = lds + d * kValuePitch + 8 * g;
         const size_t base = ((size_t)head * D + d) * P;
         if (run[g]) {
             const uint32_t* w = reinterpret_cast<const uint32_t*>(col);
-            *reinterpret_cast<u4*>(a.c.v + (size_t)slot_page[8 * g] * a.c.v_stride + base + slot_off[8 * g]) =
+            *reinterpret_cast<u4*>(a.c.v + (size_t)slot_page[t] * a.c.v_stride + base + slot_off[t]) =
                 (u4){w[0], w[1], w[2], w[3]};
         } else {
-            for (int e = 0; e < 8 && 8 * g + e < nt; ++e) {
-                const int p = slot_page[8 * g + e];
-                if (p >= 0) a.c.v[(size_t)p * a.c.v_stride + base + slot_off[8 * g + e]] = col[e];
+            for (int e = max(0, -t); e < 8 && t + e < nt; ++e) {
+                const int p = slot_page[t + e];
+                if (p >= 0) a.c.v[(size_t)p * a.c.v_stride + base + slot_off[t + e]] = col[e];
             }
         }
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(AppendArgs a, int value_blocks, int hb) {
+__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(AppendArgs a, int value_blocks, int vt, int hb) {
     __shared__ uint16_t lds[D * kValuePitch];
     if ((int)blockIdx.x < value_blocks) {
-        append_values<D>(a, blockIdx.x / a.c.kv_heads, blockIdx.x % a.c.kv_heads, lds);
+        append_values<D>(a, blockIdx.x / a.c.kv_heads, vt, blockIdx.x % a.c.kv_heads, lds);
         return;
     }
     constexpr int LR = D <= 64 ? 16 : D <= 128 ? 32 : 64;
@@ -135,48 +152,64 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(AppendArgs 
             c0 *= a.mscale; s0 *= a.mscale; c1 *= a.mscale; s1 *= a.mscale;
         }
     }
+    float wq[4] = {1.0f, 1.0f, 1.0f, 1.0f}, wk[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if (wide && a.q_norm) {
+        wq[0] = f16_bits_to_f32(a.q_norm[oa]);
+        wq[1] = f16_bits_to_f32(a.q_norm[oa + 1]);
+        wq[2] = f16_bits_to_f32(a.q_norm[ob]);
+        wq[3] = f16_bits_to_f32(a.q_norm[ob + 1]);
+    }
+    if (wide && a.k_norm) {
+        wk[0] = f16_bits_to_f32(a.k_norm[oa]);
+        wk[1] = f16_bits_to_f32(a.k_norm[oa + 1]);
+        wk[2] = f16_bits_to_f32(a.k_norm[ob]);
+        wk[3] = f16_bits_to_f32(a.k_norm[ob + 1]);
+    }
     const float* src = a.qkv + (size_t)t * a.ld;
-    for (int h = h0; h < h1; ++h) {
-        const bool is_q = h < a.heads;
-        const float* x = src + (size_t)h * D;
-        float2 u = {0.0f, 0.0f}, w = {0.0f, 0.0f};
-        if (wide) {
-            u = *reinterpret_cast<const float2*>(x + oa);
-            w = *reinterpret_cast<const float2*>(x + ob);
-        }
-        const uint16_t* norm = is_q ? a.q_norm : a.k_norm;
-        if (norm) {
-            const float ss = reduce_lanes<LR>(u.x * u.x + u.y * u.y + (w.x * w.x + w.y * w.y));
-            const float r = 1.0f / __builtin_sqrtf(ss * (1.0f / D) + a.eps);
-            if (wide) {
-                u.x *= r * f16_bits_to_f32(norm[oa]);
-                u.y *= r * f16_bits_to_f32(norm[oa + 1]);
-                w.x *= r * f16_bits_to_f32(norm[ob]);
-                w.y *= r * f16_bits_to_f32(norm[ob + 1]);
+    uint16_t* qrow = a.q + (size_t)t * a.heads * D;
+    uint16_t* krow = a.c.k + (size_t)max(page, 0) * a.c.k_stride + (size_t)off * D;
+    for (int h = h0; h < h1; h += kAppendAhead) {
+        // The rows of several heads are requested together.
+        float2 us[kAppendAhead], ws[kAppendAhead];
+#pragma unroll
+        for (int j = 0; j < kAppendAhead; ++j) {
+            us[j] = ws[j] = {0.0f, 0.0f};
+            if (wide && h + j < h1) {
+                const float* x = src + (size_t)(h + j) * D;
+                us[j] = *reinterpret_cast<const float2*>(x + oa);
+                ws[j] = *reinterpret_cast<const float2*>(x + ob);
             }
         }
-        if (!wide) continue;
-        float2 y = u, z = w;
-        if (split) {
-            y.x = u.x * c0 - w.x * s0;
-            z.x = w.x * c0 + u.x * s0;
-            y.y = u.y * c1 - w.y * s1;
-            z.y = w.y * c1 + u.y * s1;
-        } else if (turned) {
-            y.x = u.x * c0 - u.y * s0;
-            y.y = u.y * c0 + u.x * s0;
-            z.x = w.x * c1 - w.y * s1;
-            z.y = w.y * c1 + w.x * s1;
+#pragma unroll
+        for (int j = 0; j < kAppendAhead; ++j) {
+            if (h + j >= h1) break;
+            const bool is_q = h + j < a.heads;
+            float2 u = us[j], w = ws[j];
+            if (is_q ? a.q_norm != nullptr : a.k_norm != nullptr) {
+                const float ss = reduce_lanes<LR>(u.x * u.x + u.y * u.y + (w.x * w.x + w.y * w.y));
+                const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+                u.x *= r * (is_q ? wq[0] : wk[0]);
+                u.y *= r * (is_q ? wq[1] : wk[1]);
+                w.x *= r * (is_q ? wq[2] : wk[2]);
+                w.y *= r * (is_q ? wq[3] : wk[3]);
+            }
+            float2 y = u, z = w;
+            if (split) {
+                y.x = u.x * c0 - w.x * s0;
+                z.x = w.x * c0 + u.x * s0;
+                y.y = u.y * c1 - w.y * s1;
+                z.y = w.y * c1 + u.y * s1;
+            } else if (turned) {
+                y.x = u.x * c0 - u.y * s0;
+                y.y = u.y * c0 + u.x * s0;
+                z.x = w.x * c1 - w.y * s1;
+                z.y = w.y * c1 + w.x * s1;
+            }
+            if (!wide || (!is_q && page < 0)) continue;
+            uint16_t* dst = is_q ? qrow + (size_t)(h + j) * D : krow + ((size_t)(h + j - a.heads) << a.c.shift) * D;
+            *reinterpret_cast<uint32_t*>(dst + oa) = pack_f16(y.x, y.y);
+            *reinterpret_cast<uint32_t*>(dst + ob) = pack_f16(z.x, z.y);
         }
-        uint16_t* dst;
-        if (is_q) {
-            dst = a.q + ((size_t)t * a.heads + h) * D;
-        } else {
-            if (page < 0) continue;
-            dst = a.c.k + (size_t)page * a.c.k_stride + (((size_t)(h - a.heads) << a.c.shift) + off) * D;
-        }
-        *reinterpret_cast<uint32_t*>(dst + oa) = pack_f16(y.x, y.y);
-        *reinterpret_cast<uint32_t*>(dst + ob) = pack_f16(z.x, z.y);
     }
 }
 
@@ -185,14 +218,17 @@ static hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
     constexpr int TEAMS = kAppendThreads / (D <= 64 ? 16 : D <= 128 ? 32 : 64);
     const int rows = a.heads + a.c.kv_heads;
     int hb = 1;
+    while ((long)a.tokens * ((rows + hb - 1) / hb) > kAppendTeams && hb < rows) hb *= 2;
     // A launch takes at most 2^32 - 1 threads.
     while ((long)a.tokens * ((rows + hb - 1) / hb) > (1L << 23) * TEAMS && hb < rows) hb *= 2;
-    const long value_blocks = ((long)a.tokens + kValueTokens - 1) / kValueTokens * a.c.kv_heads;
+    const long full = ((long)a.tokens + kValueTokens - 1) / kValueTokens * a.c.kv_heads;
+    const int vt = full >= kValueBlocks ? kValueTokens : kValueFew;
+    const long value_blocks = ((long)a.tokens + vt - 1) / vt * a.c.kv_heads;
     const long teams = (long)a.tokens * ((rows + hb - 1) / hb);
     const long grid = value_blocks + (teams + TEAMS - 1) / TEAMS;
     if (grid > (1L << 24) - 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL((rope_append_kernel<D>), dim3((unsigned)grid), dim3(kAppendThreads), 0, st, a,
-                       (int)value_blocks, hb);
+                       (int)value_blocks, vt, hb);
     return hipGetLastError();
 }
 
