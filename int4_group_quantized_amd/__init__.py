@@ -120,6 +120,13 @@ def _load():
 
 _lib = _load()
 
+# The cache and attention calls' checks and calls are compiled (csrc/binding.cpp);
+# their module links to the library loaded above.
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{e}: build the binding with `python int4_group_quantized_amd/build.py`") from e
+
 
 def library() -> ctypes.CDLL:
     return _lib
@@ -323,42 +330,16 @@ def q4g128_gemv_int8(q, scales, x, y=None, stream=None) -> torch.Tensor:
     return y
 
 
-def _cache(k_cache, v_cache, table) -> KvCache:
-    """The cache descriptor; pages may be a strided slice of a larger pool, each page itself is contiguous."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must live on a GPU (got {t.device})")
-        if t.dtype != torch.float16:
-            raise TypeError(f"{name} must be torch.float16 (got {t.dtype})")
-        if t.dim() != 4:
-            raise ValueError("k_cache must be [pages][kv_heads][page][dim], v_cache [pages][kv_heads][dim][page]")
-    pages, kv_heads, page, dim = k_cache.shape
-    if tuple(v_cache.shape) != (pages, kv_heads, dim, page):
-        raise ValueError(f"v_cache must have shape {(pages, kv_heads, dim, page)} (got {tuple(v_cache.shape)})")
-    if k_cache.stride()[1:] != (page * dim, dim, 1) or v_cache.stride()[1:] != (page * dim, page, 1):
-        raise ValueError("each page of k_cache and v_cache must be contiguous")
-    if table.dim() != 2:
-        raise ValueError("table must be [sequences][table_cols]")
-    _dev_tensor(table, "table", torch.int32, tuple(table.shape))
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), pages, k_cache.stride(0),
-                   v_cache.stride(0), table.shape[0], table.shape[1], kv_heads, dim, page)
-
-
-def _empty(shape, dtype, dev, stream):
-    """Memory of the stream that the call runs on, so that the allocator orders its reuse with the call."""
+def _on_stream(stream, call, name):
+    """call() on the given stream (None: the current one), its memory from that stream too."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _optional(t, name, dtype, shape):
-    if t is None:
-        return None
-    _dev_tensor(t, name, dtype, shape)
-    return t.data_ptr()
+        got = call()
+    else:
+        with torch.cuda.stream(stream):
+            got = call()
+    if type(got) is int:
+        raise Q4Error(got, name)
+    return got
 
 
 def q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq=None, q_norm=None, k_norm=None,
@@ -367,90 +348,13 @@ def q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads,
 
     qkv: fp32 [T][>= (heads + 2 kv_heads) dim], rows may be strided (a product's output: columns after the
     value heads are left alone).  k_cache fp16 [pages][kv_heads][page][dim], v_cache fp16
-    [pages][kv_heads][dim][page], table int32 [sequences][cols].  positions int32 [T]; seq int32 [T] (None:
-    token t is of sequence t).  inv_freq fp32 [rot / 2] (None: no rotation).  q_norm, k_norm fp16 [dim] or None.
+    [pages][kv_heads][dim][page], table int32 [sequences][cols]; a page is contiguous, the pages may be a strided
+    slice of a larger pool.  positions int32 [T]; seq int32 [T] (None: token t is of sequence t).  inv_freq fp32
+    [rot / 2] (None: no rotation).  q_norm, k_norm fp16 [dim] or None.
     """
-    cache = _cache(k_cache, v_cache, table)
-    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
-        raise ValueError("qkv must be [T][columns]")
-    tokens, columns = qkv.shape
-    if qkv.device.type != "cuda":
-        raise ValueError(f"qkv must live on a GPU (got {qkv.device})")
-    if qkv.dtype != torch.float32:
-        raise TypeError(f"qkv must be torch.float32 (got {qkv.dtype})")
-    if columns < (heads + 2 * cache.kv_heads) * cache.dim:
-        raise ValueError(f"qkv has {columns} columns, fewer than (heads + 2 kv_heads) dim")
-    if qkv.stride(1) != 1:
-        raise ValueError("rows of qkv must be contiguous")
-    _dev_tensor(positions, "positions", torch.int32, (tokens,))
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot / 2]")
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    if q is None:
-        q = _empty((tokens, heads, cache.dim), torch.float16, qkv.device, stream)
-    _dev_tensor(q, "q", torch.float16, (tokens, heads, cache.dim))
-    freq = _optional(inv_freq, "inv_freq", torch.float32, (rot // 2,))
-    seqp = _optional(seq, "seq", torch.int32, (tokens,))
-    qn = _optional(q_norm, "q_norm", torch.float16, (cache.dim,))
-    kn = _optional(k_norm, "k_norm", torch.float16, (cache.dim,))
-    dev = _same_device(qkv, k_cache, v_cache, table, positions, q,
-                       *(t for t in (inv_freq, seq, q_norm, k_norm) if t is not None))
-    ld = qkv.stride(0) if tokens > 1 else max(qkv.stride(0), columns + -columns % 4)
-    with torch.cuda.device(dev):
-        _check(_lib.q4g128_rope_append(qkv.data_ptr(), ld, tokens, heads, ctypes.byref(cache), seqp,
-                                       positions.data_ptr(), freq, rot, int(bool(interleaved)), mscale, qn, kn, eps,
-                                       q.data_ptr(), _stream(dev, stream)), "q4g128_rope_append")
-    return q
-
-
-def _attn_args(q, k_cache, v_cache, table, lengths, count, scale, softcap, window, slopes, prefix, max_length, out, stream):
-    """Checks shared by the two attention calls -> (cache, options, max_length, out, device)."""
-    cache = _cache(k_cache, v_cache, table)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [rows][heads][dim]")
-    rows, heads, _ = q.shape
-    _dev_tensor(q, "q", torch.float16, (rows, heads, cache.dim))
-    _dev_tensor(lengths, "lengths", torch.int32, (count,))
-    if count > cache.sequences:
-        raise ValueError(f"table has {cache.sequences} sequences, fewer than {count}")
-    options = AttnOptions(cache.dim ** -0.5 if scale is None else scale, softcap, window,
-                          _optional(slopes, "slopes", torch.float32, (heads,)),
-                          _optional(prefix, "prefix", torch.int32, (count,)))
-    if max_length is None:
-        max_length = cache.table_cols * cache.page
-    if out is None:
-        out = _empty(tuple(q.shape), torch.float16, q.device, stream)
-    _dev_tensor(out, "out", torch.float16, tuple(q.shape))
-    dev = _same_device(q, k_cache, v_cache, table, lengths, out, *(t for t in (slopes, prefix) if t is not None))
-    return cache, options, max_length, out, dev
-
-
-# The workspaces that the attention calls use when none is given: one per device
-# and stream (calls on one stream run one after the other), grown as needed,
-# with its counters zeroed once.
-_workspaces = {}
-
-
-def _workspace(workspace, need, dev, stream):
-    if need < 0:
-        raise Q4Error(need, "attention workspace")
-    if workspace is not None:
-        if workspace.device != dev:
-            raise ValueError("all tensors must be on the same GPU")
-        if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 vector")
-        return workspace
-    on = torch.cuda.current_stream(dev) if stream is None else stream
-    with torch.cuda.stream(on):
-        # A graph may be replayed on any stream: calls in a capture get memory of their own.
-        capturing = torch.cuda.is_current_stream_capturing()
-        got = None if capturing else _workspaces.get((dev.index, on.cuda_stream))
-        if got is None or got.numel() < need:
-            got = torch.empty((need,), dtype=torch.uint8, device=dev)
-            got[:ATTN_COUNTER_BYTES].zero_()
-            if not capturing:
-                _workspaces[dev.index, on.cuda_stream] = got
-    return got
+    return _on_stream(stream, lambda: _binding.rope_append(
+        qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq, q_norm, k_norm, eps, interleaved, mscale, q),
+        "q4g128_rope_append")
 
 
 def q4g128_attn_decode_workspace(batch, heads, dim) -> int:
@@ -470,18 +374,12 @@ def q4g128_attn_decode(q, k_cache, v_cache, table, lengths, scale=None, softcap=
     lengths int32 [B] counts the cached positions of sequence b (row b of table), the new one included.
     scale: dim ** -0.5 by default; softcap, window, slopes as in include/q4g128.h.  max_length: an upper bound on
     the lengths (default: what the table holds).  workspace: uint8 of q4g128_attn_decode_workspace bytes, its first
-    ATTN_COUNTER_BYTES zero before its first use (default: one that the binding keeps for the stream).
+    ATTN_COUNTER_BYTES zero before its first use (default: one that the binding keeps for the stream, or in a graph
+    capture one of the graph's own).
     """
-    cache, options, max_length, out, dev = _attn_args(q, k_cache, v_cache, table, lengths, q.shape[0], scale, softcap,
-                                                      window, slopes, None, max_length, out, stream)
-    b, heads, dim = q.shape
-    need = _lib.q4g128_attn_decode_workspace(b, heads, dim)
-    workspace = _workspace(workspace, need, dev, stream)
-    with torch.cuda.device(dev):
-        _check(_lib.q4g128_attn_decode(q.data_ptr(), ctypes.byref(cache), lengths.data_ptr(), max_length, b, heads,
-                                       ctypes.byref(options), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                       _stream(dev, stream)), "q4g128_attn_decode")
-    return out
+    return _on_stream(stream, lambda: _binding.attn_decode(
+        q, k_cache, v_cache, table, lengths, scale, softcap, window, slopes, max_length, out, workspace),
+        "q4g128_attn_decode")
 
 
 def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=None, softcap=0.0, window=0, slopes=None,
@@ -492,20 +390,9 @@ def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=Non
     positions (int32 [S]), these included.  prefix int32 [S]: positions below prefix[s] are seen by every token of
     the sequence (not together with a window).  Other arguments as q4g128_attn_decode.
     """
-    cache, options, max_length, out, dev = _attn_args(q, k_cache, v_cache, table, lengths, lengths.shape[0], scale,
-                                                      softcap, window, slopes, prefix, max_length, out, stream)
-    tokens, heads, dim = q.shape
-    count = lengths.shape[0]
-    _dev_tensor(q_starts, "q_starts", torch.int32, (count + 1,))
-    _same_device(q, q_starts)
-    need = _lib.q4g128_attn_prefill_workspace(tokens, count, heads, cache.kv_heads, dim, max_length)
-    workspace = _workspace(workspace, need, dev, stream)
-    with torch.cuda.device(dev):
-        _check(_lib.q4g128_attn_prefill(q.data_ptr(), ctypes.byref(cache), q_starts.data_ptr(), lengths.data_ptr(),
-                                        max_length, tokens, count, heads, ctypes.byref(options), out.data_ptr(),
-                                        workspace.data_ptr(), workspace.numel(), _stream(dev, stream)),
-               "q4g128_attn_prefill")
-    return out
+    return _on_stream(stream, lambda: _binding.attn_prefill(
+        q, k_cache, v_cache, table, q_starts, lengths, scale, softcap, window, slopes, prefix, max_length, out,
+        workspace), "q4g128_attn_prefill")
 
 
 def q4g128_status_string(status: int) -> str:

@@ -1,4 +1,5 @@
-"""Build libq4g128.so (the C-ABI library) in-tree with hipcc for gfx950.
+"""Build libq4g128.so (the C-ABI library) and the compiled part of the Python
+binding in-tree with hipcc for gfx950.
 
 Usage:  python int4_group_quantized_amd/build.py   (or call build_library()).
 Run it as a script, not as a module of the package: importing the package
@@ -29,6 +30,10 @@ DIAG_SOURCES = ["diag.hip"]
 
 SOURCES = ["api.cpp", "gemv.hip", "gemv_group.hip", "gemv_seg.hip", "prefill.hip", "prefill_split.hip", "prefill_pair.hip", "prefill_epilogue.hip", "pack.hip",
            "quantize.hip", "head_int8.hip", "rope_append.hip", "attn_decode.hip", "attn_prefill.hip"]
+# Python binding of the cache and attention calls: an extension module against
+# the torch and Python that run this script.
+BINDING_SOURCE = "binding.cpp"
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 ARCH = "gfx950"
 
 
@@ -92,14 +97,47 @@ def _link(objs, name: str, path: str, verbose: bool) -> None:
     os.replace(tmp, path)
 
 
+def _build_binding(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    include = os.path.join(root, "include")
+    obj = os.path.join(BUILD_DIR, BINDING_SOURCE + ".o")
+    _run([hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f"-I{INCLUDE}", "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"],
+          "-isystem", os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
+          "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj], BINDING_SOURCE, verbose)
+    tmp = BINDING_PATH + ".tmp"
+    _run([hipcc(), "-shared", "-fPIC", "-o", tmp, obj, f"-L{PKG_DIR}", "-lq4g128", f"-L{os.path.join(root, 'lib')}",
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"],
+         "the binding", verbose)
+    os.replace(tmp, BINDING_PATH)
+
+
+def _run(cmd, what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building {what} failed:\n{res.stdout}{res.stderr}")
+    if verbose and (res.stdout + res.stderr).strip():
+        print(res.stdout + res.stderr, flush=True)
+
+
 def build_library(verbose: bool = False) -> str:
-    """Compile and link libq4g128.so and the diagnostics library; returns the former's path."""
+    """Compile and link libq4g128.so, the diagnostics library and the binding; returns the first one's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = SOURCES + DIAG_SOURCES
     with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
     _link([objs[s] for s in SOURCES], LIB_NAME, LIB_PATH, verbose)
     _link([objs[s] for s in DIAG_SOURCES], DIAG_NAME, DIAG_PATH, verbose)
+    _build_binding(verbose)
     return LIB_PATH
 
 
