@@ -441,7 +441,10 @@ q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache, c
         (need > 0 && overlaps(workspace, (size_t)need, q_starts, sbytes)))
         return Q4_EINVAL;
     a.q_starts = q_starts;
-    hipError_t e = q4::launch_attn_prefill(a, (hipStream_t)stream);
+    q4::DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != Q4_OK) return s;
+    hipError_t e = q4::launch_attn_prefill(a, dev, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

@@ -64,6 +64,8 @@ struct AttnArgs {
     const int* prefix;     // or NULL
     int count;             // sequences
     int splits;            // parts that the positions are cut into
+    float inv_group;       // 1 / group
+    int images;            // tiles that fit into the launch's LDS, 2 to 4
 };
 
 // Widths the attention kernels are compiled for.
@@ -72,7 +74,7 @@ inline bool attn_dim_supported(int dim) { return dim == 64 || dim == 96 || dim =
 hipError_t launch_rope_append(const AppendArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t st);
 int64_t attn_decode_workspace(int64_t batch, int heads, int dim);
-hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t st);
+hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length);
 
 // The table's page for a position of sequence `row`, or -1 when the page is

@@ -72,13 +72,32 @@ struct PrefillTile {
     int len;    // positions of the sequence
 };
 
-// Tile number `item`; a sequence's last tokens, which see the most positions, come first.
+// Tile t of the `tiles` of sequence s, whose rows are first .. last - 1.  A
+// sequence's last tokens, which see the most positions, come first.
+__device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s, int first, int last, int tiles, int t) {
+    const int tb = prefill_tokens(a.group);
+    const int at = (tiles - 1 - t) * tb;
+    PrefillTile r;
+    r.s = s;
+    r.token = first + at;
+    r.n = min(tb, last - r.token);
+    r.len = min(max(a.lengths[s], 0), a.max_length);
+    r.pos = r.len - (last - first) + at;
+    return r;
+}
+
+// Tile number `item`.
 __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item) {
     const int lane = threadIdx.x & 63;
     const int tb = prefill_tokens(a.group);
-    PrefillTile r;
-    r.s = -1;
-    r.token = r.n = r.pos = r.len = 0;
+    PrefillTile none;
+    none.s = -1;
+    none.token = none.n = none.pos = none.len = 0;
+    if (a.count == 1) {
+        const int st = min(max(a.q_starts[0], 0), a.rows), en = min(max(a.q_starts[1], st), a.rows);
+        const int n = (en - st + tb - 1) / tb;
+        return item < n ? prefill_tile_of(a, 0, st, en, n, item) : none;
+    }
     int before = 0;
     for (int s0 = 0; s0 < a.count; s0 += 64) {
         int st = 0, en = 0;
@@ -87,27 +106,17 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
             en = min(max(a.q_starts[s0 + lane + 1], st), a.rows);
         }
         const int n = (en - st + tb - 1) / tb;
-        int upto = n;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(upto, d, 64);
-            if (lane >= d) upto += o;
-        }
-        const uint64_t hit = __ballot(n > 0 && item < before + upto && item >= before + upto - n);
+        const LaneScan c = lane_scan(n);
+        const uint64_t hit = __ballot(n > 0 && item < before + c.upto && item >= before + c.upto - n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
-            const int first = __builtin_amdgcn_readlane(st, l), last = __builtin_amdgcn_readlane(en, l);
             const int tiles = __builtin_amdgcn_readlane(n, l);
-            const int t = tiles - 1 - (item - (before + __builtin_amdgcn_readlane(upto, l) - tiles));
-            r.s = s0 + l;
-            r.token = first + t * tb;
-            r.n = min(tb, last - r.token);
-            r.len = min(max(a.lengths[r.s], 0), a.max_length);
-            r.pos = r.len - (last - first) + t * tb;
-            return r;
+            return prefill_tile_of(a, s0 + l, __builtin_amdgcn_readlane(st, l), __builtin_amdgcn_readlane(en, l), tiles,
+                                   item - (before + __builtin_amdgcn_readlane(c.upto, l) - tiles));
         }
-        before += __builtin_amdgcn_readlane(upto, 63);
+        before += c.last;
     }
-    return r;
+    return none;
 }
 
 // Chunk of 16 bytes (eight halves) c of K row `key`, and of V row `dim`, in a
@@ -135,26 +144,36 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
     return (((w & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
 }
 
-// Row r of a tile: the positions it sees are lo <= j < hi.  Rows that the tile
-// does not have are not live and see nothing.
+// Token `tok` of a tile sees positions lo <= j < hi.
+struct Seen {
+    int lo, hi;
+};
+__device__ __forceinline__ Seen prefill_sees(const AttnArgs& a, const PrefillTile& it, int prefix, int tok) {
+    const int pos = it.pos + tok;
+    if (tok >= it.n || pos < 0) return {0, 0};
+    return {a.window > 0 ? max(pos + 1 - a.window, 0) : 0, min(max(pos + 1, prefix), it.len)};
+}
+
+// Row r of a tile, r < 128.  Rows that the tile does not have are not live.
 struct PrefillRow {
-    int token, head, pos, lo, hi;
+    int token, head, pos;
+    Seen see;
     bool live;
 };
 
-__device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const PrefillTile& it, int kvh, int r) {
+// r / group: the quotient of r + 1/2 keeps 1 / 128 from every whole number.
+__device__ __forceinline__ int prefill_token_of(const AttnArgs& a, int r) {
+    return (int)(((float)r + 0.5f) * a.inv_group);
+}
+
+__device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const PrefillTile& it, int prefix, int kvh, int r) {
     PrefillRow q;
-    const int tok = r / a.group;
+    const int tok = prefill_token_of(a, r);
     q.live = tok < it.n;
     q.head = kvh * a.group + (q.live ? r - tok * a.group : 0);
     q.token = it.token + (q.live ? tok : 0);
     q.pos = it.pos + tok;
-    q.hi = q.lo = 0;
-    if (q.live && q.pos >= 0) {
-        const int prefix = a.prefix ? a.prefix[it.s] : 0;
-        q.hi = min(max(q.pos + 1, prefix), it.len);
-        q.lo = a.window > 0 ? max(q.pos + 1 - a.window, 0) : 0;
-    }
+    q.see = prefill_sees(a, it, prefix, tok);
     return q;
 }
 
@@ -166,10 +185,10 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // live, because the same handling inside that loop cost it 100 registers
 // (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
 template <int D, bool EXTRA>
-__device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int split,
-                                                                  int kvh, int wave, int k_begin, int k_end) {
+__device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
+                                                        int split, int kvh, int wave, int k_begin, int k_end) {
     const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
-    const PrefillRow q = prefill_row(a, it, kvh, wave * 32 + n);
+    const PrefillRow q = prefill_row(a, it, prefix, kvh, wave * 32 + n);
     const ScoreParams sp = score_params<EXTRA>(a, q.head);
     const _Float16* qp = reinterpret_cast<const _Float16*>(a.q) + ((size_t)q.token * a.heads + q.head) * D + d0;
     const int* row = a.c.table + (size_t)it.s * a.c.cols;
@@ -189,7 +208,7 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
 #pragma unroll 4
         for (int i = 0; i < D / 2; ++i) dot = __builtin_fmaf((float)qp[i], (float)kp[i], dot);
         dot += __shfl_xor(dot, 32, 64);
-        if (key < q.lo || key >= q.hi) continue;
+        if (key < q.see.lo || key >= q.see.hi) continue;
         const float s = score<EXTRA>(dot, sp, key - q.pos);
         const float m_new = fmaxf(m, s), base = m_new == Q4_NEG_INF ? 0.0f : m_new;
         const float f = exp2_hw(m - base), p = exp2_hw(s - base);
@@ -222,17 +241,28 @@ __device__ __forceinline__ float max_of(float a, float b) {
     return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
 }
 
-// 16 bytes per lane from memory into LDS: lane i's to base + 16 i.
-__device__ __forceinline__ void load_lds(const uint16_t* p, u4* base) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)p,
-                                     (__attribute__((address_space(3))) uint32_t*)base, 16, 0, 0);
+// 16 bytes per lane from memory into LDS: lane i's to base + 16 i.  In assembly
+// because the compiler, which sees that images follow each other in one array,
+// would let every LDS read wait for all such loads under way; the waits are
+// tile_ready's.  The instruction has no destination register.
+__device__ __forceinline__ void load_lds(const uint16_t* p, const u4* base) {
+    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u4*)base;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(p)
+                 : "memory", "m0");
 }
 
-__device__ __forceinline__ void images_ready() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-    __builtin_amdgcn_s_waitcnt(0);  // the loads into LDS count as vector memory operations
+// Waits until at most NEWER of this wave's vector memory operations (which
+// complete in order) and none of its LDS operations are under way, then for the
+// workgroup.
+template <int NEWER>
+__device__ __forceinline__ void wait_and_meet() {
+    static_assert(NEWER < 64, "the counter has six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((NEWER & 15) | 0x70 | (NEWER >> 4) << 14);
     __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    asm volatile("" ::: "memory");
 }
 
 template <int D, bool EXTRA>
@@ -241,31 +271,24 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     constexpr int C = D / 8;             // 16-byte chunks of a K row
     constexpr int STAGE = D / 32;        // chunks per thread and tile, for K and for V
     constexpr int IMAGE = 2 * kTileKeys * C;  // chunks of a tile's image
-    // Two images as two arrays: the compiler then knows that reads of one do not
-    // wait for the loads under way into the other.
-    __shared__ u4 image0[IMAGE], image1[IMAGE];
-    const int kvh = blockIdx.x % a.c.kv_heads;
-    const int rest = blockIdx.x / a.c.kv_heads;
-    const int split = splits == 1 ? 0 : rest % splits;
-    const PrefillTile it = prefill_tile(a, tile0 + (splits == 1 ? rest : rest / splits));
+    extern __shared__ u4 lds[];               // a.images of them, used in turn
+    const int kvh = blockIdx.x, split = blockIdx.y;
+    const PrefillTile it = prefill_tile(a, tile0 + blockIdx.z);
     if (it.s < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
 
-    const PrefillRow q = prefill_row(a, it, kvh, wave * 32 + n);
-    const int head = q.head, token = q.token, qpos = q.pos, hi = q.hi, lo = q.lo;
-    const bool live = q.live;
     const int prefix = a.prefix ? a.prefix[it.s] : 0;
-    // The wave's rows: all see [all_lo, all_hi), none sees from any_hi on.
-    int all_hi = live ? hi : 0x7FFFFFFF, any_hi = hi, all_lo = lo;
-    for (int d = 16; d >= 1; d >>= 1) {
-        all_hi = min(all_hi, __shfl_xor(all_hi, d, 64));
-        any_hi = max(any_hi, __shfl_xor(any_hi, d, 64));
-        all_lo = max(all_lo, __shfl_xor(all_lo, d, 64));
-    }
-    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
-    all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+    const PrefillRow q = prefill_row(a, it, prefix, kvh, wave * 32 + n);
+    const int head = q.head, token = q.token, qpos = q.pos, hi = q.see.hi, lo = q.see.lo;
+    const bool live = q.live;
+    // What a token sees starts and ends no earlier than what the one before it
+    // sees: all of the wave's rows see [all_lo, all_hi), none sees from any_hi on.
+    const int tok0 = __builtin_amdgcn_readfirstlane(prefill_token_of(a, wave * 32));
+    const int tok1 = min(__builtin_amdgcn_readfirstlane(prefill_token_of(a, wave * 32 + 31)), it.n - 1);
+    const int all_hi = prefill_sees(a, it, prefix, tok0).hi;
+    const Seen most = prefill_sees(a, it, prefix, tok1);
+    const int any_hi = tok0 < it.n ? most.hi : 0, all_lo = most.lo;
 
     // Tiles of the workgroup: the first token sees the lowest position, the last
     // (or the prefix) the highest.
@@ -338,22 +361,36 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = (f16v)0.0f;
     float m = Q4_NEG_INF, l = 0.0f;
+    int t_use = t_begin;
     const int km = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);  // key of this lane's K row
 
-    // One tile from image `im`, while the next one goes to `other`.
-    Pages pg = {};
-    int gone = 0;
+    const int ahead = a.images - 1;  // tiles requested ahead
+    // Bit i of pages.gone() for the tiles under way, four bits each, oldest first.
+    uint32_t gone_bits = 0;
     uint32_t bad = 0;  // nonzero: a tile with masked positions holds infinities or NaN
-    auto tile = [&](int t, u4* im, u4* other) {
-        const int kb = t * kTileKeys;
-        // This wave's loads and LDS reads are done; after the barrier everyone's:
-        // the image is complete, and the other one is free.
-        images_ready();
-        const int gone_next = t + 1 < t_end ? pg.gone() : 0;
-        if (t + 1 < t_end) {
-            load(t + 1, pg, other);
-            if (t + 2 < t_end) pg = pages_of(t + 2);
-        }
+    Pages pg = {};
+    if (t_begin < t_end) pg = pages_of(t_begin);
+    int t_load = t_begin, slot_load = 0;  // next tile to request, and its image
+    auto request = [&] {
+        gone_bits |= (uint32_t)pg.gone() << (4 * (t_load - t_use));
+        load(t_load, pg, lds + slot_load * IMAGE);
+        slot_load = slot_load == ahead ? 0 : slot_load + 1;
+        ++t_load;
+        if (t_load < t_end) pg = pages_of(t_load);
+    };
+    for (int i = 0; i < ahead && t_load < t_end; ++i) request();
+    int slot = 0;
+    for (; t_use < t_end; ++t_use, gone_bits >>= 4) {
+        const int kb = t_use * kTileKeys, gone = gone_bits & 15;
+        u4* im = lds + slot * IMAGE;
+        slot = slot == ahead ? 0 : slot + 1;
+        // This tile's loads are done (2 STAGE operations per newer tile may be
+        // under way), and everyone has read the image that the next request
+        // overwrites.
+        if (t_load - t_use == 3) wait_and_meet<4 * STAGE>();
+        else if (t_load - t_use == 2) wait_and_meet<2 * STAGE>();
+        else wait_and_meet<0>();
+        if (t_load < t_end) request();
         if (gone || kb + kTileKeys > it.len) {
             // Values past the end and of absent pages are cleared: their weight is
             // zero, but zero times what an unwritten slot holds may be NaN.
@@ -400,11 +437,24 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             // (scale > 0), and scale and maximum enter the exponent in one
             // multiply-add.
             if constexpr (EXTRA) {
+                if (a.softcap > 0.0f) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[b][i] = score<true>(s[b][i], sp, kb + 32 * b + 16 * (i >> 3) + 8 * h + (i & 7) - qpos);
+                        for (int i = 0; i < 16; ++i) s[b][i] = capped(s[b][i], sp);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[b][i] *= sp.scale2;
+                }
+                if (a.slopes) {
+                    const float bias = sp.slope2 * (float)(kb + 8 * h - qpos);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            s[b][i] += __builtin_fmaf(sp.slope2, (float)(32 * b + 16 * (i >> 3) + (i & 7)), bias);
                 }
             }
             if (masked) {
@@ -469,22 +519,9 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                 }
             }
         }
-        gone = gone_next;
-    };
-    if (t_begin < t_end) {
-        pg = pages_of(t_begin);
-        load(t_begin, pg, image0);
-        gone = pg.gone();
-        if (t_begin + 1 < t_end) pg = pages_of(t_begin + 1);
-        for (int t = t_begin;;) {
-            tile(t, image0, image1);
-            if (++t == t_end) break;
-            tile(t, image1, image0);
-            if (++t == t_end) break;
-        }
     }
     if (__any(bad != 0)) {
-        prefill_rows_one_by_one<D, EXTRA>(a, it, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
+        prefill_rows_one_by_one<D, EXTRA>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
     l += __shfl_xor(l, 32, 64);
@@ -535,35 +572,55 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits, a.out + r * D);
 }
 
-template <int D>
-static hipError_t launch_prefill_attn(AttnArgs a, hipStream_t st) {
+template <int D, bool EXTRA>
+static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
+    constexpr size_t image = 2 * kTileKeys * D * sizeof(uint16_t);
+    // Two workgroups per CU hide each other's waits where there are enough of them;
+    // fewer workgroups get as many images as a CU's LDS holds, up to four (three
+    // tiles ahead).
     const long tiles = prefill_tiles(a.rows, a.count, a.group);
-    a.splits = prefill_splits(a.rows, a.count, a.group, a.c.kv_heads, a.max_length);
-    const long per_tile = (long)a.c.kv_heads * a.splits;
-    const long most = ((1L << 24) - 1) / per_tile;  // tiles of one launch: at most 2^32 - 1 threads
-    const bool extra = a.softcap > 0.0f || a.slopes;
+    const size_t room = tiles * a.c.kv_heads * a.splits > dev.num_cu ? dev.max_lds / 2 : dev.max_lds;
+    const int fit = (int)(room / image);
+    a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
+    auto kernel = &attn_prefill_kernel<D, EXTRA>;
+    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, EXTRA>>::value[dev.device];
+    if (!ready.load(std::memory_order_acquire)) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
+        if (e != hipSuccess) return e;
+        ready.store(1, std::memory_order_release);
+    }
+    // Kv heads are next to each other, so that with a multiple of eight of them
+    // each XCD's L2 holds its own heads' keys and values.
+    const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
-        const dim3 grid((unsigned)((tiles - t < most ? tiles - t : most) * per_tile));
-        if (extra)
-            hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, dim3(kPrefillThreads), 0, st, a, (int)t);
-        else
-            hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, dim3(kPrefillThreads), 0, st, a, (int)t);
+        const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
+        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA>), grid, dim3(kPrefillThreads), a.images * image, st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.splits == 1) return hipSuccess;
+    return hipSuccess;
+}
+
+template <int D>
+static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
+    a.inv_group = 1.0f / (float)a.group;
+    a.splits = prefill_splits(a.rows, a.count, a.group, a.c.kv_heads, a.max_length);
+    const bool extra = a.softcap > 0.0f || a.slopes;
+    hipError_t e = extra ? launch_tiles<D, true>(a, dev, st) : launch_tiles<D, false>(a, dev, st);
+    if (e != hipSuccess || a.splits == 1) return e;
     const long rows = (long)a.rows * a.heads;
     hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
-hipError_t launch_attn_prefill(const AttnArgs& a, hipStream_t st) {
+hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st) {
     switch (a.c.dim) {
-        case 64: return launch_prefill_attn<64>(a, st);
-        case 96: return launch_prefill_attn<96>(a, st);
-        case 128: return launch_prefill_attn<128>(a, st);
-        case 192: return launch_prefill_attn<192>(a, st);
-        case 256: return launch_prefill_attn<256>(a, st);
+        case 64: return launch_prefill_attn<64>(a, dev, st);
+        case 96: return launch_prefill_attn<96>(a, dev, st);
+        case 128: return launch_prefill_attn<128>(a, dev, st);
+        case 192: return launch_prefill_attn<192>(a, dev, st);
+        case 256: return launch_prefill_attn<256>(a, dev, st);
     }
     return hipErrorInvalidValue;  // widths are validated before
 }

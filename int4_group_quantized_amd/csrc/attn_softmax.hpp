@@ -113,33 +113,37 @@ __device__ __forceinline__ void join_parts(const float* po, const float* ml, lon
     }
 }
 
-// A dot product as a base-2 score.  EXTRA: with the options' cap and bias;
-// tanh(x) = 1 - 2 / (e^(2x) + 1), absolute error about 2^-23, so the score's
-// is about softcap * 2^-23.
+// A dot product as a base-2 score: scale * log2(e) * dot, or with the options'
+// cap and bias.
 struct ScoreParams {
-    float scale2;     // scale * log2(e); EXTRA: unused
-    float scale;      // EXTRA: scale, or with a cap scale / softcap * 2 log2(e)
-    float softcap;
-    float slope;
+    float scale2;  // scale * log2(e)
+    float cap_in;  // 2 log2(e) * scale / softcap
+    float cap2;    // softcap * log2(e)
+    float slope2;  // slope * log2(e)
 };
 
 template <bool EXTRA>
 __device__ __forceinline__ ScoreParams score_params(const AttnArgs& a, int head) {
     ScoreParams p;
     p.scale2 = a.scale * kLog2e;
-    p.scale = a.softcap > 0.0f ? a.scale / a.softcap * (2.0f * kLog2e) : a.scale;
-    p.softcap = a.softcap;
-    p.slope = EXTRA && a.slopes ? a.slopes[head] : 0.0f;
+    p.cap_in = EXTRA ? 2.0f * kLog2e * a.scale / a.softcap : 0.0f;  // without a cap unused
+    p.cap2 = a.softcap * kLog2e;
+    p.slope2 = EXTRA && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
     return p;
+}
+
+// softcap tanh(scale dot / softcap) log2(e), from tanh(x) = 1 - 2 / (e^(2x) + 1):
+// its absolute error is about 2^-23, so the score's is about softcap * 2^-23.
+__device__ __forceinline__ float capped(float dot, const ScoreParams& p) {
+    return __builtin_fmaf(-2.0f * p.cap2, __builtin_amdgcn_rcpf(exp2_hw(dot * p.cap_in) + 1.0f), p.cap2);
 }
 
 // distance = key position - query position
 template <bool EXTRA>
 __device__ __forceinline__ float score(float dot, const ScoreParams& p, int distance) {
     if constexpr (!EXTRA) return dot * p.scale2;
-    float s = dot * p.scale;
-    if (p.softcap > 0.0f) s = p.softcap - p.softcap * 2.0f * __builtin_amdgcn_rcpf(exp2_hw(s) + 1.0f);
-    return (s + p.slope * (float)distance) * kLog2e;
+    const float s = p.cap2 > 0.0f ? capped(dot, p) : dot * p.scale2;
+    return __builtin_fmaf(p.slope2, (float)distance, s);
 }
 
 }  // namespace q4
