@@ -241,16 +241,26 @@ __device__ __forceinline__ float max_of(float a, float b) {
     return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
 }
 
-// 16 bytes per lane from memory into LDS: lane i's to base + 16 i.  In assembly
-// because the compiler, which sees that images follow each other in one array,
-// would let every LDS read wait for all such loads under way; the waits are
-// tile_ready's.  The instruction has no destination register.
-__device__ __forceinline__ void load_lds(const uint16_t* p, const u4* base) {
-    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u4*)base;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+// 16 bytes per lane from memory into LDS: lane i's to byte `to` + 16 i.  In
+// assembly because the compiler, which sees that images follow each other in
+// one array, would let every LDS read wait for all such loads under way; the
+// waits are wait_and_meet's.  The instruction has no destination register, and
+// nothing else in these kernels uses m0.
+// First form: from base + the lane's offset in bytes, base the same in all lanes.
+__device__ __forceinline__ void load_lds(const uint16_t* base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(p)
-                 : "memory", "m0");
+                 : "s"(to), "v"(offset), "s"(base)
+                 : "memory");
+}
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint16_t*)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ void load_lds(const uint16_t* p, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(p) : "memory");
 }
 
 // Waits until at most NEWER of this wave's vector memory operations (which
@@ -317,44 +327,81 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     // Pages of a tile's four quarters (16 positions each); positions past the end
     // take the last one's.  Uniform over the workgroup.
     struct Pages {
-        int p[4];
+        int p0, p1, p2, p3;
         __device__ int gone() const {  // bit i: quarter i has no page
-            return (p[0] < 0 ? 1 : 0) | (p[1] < 0 ? 2 : 0) | (p[2] < 0 ? 4 : 0) | (p[3] < 0 ? 8 : 0);
+            return (p0 < 0 ? 1 : 0) | (p1 < 0 ? 2 : 0) | (p2 < 0 ? 4 : 0) | (p3 < 0 ? 8 : 0);
         }
+        __device__ size_t of(int quarter) const {
+            const int even = quarter & 2 ? p2 : p0, odd = quarter & 2 ? p3 : p1;
+            return (size_t)max(quarter & 1 ? odd : even, 0);
+        }
+    };
+    // Table entries [ids_first, ids_first + 64), one per lane: an entry read when
+    // its tile is requested would wait for all tiles under way, because loads
+    // complete in order.
+    const int last_entry = max(it.len - 1, 0) >> a.c.shift;
+    int ids = -1, ids_first = -64;
+    auto page_at = [&](int pos) {
+        const int e = min(pos, it.len - 1) >> a.c.shift;
+        if (e >= ids_first + 64) {
+            ids_first = e;
+            ids = row[min(e + lane, last_entry)];
+            ids = (unsigned)ids < (unsigned)a.c.pages ? ids : -1;
+        }
+        return __builtin_amdgcn_readlane(ids, e - ids_first);
     };
     auto pages_of = [&](int t) {
         Pages r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r.p[i] = __builtin_amdgcn_readfirstlane(page_of(a.c, row, min(t * kTileKeys + 16 * i, it.len - 1)));
+        r.p0 = page_at(t * kTileKeys);
+        r.p1 = r.p2 = r.p3 = r.p0;
+        if (a.c.shift < 6) {
+            r.p1 = page_at(t * kTileKeys + 16);
+            r.p2 = page_at(t * kTileKeys + 32);
+            r.p3 = page_at(t * kTileKeys + 48);
+        }
         return r;
     };
     // A tile straight into an image, 16 bytes per lane: LDS takes a wave's lanes
-    // in order, so each lane fetches the chunk that the swizzle puts at its place.
-    auto load = [&](int t, const Pages& pg, u4* im) {
+    // in order, so each lane fetches the chunk that the swizzle puts at its place:
+    // of K, load j of thread tid is place x = 256 j + tid, row x / C; of V,
+    // dimension 32 j + tid / 8, whose swizzle is the same for all j.
+    const int v_c = v_chunk<D>(tid >> 3, tid & 7) & 7;
+    uint32_t k_at[STAGE];  // byte offset from the tile's first row
+#pragma unroll
+    for (int j = 0; j < STAGE; ++j) {
+        const int x = kPrefillThreads * j + tid, key = x / C;
+        k_at[j] = 2 * (key * D + 8 * (k_chunk<D>(key, x % C) - key * C));
+    }
+    const uint32_t v_at = 2 * (((uint32_t)(tid >> 3) << a.c.shift) + 8 * v_c);
+    const uint32_t lds_at =
+        __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u4*)lds + 1024 * wave);
+    auto load = [&](int t, const Pages& pg, int image) {
         const int kb = t * kTileKeys;
-        const uint16_t *kp[4], *vp[4];
+        const uint32_t to = lds_at + image * (IMAGE * 16);
+        if (a.c.shift >= 6) {  // the tile lies in one page
+            const int off = kb & pmask;
+            const size_t p = (size_t)max(pg.p0, 0);
+            const uint16_t* kp = uniform(a.c.k + p * a.c.k_stride + (((size_t)kvh << a.c.shift) + off) * D);
+            const uint16_t* vp = uniform(a.c.v + p * a.c.v_stride + ((size_t)(kvh * D) << a.c.shift) + off);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const size_t p = (size_t)max(pg.p[i], 0);
-            const int off = (kb + 16 * i) & pmask;
-            kp[i] = a.c.k + p * a.c.k_stride + (((size_t)kvh << a.c.shift) + off) * D;
-            vp[i] = a.c.v + p * a.c.v_stride + ((size_t)(kvh * D) << a.c.shift) + off;
+            for (int j = 0; j < STAGE; ++j) load_lds(kp, k_at[j], to + 4096 * j);
+#pragma unroll
+            for (int j = 0; j < STAGE; ++j)
+                load_lds(vp + ((size_t)(32 * j) << a.c.shift), v_at, to + kTileKeys * C * 16 + 4096 * j);
+        } else {
+            // Quarters of 16 positions, each in a page of its own or shared.
+            const size_t vpage = pg.of(v_c >> 1);
+            const uint16_t* vp = a.c.v + vpage * a.c.v_stride + ((size_t)(kvh * D + (tid >> 3)) << a.c.shift) +
+                                 ((kb + 8 * v_c) & pmask);
+#pragma unroll
+            for (int j = 0; j < STAGE; ++j) {
+                const int x = kPrefillThreads * j + tid, key = x / C;
+                load_lds(a.c.k + pg.of(key >> 4) * a.c.k_stride + (((size_t)kvh << a.c.shift) + ((kb + key) & pmask)) * D +
+                             8 * (k_chunk<D>(key, x % C) - key * C),
+                         to + 4096 * j);
+                load_lds(vp + ((size_t)(32 * j) << a.c.shift), to + kTileKeys * C * 16 + 4096 * j);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < STAGE; ++j) {
-            const int x = kPrefillThreads * j + tid;
-            const int key = x / C, c = k_chunk<D>(key, x % C) - key * C, quarter = key >> 4;
-            const uint16_t* k0 = quarter < 2 ? (quarter == 0 ? kp[0] : kp[1]) : (quarter == 2 ? kp[2] : kp[3]);
-            load_lds(k0 + (unsigned)((key & 15) * D + 8 * c), im + kPrefillThreads * j + 64 * wave);
-        }
-        // x = 256 j + tid: dimension 32 j + tid / 8, whose swizzle is the same for all j
-        const int vc = v_chunk<D>(tid >> 3, tid & 7) & 7;
-        const uint16_t* v0 = (vc < 4 ? (vc < 2 ? vp[0] : vp[1]) : (vc < 6 ? vp[2] : vp[3])) + 8 * (vc & 1);
-#pragma unroll
-        for (int j = 0; j < STAGE; ++j)
-            load_lds(v0 + ((unsigned)(32 * j + (tid >> 3)) << a.c.shift),
-                     im + kTileKeys * C + kPrefillThreads * j + 64 * wave);
     };
 
     f16v acc[D / 32];
@@ -373,7 +420,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     int t_load = t_begin, slot_load = 0;  // next tile to request, and its image
     auto request = [&] {
         gone_bits |= (uint32_t)pg.gone() << (4 * (t_load - t_use));
-        load(t_load, pg, lds + slot_load * IMAGE);
+        load(t_load, pg, slot_load);
         slot_load = slot_load == ahead ? 0 : slot_load + 1;
         ++t_load;
         if (t_load < t_end) pg = pages_of(t_load);
@@ -406,26 +453,25 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             lds_barrier();
         }
         if (kb < any_hi) {
-            // Operand reads run ahead of the products: half of K's, the rest of K's,
-            // half of V's before the softmax.
+            // Operand reads run ahead of the products: half of K's, and half of V's
+            // before the softmax.
             constexpr int KH = D / 32;  // of D / 16 steps
-            u4 kf[2][KH][2];
+            u4 kf[KH][2];
 #pragma unroll
             for (int d = 0; d < KH; ++d)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) kf[0][d][b] = im[k_chunk<D>(32 * b + km, 2 * d + h)];
-#pragma unroll
-            for (int d = 0; d < KH; ++d)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) kf[1][d][b] = im[k_chunk<D>(32 * b + km, 2 * (KH + d) + h)];
+                for (int b = 0; b < 2; ++b) kf[d][b] = im[k_chunk<D>(32 * b + km, 2 * d + h)];
             __builtin_amdgcn_sched_barrier(0);
             f16v s[2];
             s[0] = s[1] = (f16v)0.0f;
 #pragma unroll
-            for (int d = 0; d < 2 * KH; ++d)
+            for (int d = 0; d < 2 * KH; ++d) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(kf[d / KH][d % KH][b]), qf[d], s[b], 0, 0, 0);
+                for (int b = 0; b < 2; ++b) {
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(kf[d % KH][b]), qf[d], s[b], 0, 0, 0);
+                    if (d < KH) kf[d][b] = im[k_chunk<D>(32 * b + km, 2 * (KH + d) + h)];
+                }
+            }
             u4 vf[2][D / 32];
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) vf[0][d] = im[v_chunk<D>(32 * d + n, h)];
@@ -490,6 +536,8 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                 m = m_new;
             }
             const float base = m == Q4_NEG_INF ? 0.0f : m;
+            // The weights are summed as they enter the second product, rounded.
+            const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
             float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             h8 pf[4];
 #pragma unroll
@@ -497,10 +545,14 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float p = exp2_hw(EXTRA ? s[b][i] - base : __builtin_fmaf(s[b][i], sp.scale2, -base));
-                    sums[i & 3] += p;
                     pf[2 * b + (i >> 3)][i & 7] = (_Float16)p;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sums[e] = __builtin_amdgcn_fdot2((h2){pf[i][2 * e], pf[i][2 * e + 1]}, one, sums[e], false);
             l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             if (masked) {
                 // A weight of zero hides a masked value only if the value is finite.
