@@ -38,6 +38,7 @@ constexpr int kDecodeWaves = 4;
 constexpr int kDecodeThreads = 64 * kDecodeWaves;
 constexpr int kDecodeSlots = 512;   // workgroups wanted per launch: two per CU
 static_assert(kDecodeSlots <= kAttnCounters, "a counter for each sequence of several parts");
+constexpr int kDecodeGridY = 32768;  // parts per layer of the grid
 constexpr int kDecodeMinTiles = 4;  // tiles per part at least: one per wave
 
 // First visible tile and the number of tiles of sequence b.
@@ -59,8 +60,9 @@ struct DecodePart {
 // Tiles per part: the total over `target`, the parts wanted per kv head and row
 // block, rounded up, so that there are at most target + rows parts.
 __device__ __forceinline__ int decode_chunk(int64_t total, int target) {
-    int c = (int)((float)total / (float)target);  // within one of the quotient, up to 2^22 tiles per part
-    c = max(c - 1, kDecodeMinTiles);
+    const float quotient = (float)total / (float)target;
+    if (quotient > (float)(1 << 22)) return 1 << 26;  // more than any sequence has: one part each
+    int c = max((int)quotient - 1, kDecodeMinTiles);  // at most two below
     while ((int64_t)c * target < total) ++c;
     return c;
 }
@@ -157,11 +159,11 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
     // Kv heads and row blocks first, so that neighbouring workgroups read
     // neighbouring parts of the same pages at the same time.
     const int row_blocks = (a.group + 15) / 16;
-    const int pairs = a.c.kv_heads * row_blocks, pair = blockIdx.x % pairs;
+    const int pairs = gridDim.x, pair = blockIdx.x;
     const int kvh = row_blocks == 1 ? pair : pair / row_blocks;
     const int row0 = (pair - kvh * row_blocks) * 16;   // first head of the group in this workgroup
     const int nrows = min(16, a.group - row0);
-    const DecodePart it = decode_part(a, blockIdx.x / pairs, target);
+    const DecodePart it = decode_part(a, blockIdx.y + blockIdx.z * kDecodeGridY, target);
     if (it.b < 0) return;
     int first, len;
     const int tiles = decode_tiles(a, it.b, first, len);
@@ -377,12 +379,12 @@ static hipError_t launch_decode(const AttnArgs& a, hipStream_t st) {
     const long most = ((long)a.max_length + kTileKeys * kDecodeMinTiles - 1) / (kTileKeys * kDecodeMinTiles);
     const long grid = (long)target + a.rows < most * a.rows ? (long)target + a.rows : most * a.rows;
     const bool extra = a.softcap > 0.0f || a.slopes;
+    const dim3 blocks(pairs, (unsigned)(grid < kDecodeGridY ? grid : kDecodeGridY),
+                      (unsigned)((grid + kDecodeGridY - 1) / kDecodeGridY));
     if (extra)
-        hipLaunchKernelGGL((attn_decode_kernel<D, true>), dim3((unsigned)(grid * pairs)), dim3(kDecodeThreads), 0, st, a,
-                           target);
+        hipLaunchKernelGGL((attn_decode_kernel<D, true>), blocks, dim3(kDecodeThreads), 0, st, a, target);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<D, false>), dim3((unsigned)(grid * pairs)), dim3(kDecodeThreads), 0, st, a,
-                           target);
+        hipLaunchKernelGGL((attn_decode_kernel<D, false>), blocks, dim3(kDecodeThreads), 0, st, a, target);
     return hipGetLastError();
 }
 

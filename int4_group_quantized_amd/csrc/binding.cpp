@@ -220,8 +220,11 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 at::Tensor kept_workspace(int64_t need, const at::Device& d, hipStream_t stream) {
     static auto* kept = new std::map<std::pair<int, hipStream_t>, at::Tensor>;
     hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-    const bool capturing =
-        hipStreamIsCapturing(stream, &status) == hipSuccess && status != hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(stream, &status) != hipSuccess) {
+        (void)hipGetLastError();  // the null stream while another one is captured: not a capture itself
+        status = hipStreamCaptureStatusNone;
+    }
+    const bool capturing = status != hipStreamCaptureStatusNone;
     at::Tensor fresh;
     at::Tensor& t = capturing ? fresh : (*kept)[{d.index(), stream}];
     if (!t.defined() || t.numel() < need) {

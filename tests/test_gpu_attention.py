@@ -526,3 +526,145 @@ def test_step_in_a_graph(dev):
         torch.cuda.synchronize()
         for x, y in zip(got, (q, out, out2, k, v)):
             assert torch.equal(x, y), i
+
+
+# ---------------------------------------------------------------------------
+# the binding and the calls together
+# ---------------------------------------------------------------------------
+
+def test_pools_beyond_4_gb(dev):
+    """Page offsets of more than 2^32 bytes, in both directions of both pools."""
+    rng = np.random.default_rng(31)
+    heads, kv, dim, page, n = 4, 2, 64, 16, 40
+    stride = 3 << 30  # elements: page 1 starts 6 GB after page 0
+    small = Pool(rng, [n], kv, page, dim)
+    k_all = torch.empty(2 * stride + kv * page * dim, dtype=torch.float16, device=dev)
+    v_all = torch.empty(2 * stride + kv * page * dim, dtype=torch.float16, device=dev)
+    k = k_all.as_strided((3, kv, page, dim), (stride, page * dim, dim, 1))
+    v = v_all.as_strided((3, kv, dim, page), (stride, page * dim, page, 1))
+    order = [2, 0, 1]
+    for i, p in enumerate(small.table[0]):
+        k[order[i]] = torch.from_numpy(small.k[p]).to(dev)
+        v[order[i]] = torch.from_numpy(small.v[p]).to(dev)
+    table = i32([order], dev)
+    q = rng.standard_normal((1, heads, dim)).astype(np.float16)
+    qd = torch.from_numpy(q).to(dev)
+    for out in (q4.q4g128_attn_decode(qd, k, v, table, i32([n], dev), scale=0.1),
+                q4.q4g128_attn_prefill(qd, k, v, table, i32([0, 1], dev), i32([n], dev), scale=0.1)):
+        check_attention(out, q, small, [0, 1], [n], 0.1, "large pool")
+    qkv = torch.from_numpy(rng.standard_normal((n, (heads + 2 * kv) * dim)).astype(np.float32)).to(dev)
+    q4.q4g128_rope_append(qkv, k, v, table, i32(range(n), dev), None, heads, seq=i32([0] * n, dev))
+    for j in range(n):
+        row = qkv[j].half().view(-1, dim)
+        assert torch.equal(k[order[j // page], :, j % page], row[heads:heads + kv])
+        assert torch.equal(v[order[j // page], :, :, j % page], row[heads + kv:])
+
+
+def test_binding_refusals(dev):
+    f16, i = dict(dtype=torch.float16, device=dev), dict(dtype=torch.int32, device=dev)
+    k, v = torch.zeros(4, 2, 16, 64, **f16), torch.zeros(4, 2, 64, 16, **f16)
+    table, n = torch.zeros(3, 4, **i), torch.ones(3, **i)
+    q, qkv, pos = torch.zeros(3, 4, 64, **f16), torch.zeros(3, 512, device=dev), torch.zeros(3, **i)
+    starts = torch.arange(4, **i)
+
+    def append(**kw):
+        a = dict(qkv=qkv, k_cache=k, v_cache=v, table=table, positions=pos, inv_freq=None, heads=4)
+        a.update(kw)
+        return q4.q4g128_rope_append(**a)
+
+    def decode(**kw):
+        a = dict(q=q, k_cache=k, v_cache=v, table=table, lengths=n)
+        a.update(kw)
+        return q4.q4g128_attn_decode(**a)
+
+    def prefill(**kw):
+        a = dict(q=q, k_cache=k, v_cache=v, table=table, q_starts=starts, lengths=n)
+        a.update(kw)
+        return q4.q4g128_attn_prefill(**a)
+
+    append(), decode(), prefill()
+    for call in (append, decode, prefill):
+        for bad, error in ((dict(k_cache=k.float()), TypeError), (dict(v_cache=v.cpu()), ValueError),
+                           (dict(k_cache=k[0]), ValueError), (dict(v_cache=k), ValueError),
+                           (dict(k_cache=k.transpose(1, 2)), ValueError), (dict(table=table.long()), TypeError),
+                           (dict(table=table[0]), ValueError), (dict(table=table.t()), ValueError),
+                           (dict(table="table"), TypeError), (dict(k_cache=k[:0], v_cache=v[:0]), q4.Q4Error),
+                           (dict(k_cache=torch.zeros(4, 2, 16, 80, **f16), v_cache=torch.zeros(4, 2, 80, 16, **f16)),
+                            (ValueError, q4.Q4Error))):
+            with pytest.raises(error):
+                call(**bad)
+    for bad, error in ((dict(qkv=qkv.half()), TypeError), (dict(qkv=qkv[:, :511]), ValueError),
+                       (dict(qkv=qkv.t()), ValueError), (dict(qkv=qkv[0]), ValueError), (dict(heads=5), ValueError),
+                       (dict(heads=3), q4.Q4Error), (dict(heads=-1), ValueError), (dict(positions=pos[:2]), ValueError),
+                       (dict(inv_freq=torch.ones(3, device=dev)), q4.Q4Error),
+                       (dict(inv_freq=torch.ones(40, device=dev)), q4.Q4Error),
+                       (dict(inv_freq=torch.ones(2, 2, device=dev)), ValueError), (dict(q_norm=pos), TypeError),
+                       (dict(q_norm=torch.ones(32, **f16)), ValueError), (dict(seq=pos.long()), TypeError),
+                       (dict(eps=-1.0), q4.Q4Error), (dict(q=torch.zeros(3, 4, 32, **f16)), ValueError),
+                       (dict(qkv=qkv[:0], positions=pos[:0]), q4.Q4Error)):
+        with pytest.raises(error):
+            append(**bad)
+    for call in (decode, prefill):
+        for bad, error in ((dict(q=q.float()), TypeError), (dict(q=q[0]), ValueError), (dict(q=q[..., :32]), ValueError),
+                           (dict(lengths=n.long()), TypeError), (dict(scale=0.0), q4.Q4Error),
+                           (dict(softcap=-1.0), q4.Q4Error), (dict(window=-1), q4.Q4Error),
+                           (dict(slopes=torch.ones(3, device=dev)), ValueError), (dict(max_length=0), q4.Q4Error),
+                           (dict(max_length=65), q4.Q4Error), (dict(out=q), q4.Q4Error), (dict(out=n), TypeError),
+                           (dict(workspace=n), ValueError), (dict(softcap="1"), TypeError)):
+            with pytest.raises(error):
+                call(**bad)
+    with pytest.raises(q4.Q4Error):
+        decode(workspace=torch.zeros(64, dtype=torch.uint8, device=dev))
+    with pytest.raises(ValueError):
+        decode(lengths=n[:2])
+    with pytest.raises(ValueError):
+        prefill(q_starts=starts[:3])
+    with pytest.raises(q4.Q4Error):
+        prefill(prefix=n, window=3)
+    with pytest.raises(ValueError):
+        decode(q=torch.zeros(4, 4, 64, **f16), lengths=torch.ones(4, **i))  # more rows than the table
+    torch.cuda.synchronize()
+
+
+def test_calls_without_a_workspace_in_a_graph_and_on_streams(dev):
+    """The workspaces that the binding keeps: one per stream, a graph's own."""
+    rng = np.random.default_rng(32)
+    pool = Pool(rng, [3000, 1500], 2, 64, 128)
+    c = pool.on(dev)
+    q = torch.from_numpy(rng.standard_normal((2, 8, 128)).astype(np.float16)).to(dev)
+    n, starts = i32([3000, 1500], dev), i32([0, 1, 2], dev)
+
+    def both(stream=None):
+        return (q4.q4g128_attn_decode(q, *c, n, stream=stream), q4.q4g128_attn_prefill(q, *c, starts, n, stream=stream))
+
+    want = both()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [both(s) for s in streams for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both()
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        eager = both()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert all(torch.equal(a, b) for a, b in zip(eager, want))
+
+
+def test_example_decodes_what_the_prompt_path_gives(dev):
+    """Decoded tokens against the same tokens as a prompt.  Both paths round q, k, the weights and the
+    attention outputs to fp16 once, each up to 2^-11 of values about their rms, and the products carry
+    fp32 sums: within 16 such roundings of the outputs' rms."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_block.py")
+    spec = importlib.util.spec_from_file_location("attention_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(steps=5) < 16 * H
