@@ -453,30 +453,31 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             lds_barrier();
         }
         if (kb < any_hi) {
-            // Operand reads run ahead of the products: half of K's, and half of V's
-            // before the softmax.
-            constexpr int KH = D / 32;  // of D / 16 steps
-            u4 kf[KH][2];
+            // Operand reads run ahead of the products: KW steps of K, and VW of V before
+            // the softmax, as many as registers hold without spilling (a spilled
+            // register's reload would wait for the tiles under way).
+            constexpr int STEPS = D / 16, KW = STEPS / 2 < 4 ? STEPS / 2 : 4, VW = D <= 128 && !EXTRA ? 2 : 1;
+            u4 kf[KW][2];
 #pragma unroll
-            for (int d = 0; d < KH; ++d)
+            for (int d = 0; d < KW; ++d)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) kf[d][b] = im[k_chunk<D>(32 * b + km, 2 * d + h)];
             __builtin_amdgcn_sched_barrier(0);
             f16v s[2];
             s[0] = s[1] = (f16v)0.0f;
 #pragma unroll
-            for (int d = 0; d < 2 * KH; ++d) {
+            for (int d = 0; d < STEPS; ++d) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(kf[d % KH][b]), qf[d], s[b], 0, 0, 0);
-                    if (d < KH) kf[d][b] = im[k_chunk<D>(32 * b + km, 2 * (KH + d) + h)];
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(kf[d % KW][b]), qf[d], s[b], 0, 0, 0);
+                    if (d + KW < STEPS) kf[d % KW][b] = im[k_chunk<D>(32 * b + km, 2 * (d + KW) + h)];
                 }
             }
-            u4 vf[2][D / 32];
+            u4 vf[VW][D / 32];
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) vf[0][d] = im[v_chunk<D>(32 * d + n, h)];
+            for (int w = 0; w < VW; ++w)
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) vf[1][d] = im[v_chunk<D>(32 * d + n, 2 + h)];
+                for (int d = 0; d < D / 32; ++d) vf[w][d] = im[v_chunk<D>(32 * d + n, 2 * w + h)];
             __builtin_amdgcn_sched_barrier(0);
             const bool masked = gone || kb < all_lo || kb + kTileKeys > all_hi;
             // Without options the running maximum is that of the plain products
@@ -566,8 +567,8 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d) {
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(vf[kk & 1][d]), pf[kk], acc[d], 0, 0, 0);
-                    if (kk < 2) vf[kk][d] = im[v_chunk<D>(32 * d + n, 2 * (kk + 2) + h)];
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(vf[kk % VW][d]), pf[kk], acc[d], 0, 0, 0);
+                    if (kk + VW < 4) vf[kk % VW][d] = im[v_chunk<D>(32 * d + n, 2 * (kk + VW) + h)];
                 }
             }
         }
