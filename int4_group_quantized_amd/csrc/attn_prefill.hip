@@ -25,6 +25,8 @@
 // then cut into equal splits joined by a second launch.
 #include "attn_softmax.hpp"
 
+#include <cmath>
+
 namespace q4 {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
@@ -32,13 +34,8 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 constexpr int kPrefillWaves = 4;
 constexpr int kPrefillThreads = 64 * kPrefillWaves;
 constexpr int kPrefillRows = 32 * kPrefillWaves;
-constexpr int kPrefillBlocks = 512;     // workgroups below which the cache is split
-// Tiles per split at least (34 tokens on 8,000 positions: 4 tiles 20.7 us, 2
-// tiles 23.9, 8 tiles 25.1), and tiles below which the second launch costs more
-// than it saves (five prompts of up to 473 tokens: 23.4 us whole, 25.8 halved).
-constexpr int kPrefillMinTiles = 4;
-constexpr int kPrefillSplitTiles = 16;
-
+constexpr int kPrefillBlocks = 512;     // workgroups that splits make at most: two per CU
+constexpr double kSecondLaunch = 5.0;   // us, launch and join of short partial results
 // Tokens per workgroup.
 __host__ __device__ inline int prefill_tokens(int group) { return kPrefillRows / group; }
 
@@ -48,18 +45,30 @@ static long prefill_tiles(long tokens, long count, int group) {
     return a < tokens ? a : tokens;      // each tile has a token
 }
 
-static int prefill_splits(long tokens, long count, int group, int kv_heads, long max_length) {
-    const long blocks = prefill_tiles(tokens, count, group) * kv_heads;
+// Splits of the positions.  A workgroup alone on its CU takes a time c per tile
+// (1.1, 1.4 and 2.4 us at dim 64, 128 and 256); n splits of L tiles take
+// c L / n, the second launch and n times what writing and reading one partial
+// output per row costs (v, at about 4 TB/s): least at n = sqrt(c L / v), and
+// worth it where it saves more than the launch.  Measured, dim 128, 16 heads:
+// 34 tokens on 8,000 positions 20.7 us with 32 splits, 23.9 with 63, 25.1 with
+// 16; 300 tokens on 720 19.8 with 4, 22.1 with 8, 28.5 whole; 20 tokens on 740
+// 22.3 whole, 14.4 with 3, 12.0 with 6; 1,000 tokens 29.1 whole, 29.7 with 4.
+static int prefill_splits(long tokens, long count, int heads, int kv_heads, int dim, long max_length) {
+    const long blocks = prefill_tiles(tokens, count, heads / kv_heads) * kv_heads;
     const long length = (max_length + kTileKeys - 1) / kTileKeys;
-    if (length < kPrefillSplitTiles) return 1;
-    const long most = (length + kPrefillMinTiles - 1) / kPrefillMinTiles;
-    const long want = kPrefillBlocks / blocks;
-    const long n = want < most ? want : most;
-    return n > 1 ? (int)n : 1;
+    const long most = kPrefillBlocks / blocks < length ? kPrefillBlocks / blocks : length;
+    if (most < 2) return 1;
+    const double c = 0.6 + dim / 150.0, v = 8e-6 / 4.0 * (double)tokens * heads * dim;
+    long n = (long)(std::sqrt(c * (double)length / v) + 0.5);
+    n = n < 1 ? 1 : n > most ? most : n;
+    const long per = (length + n - 1) / n;
+    n = (length + per - 1) / per;  // as many as that many tiles each make
+    const double saved = c * (double)(length - per) - v * (double)n;
+    return saved > kSecondLaunch ? (int)n : 1;
 }
 
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length) {
-    const int splits = prefill_splits(tokens, count, heads / kv_heads, kv_heads, max_length);
+    const int splits = prefill_splits(tokens, count, heads, kv_heads, dim, max_length);
     // The counters of the decode call come first, so that both can share one.
     return splits == 1 ? 0 : ((int64_t)splits * tokens * heads * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
@@ -658,7 +667,7 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
 template <int D>
 static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     a.inv_group = 1.0f / (float)a.group;
-    a.splits = prefill_splits(a.rows, a.count, a.group, a.c.kv_heads, a.max_length);
+    a.splits = prefill_splits(a.rows, a.count, a.heads, a.c.kv_heads, D, a.max_length);
     const bool extra = a.softcap > 0.0f || a.slopes;
     hipError_t e = extra ? launch_tiles<D, true>(a, dev, st) : launch_tiles<D, false>(a, dev, st);
     if (e != hipSuccess || a.splits == 1) return e;
