@@ -39,7 +39,6 @@ constexpr int kDecodeThreads = 64 * kDecodeWaves;
 constexpr int kDecodeSlots = 512;   // workgroups wanted per launch: two per CU
 static_assert(kDecodeSlots <= kAttnCounters, "a counter for each sequence of several parts");
 constexpr int kDecodeGridY = 32768;  // parts per layer of the grid
-constexpr int kDecodeMinTiles = 4;  // tiles per part at least: one per wave
 
 // First visible tile and the number of tiles of sequence b.
 __device__ __forceinline__ int decode_tiles(const AttnArgs& a, int b, int& first, int& len) {
@@ -57,19 +56,29 @@ struct DecodePart {
     int chunk;    // tiles per part
 };
 
+__host__ __device__ constexpr int decode_least(int dim) { return dim <= 128 ? 2 : 1; }
+
 // Tiles per part: the total over `target`, the parts wanted per kv head and row
-// block, rounded up, so that there are at most target + rows parts.
-__device__ __forceinline__ int decode_chunk(int64_t total, int target) {
+// block, rounded up, so that there are at most target + rows parts; and at least
+// one tile per wave, except that where sequences average 3 to 32 tiles (above
+// dim 128, 64) and CUs are idle they are cut finer (least: 2, above dim 128 1),
+// which shortens the loads of a CU by more than the longer join costs: one
+// sequence of 2,000 positions 7.4 us with two tiles per part, 8.7 with four; 2,772
+// of dim 256 10.3 with one, 12.9 with four; eight of up to 300 7.4 and 8.9; but one
+// of 130 6.4 with two, 5.8 with four, one of 8,000 of dim 64 15.8 and 11.2.
+__device__ __forceinline__ int decode_chunk(int64_t total, int rows, int target, int least) {
+    if (total > target || total <= 4 || total < 3 * (int64_t)rows || total > 64 / least * (int64_t)rows)
+        least = kDecodeWaves;
     const float quotient = (float)total / (float)target;
     if (quotient > (float)(1 << 22)) return 1 << 26;  // more than any sequence has: one part each
-    int c = max((int)quotient - 1, kDecodeMinTiles);  // at most two below
+    int c = max((int)quotient - 1, least);            // at most two below
     while ((int64_t)c * target < total) ++c;
     return c;
 }
 
 // The part with number `item`; parts are numbered sequence by sequence.  Each
 // wave computes it for itself.
-__device__ __forceinline__ DecodePart decode_part(const AttnArgs& a, int item, int target) {
+__device__ __forceinline__ DecodePart decode_part(const AttnArgs& a, int item, int target, int least) {
     const int lane = threadIdx.x & 63;
     DecodePart r;
     r.b = -1;
@@ -77,7 +86,7 @@ __device__ __forceinline__ DecodePart decode_part(const AttnArgs& a, int item, i
     if (a.rows == 1) {
         int first, len;
         const int n = decode_tiles(a, 0, first, len);
-        r.chunk = decode_chunk(n, target);
+        r.chunk = decode_chunk(n, 1, target, least);
         r.parts = n > r.chunk ? (n + r.chunk - 1) / r.chunk : 1;
         r.part = item;
         if (item < r.parts) r.b = 0;
@@ -88,7 +97,7 @@ __device__ __forceinline__ DecodePart decode_part(const AttnArgs& a, int item, i
         int first, len;
         total += lane_scan(b0 + lane < a.rows ? decode_tiles(a, b0 + lane, first, len) : 0).last;
     }
-    r.chunk = decode_chunk(total, target);
+    r.chunk = decode_chunk(total, a.rows, target, least);
     int before = 0;  // parts of earlier sequences
     for (int b0 = 0; b0 < a.rows; b0 += 64) {
         int first, len, n = 0;
@@ -119,9 +128,9 @@ __host__ __device__ inline int decode_target(int pairs) {
 }
 
 // Counters of finished parts, then partial outputs [parts][heads][dim], their
-// maxima and sums [parts][heads][2].  A sequence of several parts has more than
-// total / target tiles, so there are fewer than `target` of them, and target
-// times the kv heads and row blocks is at most kDecodeSlots: the counters have
+// maxima and sums [parts][heads][2].  A sequence of several parts has at least
+// two tiles and more than total / target, so there are fewer than `target` of
+// them, and target times the kv heads and row blocks is at most kDecodeSlots: the counters have
 // one place whatever the shape, so calls of all shapes can share a workspace.
 struct DecodeWorkspace {
     float* o;
@@ -163,7 +172,7 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
     const int kvh = row_blocks == 1 ? pair : pair / row_blocks;
     const int row0 = (pair - kvh * row_blocks) * 16;   // first head of the group in this workgroup
     const int nrows = min(16, a.group - row0);
-    const DecodePart it = decode_part(a, blockIdx.y + blockIdx.z * kDecodeGridY, target);
+    const DecodePart it = decode_part(a, blockIdx.y + blockIdx.z * kDecodeGridY, target, decode_least(D));
     if (it.b < 0) return;
     int first, len;
     const int tiles = decode_tiles(a, it.b, first, len);
@@ -376,7 +385,7 @@ template <int D>
 static hipError_t launch_decode(const AttnArgs& a, hipStream_t st) {
     const int pairs = a.c.kv_heads * ((a.group + 15) / 16);
     const int target = decode_target(pairs);
-    const long most = ((long)a.max_length + kTileKeys * kDecodeMinTiles - 1) / (kTileKeys * kDecodeMinTiles);
+    const long most = ((long)a.max_length + kTileKeys * decode_least(D) - 1) / (kTileKeys * decode_least(D));
     const long grid = (long)target + a.rows < most * a.rows ? (long)target + a.rows : most * a.rows;
     const bool extra = a.softcap > 0.0f || a.slopes;
     const dim3 blocks(pairs, (unsigned)(grid < kDecodeGridY ? grid : kDecodeGridY),
