@@ -78,7 +78,7 @@ typedef int32_t q4_status;
 #define Q4G128_MAX_GROUP 64
 #define Q4G128_MAX_TOKENS 1048576
 #define Q4G128_MAX_SEQUENCES 65536
-#define Q4G128_ATTN_COUNTER_BYTES 2048
+#define Q4G128_ATTN_COUNTER_BYTES 4096
 
 /*
  * q4g128_pack -- two codes per byte.

@@ -31,7 +31,7 @@ MAX_K = 32768
 MAX_BATCH = 16
 INT8_MAX_K = 8192
 MAX_GROUPED = 65536
-ATTN_COUNTER_BYTES = 2048
+ATTN_COUNTER_BYTES = 4096
 
 
 class GemvDesc(ctypes.Structure):

@@ -11,7 +11,7 @@ namespace q4 {
 // Attention's kernels treat 64 positions as one tile.
 constexpr int kTileKeys = 64;
 // Counters at the start of an attention workspace.
-constexpr int kAttnCounters = 512;
+constexpr int kAttnCounters = 1024;
 
 struct KvCache {
     uint16_t* k;        // [pages][kv_heads][page][dim]

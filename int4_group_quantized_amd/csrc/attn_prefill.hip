@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     const int token = (int)(r / a.heads);
     if (token < a.q_starts[0] || token >= a.q_starts[a.count]) return;
     const float* part = a.workspace + kAttnCounters;
-    join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits, a.out + r * D);
+    store_joined(join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits), a.out + r * D);
 }
 
 template <int D, bool EXTRA>

@@ -55,21 +55,31 @@ __device__ __forceinline__ bool parts_done(int* counter, int parts) {
     return last != 0;
 }
 
-// One wave joins the parts of one query row in order and writes the row: part p
-// has its output at po + p * stride * D and (m, l) at ml + p * stride * 2.  Up
-// to kJoin parts at a time are requested together, lane p holding part p's
-// statistics; part after part waited for each time took 3.3 us for 8 parts.
-// AGENT: the parts come from workgroups of the same launch.
+// A query row over some of its positions, held by a wave: lane l has the pairs
+// of dimensions 2 (l + 64 i) of the unnormalised output; m and l in all lanes.
+template <int D>
+struct JoinedRow {
+    static constexpr int PER = (D + 127) / 128;
+    float2 o[PER];
+    float m, l;
+};
+
+// Joins the parts of a row in order: part p has its output at po + p * stride * D
+// and (m, l) at ml + p * stride * 2.  Up to kJoin parts at a time are requested
+// together, lane p holding part p's statistics; part after part waited for each
+// time took 3.3 us for 8 parts.  AGENT: the parts come from workgroups of the
+// same launch.
 constexpr int kJoin = 16;
 template <int D, bool AGENT>
-__device__ __forceinline__ void join_parts(const float* po, const float* ml, long stride, int parts, uint16_t* out) {
+__device__ __forceinline__ JoinedRow<D> join_parts(const float* po, const float* ml, long stride, int parts) {
     const int lane = threadIdx.x & 63;
     auto get = [](const float* p) { return AGENT ? share_load(p) : *reinterpret_cast<const float2*>(p); };
-    constexpr int PER = (D + 127) / 128;  // pairs of dimensions per lane
-    float2 o[PER];
+    constexpr int PER = JoinedRow<D>::PER;
+    JoinedRow<D> r;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = {0.0f, 0.0f};
-    float top = Q4_NEG_INF, sum = 0.0f;
+    for (int i = 0; i < PER; ++i) r.o[i] = {0.0f, 0.0f};
+    r.m = Q4_NEG_INF;
+    r.l = 0.0f;
     for (int p0 = 0; p0 < parts; p0 += kJoin) {
         float2 v[kJoin][PER];
         float2 st = {Q4_NEG_INF, 0.0f};
@@ -86,30 +96,36 @@ __device__ __forceinline__ void join_parts(const float* po, const float* ml, lon
         float t = st.x;
 #pragma unroll
         for (int d = kJoin / 2; d >= 1; d >>= 1) t = fmaxf(t, __shfl_xor(t, d, 64));
-        t = fmaxf(top, __shfl(t, 0, 64));
-        const float f0 = part_weight(top, t), w = part_weight(st.x, t);
+        t = fmaxf(r.m, __shfl(t, 0, 64));
+        const float f0 = part_weight(r.m, t), w = part_weight(st.x, t);
         float s1 = st.y * w;
 #pragma unroll
         for (int d = kJoin / 2; d >= 1; d >>= 1) s1 += __shfl_xor(s1, d, 64);
-        sum = sum * f0 + __shfl(s1, 0, 64);
-        top = t;
+        r.l = r.l * f0 + __shfl(s1, 0, 64);
+        r.m = t;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) o[i] = {o[i].x * f0, o[i].y * f0};
+        for (int i = 0; i < PER; ++i) r.o[i] = {r.o[i].x * f0, r.o[i].y * f0};
 #pragma unroll
         for (int p = 0; p < kJoin; ++p) {
             const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), p));
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                o[i].x += v[p][i].x * f;
-                o[i].y += v[p][i].y * f;
+                r.o[i].x += v[p][i].x * f;
+                r.o[i].y += v[p][i].y * f;
             }
         }
     }
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    return r;
+}
+
+template <int D>
+__device__ __forceinline__ void store_joined(const JoinedRow<D>& r, uint16_t* out) {
+    const float inv = r.l > 0.0f || r.l != r.l ? 1.0f / r.l : 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int d = 2 * (lane + 64 * i);
-        if (d < D) *reinterpret_cast<uint32_t*>(out + d) = as_u32((h2){(_Float16)(o[i].x * inv), (_Float16)(o[i].y * inv)});
+    for (int i = 0; i < JoinedRow<D>::PER; ++i) {
+        const int d = 2 * ((threadIdx.x & 63) + 64 * i);
+        if (d < D)
+            *reinterpret_cast<uint32_t*>(out + d) = as_u32((h2){(_Float16)(r.o[i].x * inv), (_Float16)(r.o[i].y * inv)});
     }
 }
 
