@@ -330,15 +330,10 @@ def q4g128_gemv_int8(q, scales, x, y=None, stream=None) -> torch.Tensor:
     return y
 
 
-def _on_stream(stream, call, name):
-    """call() on the given stream (None: the current one), its memory from that stream too."""
-    if stream is None:
-        got = call()
-    else:
-        with torch.cuda.stream(stream):
-            got = call()
+def _answer(got, where):
+    """The output tensor of a compiled call, or its status as an error."""
     if type(got) is int:
-        raise Q4Error(got, name)
+        raise Q4Error(got, where)
     return got
 
 
@@ -352,9 +347,12 @@ def q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads,
     slice of a larger pool.  positions int32 [T]; seq int32 [T] (None: token t is of sequence t).  inv_freq fp32
     [rot / 2] (None: no rotation).  q_norm, k_norm fp16 [dim] or None.
     """
-    return _on_stream(stream, lambda: _binding.rope_append(
-        qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq, q_norm, k_norm, eps, interleaved, mscale, q),
-        "q4g128_rope_append")
+    if stream is not None:
+        with torch.cuda.stream(stream):  # new memory is the stream's too
+            return q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq, q_norm, k_norm,
+                                      eps, interleaved, mscale, q)
+    return _answer(_binding.rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq, q_norm, k_norm,
+                                        eps, interleaved, mscale, q), "q4g128_rope_append")
 
 
 def q4g128_attn_decode_workspace(batch, heads, dim) -> int:
@@ -377,9 +375,12 @@ def q4g128_attn_decode(q, k_cache, v_cache, table, lengths, scale=None, softcap=
     ATTN_COUNTER_BYTES zero before its first use (default: one that the binding keeps for the stream, or in a graph
     capture one of the graph's own).
     """
-    return _on_stream(stream, lambda: _binding.attn_decode(
-        q, k_cache, v_cache, table, lengths, scale, softcap, window, slopes, max_length, out, workspace),
-        "q4g128_attn_decode")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_attn_decode(q, k_cache, v_cache, table, lengths, scale, softcap, window, slopes, max_length,
+                                      out, workspace)
+    return _answer(_binding.attn_decode(q, k_cache, v_cache, table, lengths, scale, softcap, window, slopes,
+                                        max_length, out, workspace), "q4g128_attn_decode")
 
 
 def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=None, softcap=0.0, window=0, slopes=None,
@@ -390,9 +391,12 @@ def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=Non
     positions (int32 [S]), these included.  prefix int32 [S]: positions below prefix[s] are seen by every token of
     the sequence (not together with a window).  Other arguments as q4g128_attn_decode.
     """
-    return _on_stream(stream, lambda: _binding.attn_prefill(
-        q, k_cache, v_cache, table, q_starts, lengths, scale, softcap, window, slopes, prefix, max_length, out,
-        workspace), "q4g128_attn_prefill")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale, softcap, window, slopes,
+                                       prefix, max_length, out, workspace)
+    return _answer(_binding.attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale, softcap, window, slopes,
+                                         prefix, max_length, out, workspace), "q4g128_attn_prefill")
 
 
 def q4g128_status_string(status: int) -> str:

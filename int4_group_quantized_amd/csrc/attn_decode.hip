@@ -21,7 +21,9 @@
 // while it computes (32 KB per wave, two waves per SIMD up to dim 128).  With
 // keys and values requested only when needed 64 sequences of 16,384 positions
 // (2.15 GB) took 499 us, with this 357 us (6.0 TB/s); its read-only twin, the
-// same loads without the arithmetic, takes 358 us.
+// same loads without the arithmetic, takes 358 us, a one-shot read of such a pool
+// runs at 7.0 TB/s.  One sequence of 2,000 positions takes 7.5 us, bound by the
+// chain of dependent loads (lengths, table, keys, parts).
 //
 // Split: the visible tiles of all sequences are cut into parts of one length,
 // computed on the device from the lengths so that uneven batches stay

@@ -5,7 +5,7 @@
 // Compiled, unlike the ctypes binding of the products, because these calls take
 // up to a dozen tensors and the kernels of a small step run for 3 to 9 us: the
 // same checks in Python and ctypes took 13 us more per call (one token appended:
-// 18.3 us a call with them, 5.5 us here).
+// 18.3 us a call with them, 5.2 us here).
 //
 // Every function takes its arguments by position (the Python wrappers give the
 // defaults) and returns the output tensor, or the library's status as an int
