@@ -56,13 +56,17 @@ typedef int32_t q4_status;
 
 #define Q4_OK 0
 /* NULL pointer, N <= 0, B outside [1, 16], M <= 0, or an output that
-   overlaps an input. */
+   overlaps an input; for the cache and attention calls also an option outside
+   its range or a workspace that is too small. */
 #define Q4_EINVAL (-1)
 /* K not a positive multiple of 128, K above 32768, or N / M above
-   Q4G128_MAX_N. */
+   Q4G128_MAX_N; for the cache and attention calls a size outside the limits
+   stated with them. */
 #define Q4_ESHAPE (-2)
 /* codes / packed / x / X / W not 16-byte aligned; scales / mins not 2-byte
-   aligned; y / Y not 4-byte aligned. */
+   aligned; y / Y not 4-byte aligned.  For the cache and attention calls: qkv, k,
+   v, q, out and workspace not 16-byte, q_norm / k_norm not 2-byte, other arrays
+   not 4-byte aligned. */
 #define Q4_EALIGN (-3)
 /* The HIP runtime reported an error while querying the device or launching;
    q4g128_last_hip_error() returns the hipError_t of the calling thread. */

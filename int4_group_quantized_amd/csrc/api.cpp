@@ -451,9 +451,9 @@ q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache, c
 const char* q4g128_status_string(q4_status status) {
     switch (status) {
         case Q4_OK: return "Q4_OK: success";
-        case Q4_EINVAL: return "Q4_EINVAL: null pointer, non-positive size, batch outside 1..16 or overlapping output";
-        case Q4_ESHAPE: return "Q4_ESHAPE: K must be a multiple of 128 in [128, 32768]; sizes must fit the kernels' index range";
-        case Q4_EALIGN: return "Q4_EALIGN: packed/codes/activations/float weights need 16-byte, scales/mins 2-byte, outputs 4-byte alignment";
+        case Q4_EINVAL: return "Q4_EINVAL: null pointer, non-positive size, batch outside 1..16, invalid option, short workspace or overlapping output";
+        case Q4_ESHAPE: return "Q4_ESHAPE: K must be a multiple of 128 in [128, 32768], a cache's dim, page and heads among the supported ones; sizes must fit the kernels' index range";
+        case Q4_EALIGN: return "Q4_EALIGN: packed/codes/activations/float weights, caches, queries and workspaces need 16-byte, scales/mins/norms 2-byte, other arrays 4-byte alignment";
         case Q4_EDEVICE: return "Q4_EDEVICE: the HIP runtime reported an error (see q4g128_last_hip_error)";
     }
     return "unknown q4g128 status";

@@ -286,6 +286,12 @@ def test_decode_long_and_split(dev):
     decode_case(dev, 1, [9001, 13, 5000, 0, 1], 2, 1, 64, 64)
 
 
+def test_decode_joined_in_groups(dev):
+    """Two sequences of more than 32 parts among short ones, two row blocks each; repeats find the counters at zero."""
+    first = decode_case(dev, 40, [20000, 3, 0, 9000], 17, 1, 64, 64)
+    assert torch.equal(first, decode_case(dev, 40, [20000, 3, 0, 9000], 17, 1, 64, 64))
+
+
 def test_decode_many_sequences(dev):
     rng = np.random.default_rng(2)
     decode_case(dev, 2, [int(n) for n in rng.integers(0, 40, 150)] + [3000], 2, 1, 64, 16)
