@@ -298,8 +298,14 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     constexpr int C = D / 8;             // 16-byte chunks of a K row
     constexpr int STAGE = D / 32;        // chunks per thread and tile, for K and for V
     constexpr int IMAGE = 2 * kTileKeys * C;  // chunks of a tile's image
-    extern __shared__ u4 lds[];               // a.images of them, used in turn
+    extern __shared__ u4 lds[];               // a.images of them, used in turn, and four flags
     const int kvh = blockIdx.x, split = blockIdx.y;
+    // One sequence's first table entries, requested before anything else is known.
+    int ids = -1, ids_first = -64;
+    if (a.count == 1) {
+        ids = a.c.table[min((int)(threadIdx.x & 63), a.c.cols - 1)];
+        ids_first = 0;
+    }
     const PrefillTile it = prefill_tile(a, tile0 + blockIdx.z);
     if (it.s < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -316,6 +322,9 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     const int all_hi = prefill_sees(a, it, prefix, tok0).hi;
     const Seen most = prefill_sees(a, it, prefix, tok1);
     const int any_hi = tok0 < it.n ? most.hi : 0, all_lo = most.lo;
+
+    // All of the workgroup's rows see [seen_lo, seen_hi).
+    const int seen_hi = prefill_sees(a, it, prefix, 0).hi, seen_lo = prefill_sees(a, it, prefix, it.n - 1).lo;
 
     // Tiles of the workgroup: the first token sees the lowest position, the last
     // (or the prefix) the highest.
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     // its tile is requested would wait for all tiles under way, because loads
     // complete in order.
     const int last_entry = max(it.len - 1, 0) >> a.c.shift;
-    int ids = -1, ids_first = -64;
+    ids = (unsigned)ids < (unsigned)a.c.pages ? ids : -1;
     auto page_at = [&](int pos) {
         const int e = min(pos, it.len - 1) >> a.c.shift;
         if (e >= ids_first + 64) {
@@ -469,6 +478,15 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             }
             lds_barrier();
         }
+        if (gone || kb < seen_lo || kb + kTileKeys > seen_hi) {
+            // Masked for some row.  A weight of zero hides a masked value only if the
+            // value is finite: each wave looks at a quarter of the values.
+#pragma unroll
+            for (int i = 0; i < D * (kTileKeys / 8); i += kPrefillThreads) {
+                const u4 v = im[kTileKeys * C + i + tid];
+                bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
+            }
+        }
         if (kb < any_hi) {
             // Operand reads run ahead of the products: KW steps of K, and VW of V before
             // the softmax, as many as registers hold without spilling (a spilled
@@ -522,14 +540,21 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                 }
             }
             if (masked) {
-                const int from = lo - kb - 8 * h, to = hi - kb - 8 * h;
+                // seen: lo <= key < hi, as one unsigned comparison
+                const int from = kb + 8 * h - lo;
+                const unsigned count = (unsigned)max(hi - lo, 0);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = 32 * b + 16 * (i >> 3) + (i & 7);
-                        const bool seen = key >= from && key < to && !((gone >> (2 * b + (i >> 3))) & 1);
-                        s[b][i] = seen ? s[b][i] : Q4_NEG_INF;
+                    for (int i = 0; i < 16; ++i)
+                        s[b][i] = (unsigned)(from + 32 * b + 16 * (i >> 3) + (i & 7)) < count ? s[b][i] : Q4_NEG_INF;
+                }
+                if (gone) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if ((gone >> (2 * b + (i >> 3))) & 1) s[b][i] = Q4_NEG_INF;
                     }
                 }
             }
@@ -572,14 +597,6 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                 for (int e = 0; e < 4; ++e)
                     sums[e] = __builtin_amdgcn_fdot2((h2){pf[i][2 * e], pf[i][2 * e + 1]}, one, sums[e], false);
             l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-            if (masked) {
-                // A weight of zero hides a masked value only if the value is finite.
-#pragma unroll 4
-                for (int i = lane; i < D * (kTileKeys / 8); i += 64) {
-                    const u4 v = im[kTileKeys * C + i];
-                    bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
-                }
-            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
@@ -590,7 +607,11 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             }
         }
     }
-    if (__any(bad != 0)) {
+    int* flags = reinterpret_cast<int*>(lds + a.images * IMAGE);  // one per wave, behind the images
+    const bool found = __any(bad != 0);
+    if (lane == 0) flags[wave] = found;
+    __syncthreads();
+    if (flags[0] | flags[1] | flags[2] | flags[3]) {
         prefill_rows_one_by_one<D, EXTRA>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
@@ -650,7 +671,7 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     // tiles ahead).
     const long tiles = prefill_tiles(a.rows, a.count, a.group);
     const size_t room = tiles * a.c.kv_heads * a.splits > dev.num_cu ? dev.max_lds / 2 : dev.max_lds;
-    const int fit = (int)(room / image);
+    const int fit = (int)((room - kPrefillWaves * sizeof(int)) / image);
     a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
     auto kernel = &attn_prefill_kernel<D, EXTRA>;
     std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, EXTRA>>::value[dev.device];
@@ -665,7 +686,8 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
-        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA>), grid, dim3(kPrefillThreads), a.images * image, st, a, (int)t);
+        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA>), grid, dim3(kPrefillThreads),
+                           a.images * image + kPrefillWaves * sizeof(int), st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
