@@ -4,7 +4,7 @@
 //   token t sees: causal, its own sequence only, optionally within a window or
 //   with a prefix that every token sees.
 //
-// A workgroup of four waves serves 128 query rows of one kv head: the tokens
+// A workgroup of four or eight waves serves 128 query rows of one kv head: the tokens
 // of one tile times the heads of the group (row = token * group + head), so
 // that every key and value read serves the whole group.  One pass over the
 // visible tiles of 64 positions keeps the running maximum and sum of the
@@ -18,30 +18,43 @@
 // each 16) as it stands when matrix row m of a 32-key block loads key
 // 16(m/16) + 8(m/4%2) + 4(m/8%2) + m%4: register r then is key 16(r/8) + 8h + r%8.
 //
+// Dimensions 192 and 256: one wave's outputs and queries of 32 rows take most of
+// the registers, so two waves share the rows (SHARE = 2, eight waves).  Each
+// takes half of a tile's keys in the first product and half of the output
+// dimensions in the second; between them the weights meet in LDS, with the
+// maximum they were taken from.  4,096 tokens of 16 heads of 256 (4 kv heads)
+// take 191 us, with one wave per SIMD 214; 3,044 tokens of five sequences, 8
+// heads on one kv head, with a distance bias, 48 and 85.  With fewer workgroups
+// than CUs the same was tried at dim 64 and 128: 5 to 15% slower.
+//
 // Bound by the matrix cores, the softmax's vector work and LDS reads together:
-// 8,192 tokens of 32 heads of 128 (8 kv heads, 550 GFLOP) take 596 us, 923
-// TFLOP/s, matrix cores busy 49% of the cycles; without either product, the
-// loads, the maximum or the exponentials it would be 2 to 15% less.  Few tokens
-// are bound by latency: 34 tokens take 8.3 us.
+// 8,192 tokens of 32 heads of 128 (8 kv heads, 550 GFLOP) take 614 us, 896
+// TFLOP/s; without either product, the loads, the maximum or the exponentials it
+// would be 2 to 15% less.  Few tokens are bound by latency: 34 tokens take 7.4 us.
 //
 // Tiles go straight from memory into LDS images, one ahead with two images (two
 // workgroups per CU) and up to three ahead with four (one per CU, where there are
-// not more); staged through registers the case above took 2,020 us.  LDS rows are
-// swizzled so that an operand load's rows fall on different banks (k_chunk).
+// not more); staged through registers the case above took 2,020 us.  A wave's
+// loads are spread over the first product, where a tile lies in one page: at
+// once they hold it up for 400 to 700 cycles (2 to 4% of a prompt's time).  LDS
+// rows are swizzled so that an operand load's rows fall on different banks
+// (k_chunk).
 //
 // Few tokens on a long cache leave most CUs idle, so the visible tiles are
 // then cut into equal splits joined by a second launch (prefill_splits).
 #include "attn_softmax.hpp"
 
 #include <cmath>
+#include <type_traits>
 
 namespace q4 {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kPrefillWaves = 4;
-constexpr int kPrefillThreads = 64 * kPrefillWaves;
-constexpr int kPrefillRows = 32 * kPrefillWaves;
+constexpr int kPrefillRows = 128;  // of a workgroup, 32 per wave or pair of waves
+// Waves that share 32 rows, and threads of a workgroup.
+__host__ __device__ constexpr int prefill_share(int dim) { return dim > 128 ? 2 : 1; }
+__host__ __device__ constexpr int prefill_threads(int dim) { return 2 * kPrefillRows * prefill_share(dim); }
 constexpr int kPrefillBlocks = 512;     // workgroups that splits make at most: two per CU
 constexpr double kSecondLaunch = 5.0;   // us, launch and join of short partial results
 // Tokens per workgroup.
@@ -197,22 +210,25 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // A wave's 32 rows over positions [k_begin, k_end), one position after the
 // other, never touching what a row does not see: for tiles that hold infinities
 // or NaN in masked places, where the matrix products would multiply them by
-// zero.  Lanes n and n + 32 share row n, half the dimensions each.  Far slower;
+// zero.  Lanes n and n + 32 share row n, half the dimensions each (waves that share
+// it split the output dimensions too).  Far slower;
 // the wave starts its rows again here, after the fast loop and with nothing of it
 // live, because the same handling inside that loop cost it 100 registers
 // (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
 template <int D, bool EXTRA>
 __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
                                                         int split, int kvh, int wave, int k_begin, int k_end) {
+    constexpr int SHARE = prefill_share(D), OUT = D / (2 * SHARE);  // output dimensions of a lane
     const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
-    const PrefillRow q = prefill_row(a, it, prefix, kvh, wave * 32 + n);
+    const int o0 = (2 * (wave % SHARE) + (lane >> 5)) * OUT;
+    const PrefillRow q = prefill_row(a, it, prefix, kvh, wave / SHARE * 32 + n);
     const ScoreParams sp = score_params<EXTRA>(a, q.head);
     const _Float16* qp = reinterpret_cast<const _Float16*>(a.q) + ((size_t)q.token * a.heads + q.head) * D + d0;
     const int* row = a.c.table + (size_t)it.s * a.c.cols;
     const int pmask = (1 << a.c.shift) - 1;
-    float acc[D / 2];
+    float acc[OUT];
 #pragma unroll
-    for (int i = 0; i < D / 2; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < OUT; ++i) acc[i] = 0.0f;
     float m = Q4_NEG_INF, l = 0.0f;
     for (int key = k_begin; key < min(k_end, it.len); ++key) {
         const int page = page_of(a.c, row, key);
@@ -220,7 +236,7 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
         const _Float16* kp = reinterpret_cast<const _Float16*>(a.c.k) + (size_t)page * a.c.k_stride +
                              (((size_t)kvh << a.c.shift) + (key & pmask)) * D + d0;
         const _Float16* vp = reinterpret_cast<const _Float16*>(a.c.v) + (size_t)page * a.c.v_stride +
-                             ((size_t)(kvh * D + d0) << a.c.shift) + (key & pmask);
+                             ((size_t)(kvh * D + o0) << a.c.shift) + (key & pmask);
         float dot = 0.0f;
 #pragma unroll 4
         for (int i = 0; i < D / 2; ++i) dot = __builtin_fmaf((float)qp[i], (float)kp[i], dot);
@@ -232,20 +248,20 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
         l = l * f + p;
         m = m_new;
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i) acc[i] = acc[i] * f + p * (float)vp[(size_t)i << a.c.shift];
+        for (int i = 0; i < OUT; ++i) acc[i] = acc[i] * f + p * (float)vp[(size_t)i << a.c.shift];
     }
     if (!q.live) return;
     const long at = ((long)split * a.rows + q.token) * a.heads + q.head;
-    float* po = a.workspace + kAttnCounters + at * D + d0;
-    _Float16* op = reinterpret_cast<_Float16*>(a.out) + ((size_t)q.token * a.heads + q.head) * D + d0;
+    float* po = a.workspace + kAttnCounters + at * D + o0;
+    _Float16* op = reinterpret_cast<_Float16*>(a.out) + ((size_t)q.token * a.heads + q.head) * D + o0;
     const bool partial = a.splits > 1;
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
-    for (int i = 0; i < D / 2; ++i) {
+    for (int i = 0; i < OUT; ++i) {
         if (partial) po[i] = acc[i];
         else op[i] = (_Float16)(acc[i] * inv);
     }
-    if (partial && d0 == 0) {
+    if (partial && o0 == 0) {
         float* ml = a.workspace + kAttnCounters + (long)a.splits * a.rows * a.heads * D + at * 2;
         ml[0] = m;
         ml[1] = l;
@@ -292,13 +308,33 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("" ::: "memory");
 }
 
+// LDS of a workgroup behind its images.
+template <int SHARE>
+struct PrefillShared {
+    static constexpr int WAVES = 4 * SHARE;
+    u4 weights[SHARE > 1 ? WAVES : 0][2][64];  // a wave's half of a tile's weights, as operands
+    float base[SHARE > 1 ? WAVES : 0][32];     // and the maximum that they were taken from
+    float sum[SHARE > 1 ? WAVES : 0][32];      // a wave's share of the rows' sums
+    int found[WAVES];                          // a wave has seen infinities or NaN where a row is masked
+};
+
+// The same for LDS operations only.
+__device__ __forceinline__ void lds_meet() {
+    asm volatile("" ::: "memory");
+    lds_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <int D, bool EXTRA>
-__global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefill_kernel(AttnArgs a, int tile0) {
+__global__ void __launch_bounds__(prefill_threads(D), 2) attn_prefill_kernel(AttnArgs a, int tile0) {
+    constexpr int SHARE = prefill_share(D), THREADS = prefill_threads(D);
+    constexpr int KEYS = 2 / SHARE;        // blocks of 32 keys of a wave
+    constexpr int DIMS = D / (32 * SHARE);  // and of 32 output dimensions
     const int splits = a.splits;
     constexpr int C = D / 8;             // 16-byte chunks of a K row
-    constexpr int STAGE = D / 32;        // chunks per thread and tile, for K and for V
+    constexpr int STAGE = kTileKeys * C / THREADS;  // chunks per thread and tile, for K and for V
     constexpr int IMAGE = 2 * kTileKeys * C;  // chunks of a tile's image
-    extern __shared__ u4 lds[];               // a.images of them, used in turn, and four flags
+    extern __shared__ u4 lds[];               // a.images of them, used in turn, and PrefillShared
     const int kvh = blockIdx.x, split = blockIdx.y;
     // One sequence's first table entries, requested before anything else is known.
     int ids = -1, ids_first = -64;
@@ -310,15 +346,17 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     if (it.s < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
+    const int part = wave % SHARE, rows0 = wave / SHARE * 32;
+    PrefillShared<SHARE>& shared = *reinterpret_cast<PrefillShared<SHARE>*>(lds + a.images * IMAGE);
 
     const int prefix = a.prefix ? a.prefix[it.s] : 0;
-    const PrefillRow q = prefill_row(a, it, prefix, kvh, wave * 32 + n);
+    const PrefillRow q = prefill_row(a, it, prefix, kvh, rows0 + n);
     const int head = q.head, token = q.token, qpos = q.pos, hi = q.see.hi, lo = q.see.lo;
     const bool live = q.live;
     // What a token sees starts and ends no earlier than what the one before it
     // sees: all of the wave's rows see [all_lo, all_hi), none sees from any_hi on.
-    const int tok0 = __builtin_amdgcn_readfirstlane(prefill_token_of(a, wave * 32));
-    const int tok1 = min(__builtin_amdgcn_readfirstlane(prefill_token_of(a, wave * 32 + 31)), it.n - 1);
+    const int tok0 = __builtin_amdgcn_readfirstlane(prefill_token_of(a, rows0));
+    const int tok1 = min(__builtin_amdgcn_readfirstlane(prefill_token_of(a, rows0 + 31)), it.n - 1);
     const int all_hi = prefill_sees(a, it, prefix, tok0).hi;
     const Seen most = prefill_sees(a, it, prefix, tok1);
     const int any_hi = tok0 < it.n ? most.hi : 0, all_lo = most.lo;
@@ -389,31 +427,43 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     };
     // A tile straight into an image, 16 bytes per lane: LDS takes a wave's lanes
     // in order, so each lane fetches the chunk that the swizzle puts at its place:
-    // of K, load j of thread tid is place x = 256 j + tid, row x / C; of V,
-    // dimension 32 j + tid / 8, whose swizzle is the same for all j.
+    // of K, load j of thread tid is place x = THREADS j + tid, row x / C; of V,
+    // dimension THREADS / 8 j + tid / 8, whose swizzle is the same for all j.
     const int v_c = v_chunk<D>(tid >> 3, tid & 7) & 7;
     uint32_t k_at[STAGE];  // byte offset from the tile's first row
 #pragma unroll
     for (int j = 0; j < STAGE; ++j) {
-        const int x = kPrefillThreads * j + tid, key = x / C;
+        const int x = THREADS * j + tid, key = x / C;
         k_at[j] = 2 * (key * D + 8 * (k_chunk<D>(key, x % C) - key * C));
     }
     const uint32_t v_at = 2 * (((uint32_t)(tid >> 3) << a.c.shift) + 8 * v_c);
     const uint32_t lds_at =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u4*)lds + 1024 * wave);
+    // A tile within one page.
+    struct Whole {
+        const uint16_t *k, *v;
+        uint32_t to;
+    };
+    auto whole = [&](int t, const Pages& pg, int image) {
+        const int off = (t * kTileKeys) & pmask;
+        const size_t p = (size_t)max(pg.p0, 0);
+        Whole w;
+        w.k = uniform(a.c.k + p * a.c.k_stride + (((size_t)kvh << a.c.shift) + off) * D);
+        w.v = uniform(a.c.v + p * a.c.v_stride + ((size_t)(kvh * D) << a.c.shift) + off);
+        w.to = lds_at + image * (IMAGE * 16);
+        return w;
+    };
+    auto load_piece = [&](const Whole& w, int j) {  // 0 <= j < 2 STAGE
+        if (j < STAGE) load_lds(w.k, k_at[j], w.to + 16 * THREADS * j);
+        else load_lds(w.v + ((size_t)(THREADS / 8 * (j - STAGE)) << a.c.shift), v_at, w.to + 16 * THREADS * j);
+    };
     auto load = [&](int t, const Pages& pg, int image) {
         const int kb = t * kTileKeys;
         const uint32_t to = lds_at + image * (IMAGE * 16);
-        if (a.c.shift >= 6) {  // the tile lies in one page
-            const int off = kb & pmask;
-            const size_t p = (size_t)max(pg.p0, 0);
-            const uint16_t* kp = uniform(a.c.k + p * a.c.k_stride + (((size_t)kvh << a.c.shift) + off) * D);
-            const uint16_t* vp = uniform(a.c.v + p * a.c.v_stride + ((size_t)(kvh * D) << a.c.shift) + off);
+        if (a.c.shift >= 6) {
+            const Whole w = whole(t, pg, image);
 #pragma unroll
-            for (int j = 0; j < STAGE; ++j) load_lds(kp, k_at[j], to + 4096 * j);
-#pragma unroll
-            for (int j = 0; j < STAGE; ++j)
-                load_lds(vp + ((size_t)(32 * j) << a.c.shift), v_at, to + kTileKeys * C * 16 + 4096 * j);
+            for (int j = 0; j < 2 * STAGE; ++j) load_piece(w, j);
         } else {
             // Quarters of 16 positions, each in a page of its own or shared.
             const size_t vpage = pg.of(v_c >> 1);
@@ -421,21 +471,23 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                                  ((kb + 8 * v_c) & pmask);
 #pragma unroll
             for (int j = 0; j < STAGE; ++j) {
-                const int x = kPrefillThreads * j + tid, key = x / C;
+                const int x = THREADS * j + tid, key = x / C;
                 load_lds(a.c.k + pg.of(key >> 4) * a.c.k_stride + (((size_t)kvh << a.c.shift) + ((kb + key) & pmask)) * D +
                              8 * (k_chunk<D>(key, x % C) - key * C),
-                         to + 4096 * j);
-                load_lds(vp + ((size_t)(32 * j) << a.c.shift), to + kTileKeys * C * 16 + 4096 * j);
+                         to + 16 * THREADS * j);
+                load_lds(vp + ((size_t)(THREADS / 8 * j) << a.c.shift), to + kTileKeys * C * 16 + 16 * THREADS * j);
             }
         }
     };
 
-    f16v acc[D / 32];
+    f16v acc[DIMS];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = (f16v)0.0f;
+    for (int i = 0; i < DIMS; ++i) acc[i] = (f16v)0.0f;
     float m = Q4_NEG_INF, l = 0.0f;
     int t_use = t_begin;
-    const int km = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);  // key of this lane's K row
+    // Key of this lane's K row, in its wave's blocks.
+    const int km = 32 * KEYS * part + 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+    const int dm = 32 * DIMS * part + n;  // first dimension of this lane's V rows
 
     const int ahead = a.images - 1;  // tiles requested ahead
     // Bit i of pages.gone() for the tiles under way, four bits each, oldest first.
@@ -444,16 +496,29 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
     Pages pg = {};
     if (t_begin < t_end) pg = pages_of(t_begin);
     int t_load = t_begin, slot_load = 0;  // next tile to request, and its image
-    auto request = [&] {
+    auto requested = [&] {
         gone_bits |= (uint32_t)pg.gone() << (4 * (t_load - t_use));
-        load(t_load, pg, slot_load);
         slot_load = slot_load == ahead ? 0 : slot_load + 1;
         ++t_load;
         if (t_load < t_end) pg = pages_of(t_load);
     };
+    auto request = [&] {
+        load(t_load, pg, slot_load);
+        requested();
+    };
     for (int i = 0; i < ahead && t_load < t_end; ++i) request();
+    auto follow = [&](float m_new) {
+        const float f = part_weight(m, m_new);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DIMS; ++d) acc[d] *= f;
+        m = m_new;
+    };
     int slot = 0;
-    for (; t_use < t_end; ++t_use, gone_bits >>= 4) {
+    // SPREAD: another tile, in one page, is requested piece by piece during the
+    // first product.  At once its loads hold the wave up for a time each.
+    auto tile = [&](auto spread) {
+        constexpr bool SPREAD = decltype(spread)::value;
         const int kb = t_use * kTileKeys, gone = gone_bits & 15;
         u4* im = lds + slot * IMAGE;
         slot = slot == ahead ? 0 : slot + 1;
@@ -463,11 +528,17 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
         if (t_load - t_use == 3) wait_and_meet<4 * STAGE>();
         else if (t_load - t_use == 2) wait_and_meet<2 * STAGE>();
         else wait_and_meet<0>();
-        if (t_load < t_end) request();
+        Whole next;
+        if constexpr (SPREAD) {
+            next = whole(t_load, pg, slot_load);
+            requested();
+        } else {
+            if (t_load < t_end) request();
+        }
         if (gone || kb + kTileKeys > it.len) {
             // Values past the end and of absent pages are cleared: their weight is
             // zero, but zero times what an unwritten slot holds may be NaN.
-            for (int i = tid; i < D * (kTileKeys / 8); i += kPrefillThreads) {
+            for (int i = tid; i < D * (kTileKeys / 8); i += THREADS) {
                 const int dim = i >> 3, vc = i & 7;
                 const int keep = (gone >> (vc >> 1)) & 1 ? 0 : min(max(it.len - (kb + 8 * vc), 0), 8);
                 u4 mask;
@@ -476,44 +547,60 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                     mask[e] = (2 * e < keep ? 0x0000FFFFu : 0u) | (2 * e + 1 < keep ? 0xFFFF0000u : 0u);
                 im[v_chunk<D>(dim, vc)] &= mask;
             }
-            lds_barrier();
+            lds_meet();
         }
         if (gone || kb < seen_lo || kb + kTileKeys > seen_hi) {
             // Masked for some row.  A weight of zero hides a masked value only if the
-            // value is finite: each wave looks at a quarter of the values.
+            // value is finite: each wave looks at its share of the values.
 #pragma unroll
-            for (int i = 0; i < D * (kTileKeys / 8); i += kPrefillThreads) {
+            for (int i = 0; i < D * (kTileKeys / 8); i += THREADS) {
                 const u4 v = im[kTileKeys * C + i + tid];
                 bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
             }
         }
-        if (kb < any_hi) {
+        if (kb >= any_hi) {
+            if constexpr (SPREAD) {
+#pragma unroll
+                for (int j = 0; j < 2 * STAGE; ++j) load_piece(next, j);
+            }
+            if constexpr (SHARE > 1) lds_meet();
+        } else {
             // Operand reads run ahead of the products: KW steps of K, and VW of V before
             // the softmax, as many as registers hold without spilling (a spilled
             // register's reload would wait for the tiles under way).
-            constexpr int STEPS = D / 16, KW = STEPS / 2 < 4 ? STEPS / 2 : 4, VW = D <= 128 && !EXTRA ? 2 : 1;
-            u4 kf[KW][2];
+            constexpr int STEPS = D / 16, KW = STEPS == 4 || (D > 192 && EXTRA) ? 2 : STEPS == 6 ? 3 : 4, VW = (SHARE > 1 ? D <= 192 : D <= 128 && !EXTRA) ? 2 : 1;
+            u4 kf[KW][KEYS];
 #pragma unroll
             for (int d = 0; d < KW; ++d)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) kf[d][b] = im[k_chunk<D>(32 * b + km, 2 * d + h)];
+                for (int b = 0; b < KEYS; ++b) kf[d][b] = im[k_chunk<D>(32 * b + km, 2 * d + h)];
             __builtin_amdgcn_sched_barrier(0);
-            f16v s[2];
-            s[0] = s[1] = (f16v)0.0f;
+            f16v s[KEYS];
+#pragma unroll
+            for (int b = 0; b < KEYS; ++b) s[b] = (f16v)0.0f;
 #pragma unroll
             for (int d = 0; d < STEPS; ++d) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < KEYS; ++b) {
                     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(kf[d % KW][b]), qf[d], s[b], 0, 0, 0);
                     if (d + KW < STEPS) kf[d % KW][b] = im[k_chunk<D>(32 * b + km, 2 * (d + KW) + h)];
                 }
+                if constexpr (SPREAD) {
+                    if (d % SHARE == 0) load_piece(next, d / SHARE);
+                }
             }
-            u4 vf[VW][D / 32];
+            // V operands in the order of use: the wave's own keys first.
+            const auto v_of = [&](int d, int kk) {
+                const int c = SHARE == 1 ? 2 * kk + h : 4 * (part ^ (kk >> 1)) + 2 * (kk & 1) + h;
+                return im[v_chunk<D>(32 * d + dm, c)];
+            };
+            u4 vf[VW][DIMS];
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d) vf[w][d] = im[v_chunk<D>(32 * d + n, 2 * w + h)];
+                for (int d = 0; d < DIMS; ++d) vf[w][d] = v_of(d, w);
             __builtin_amdgcn_sched_barrier(0);
+            const int kw = kb + 32 * KEYS * part;  // first position of the wave's blocks
             const bool masked = gone || kb < all_lo || kb + kTileKeys > all_hi;
             // Without options the running maximum is that of the plain products
             // (scale > 0), and scale and maximum enter the exponent in one
@@ -521,19 +608,19 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             if constexpr (EXTRA) {
                 if (a.softcap > 0.0f) {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < KEYS; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) s[b][i] = capped(s[b][i], sp);
                 } else {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < KEYS; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) s[b][i] *= sp.scale2;
                 }
                 if (a.slopes) {
-                    const float bias = sp.slope2 * (float)(kb + 8 * h - qpos);
+                    const float bias = sp.slope2 * (float)(kw + 8 * h - qpos);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < KEYS; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             s[b][i] += __builtin_fmaf(sp.slope2, (float)(32 * b + 16 * (i >> 3) + (i & 7)), bias);
@@ -541,26 +628,26 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             }
             if (masked) {
                 // seen: lo <= key < hi, as one unsigned comparison
-                const int from = kb + 8 * h - lo;
+                const int from = kw + 8 * h - lo;
                 const unsigned count = (unsigned)max(hi - lo, 0);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < KEYS; ++b) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         s[b][i] = (unsigned)(from + 32 * b + 16 * (i >> 3) + (i & 7)) < count ? s[b][i] : Q4_NEG_INF;
                 }
                 if (gone) {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                    for (int b = 0; b < KEYS; ++b) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if ((gone >> (2 * b + (i >> 3))) & 1) s[b][i] = Q4_NEG_INF;
+                            if ((gone >> (2 * (KEYS * part + b) + (i >> 3))) & 1) s[b][i] = Q4_NEG_INF;
                     }
                 }
             }
             float tops[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) tops[i] = max_of(s[0][i], s[1][i]);
+            for (int i = 0; i < 16; ++i) tops[i] = KEYS > 1 ? max_of(s[0][i], s[KEYS - 1][i]) : s[0][i];
 #pragma unroll
             for (int w = 8; w >= 1; w >>= 1)
 #pragma unroll
@@ -571,20 +658,17 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
             // when it is more than 2^8 behind: weights then stay below 2^8, and the
             // outputs are rarely rescaled after the first tiles.
             if (__any(top > m + 8.0f)) {
-                const float m_new = fmaxf(m, top);
-                const float f = part_weight(m, m_new);
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d) acc[d] *= f;
-                m = m_new;
+                // A pair's two maxima meet after the weights are rounded: whole ones
+                // differ by a power of two, which changes no digit.
+                follow(fmaxf(m, SHARE > 1 ? ceilf(top) : top));
             }
             const float base = m == Q4_NEG_INF ? 0.0f : m;
             // The weights are summed as they enter the second product, rounded.
             const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
             float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            h8 pf[4];
+            h8 pf[2 * KEYS];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < KEYS; ++b) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float p = exp2_hw(EXTRA ? s[b][i] - base : __builtin_fmaf(s[b][i], sp.scale2, -base));
@@ -592,37 +676,68 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2 * KEYS; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     sums[e] = __builtin_amdgcn_fdot2((h2){pf[i][2 * e], pf[i][2 * e + 1]}, one, sums[e], false);
             l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+            if constexpr (SHARE > 1) {
+                shared.weights[wave][0][lane] = __builtin_bit_cast(u4, pf[0]);
+                shared.weights[wave][1][lane] = __builtin_bit_cast(u4, pf[1]);
+                if (h == 0) shared.base[wave][n] = m;
+            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
+                if constexpr (SHARE > 1) {
+                    if (kk == 2) {
+                        // The other wave's weights, brought to the higher maximum.
+                        lds_meet();
+                        const float theirs = shared.base[wave ^ 1][n];
+                        pf[0] = as_h8(shared.weights[wave ^ 1][0][lane]);
+                        pf[1] = as_h8(shared.weights[wave ^ 1][1][lane]);
+                        if (__any(theirs != m)) {
+                            follow(fmaxf(m, theirs));
+                            const _Float16 f = (_Float16)part_weight(theirs, m);
+                            pf[0] *= f;
+                            pf[1] *= f;
+                        }
+                    }
+                }
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d) {
-                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(vf[kk % VW][d]), pf[kk], acc[d], 0, 0, 0);
-                    if (kk + VW < 4) vf[kk % VW][d] = im[v_chunk<D>(32 * d + n, 2 * (kk + VW) + h)];
+                for (int d = 0; d < DIMS; ++d) {
+                    acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(vf[kk % VW][d]), pf[kk % (2 * KEYS)], acc[d], 0, 0, 0);
+                    if (kk + VW < 4) vf[kk % VW][d] = v_of(d, kk + VW);
                 }
             }
         }
-    }
-    int* flags = reinterpret_cast<int*>(lds + a.images * IMAGE);  // one per wave, behind the images
+        ++t_use;
+        gone_bits >>= 4;
+    };
+    if (a.c.shift >= 6)
+        while (t_load < t_end) tile(std::true_type{});
+    while (t_use < t_end) tile(std::false_type{});
+    l += __shfl_xor(l, 32, 64);
     const bool found = __any(bad != 0);
-    if (lane == 0) flags[wave] = found;
+    if (lane == 0) shared.found[wave] = found;
+    if constexpr (SHARE > 1) {
+        if (h == 0) shared.sum[wave][n] = l;
+    }
     __syncthreads();
-    if (flags[0] | flags[1] | flags[2] | flags[3]) {
+    int any_found = 0;
+#pragma unroll
+    for (int w = 0; w < 4 * SHARE; ++w) any_found |= shared.found[w];
+    if (any_found) {
         prefill_rows_one_by_one<D, EXTRA>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
-    l += __shfl_xor(l, 32, 64);
+    if constexpr (SHARE > 1) l += shared.sum[wave ^ 1][n];
 
     if (!live) return;
     if (splits == 1) {
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        uint16_t* op = a.out + ((size_t)token * a.heads + head) * D;
+        uint16_t* op = a.out + ((size_t)token * a.heads + head) * D + 32 * DIMS * part;
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
+        for (int d = 0; d < DIMS; ++d) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint2 w;
@@ -633,15 +748,15 @@ __global__ void __launch_bounds__(kPrefillThreads, D <= 128 ? 2 : 1) attn_prefil
         }
     } else {
         const long at = ((long)split * a.rows + token) * a.heads + head;
-        float* op = a.workspace + kAttnCounters + at * D;
+        float* op = a.workspace + kAttnCounters + at * D + 32 * DIMS * part;
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
+        for (int d = 0; d < DIMS; ++d) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<f4*>(op + 32 * d + 8 * i + 4 * h) =
                     (f4){acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
         }
-        if (h == 0) {
+        if (h == 0 && part == 0) {
             float* ml = a.workspace + kAttnCounters + (long)splits * a.rows * a.heads * D + at * 2;
             ml[0] = m;
             ml[1] = l;
@@ -666,12 +781,13 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
 template <int D, bool EXTRA>
 static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     constexpr size_t image = 2 * kTileKeys * D * sizeof(uint16_t);
-    // Two workgroups per CU hide each other's waits where there are enough of them;
-    // fewer workgroups get as many images as a CU's LDS holds, up to four (three
-    // tiles ahead).
+    constexpr size_t behind = sizeof(PrefillShared<prefill_share(D)>);
+    // Two workgroups of four waves per CU hide each other's waits where there are
+    // enough of them; fewer workgroups, and those of eight waves, get as many
+    // images as a CU's LDS holds, up to four (three tiles ahead).
     const long tiles = prefill_tiles(a.rows, a.count, a.group);
-    const size_t room = tiles * a.c.kv_heads * a.splits > dev.num_cu ? dev.max_lds / 2 : dev.max_lds;
-    const int fit = (int)((room - kPrefillWaves * sizeof(int)) / image);
+    const bool two = prefill_share(D) == 1 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
+    const int fit = (int)(((two ? dev.max_lds / 2 : dev.max_lds) - behind) / image);
     a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
     auto kernel = &attn_prefill_kernel<D, EXTRA>;
     std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, EXTRA>>::value[dev.device];
@@ -686,8 +802,8 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
-        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA>), grid, dim3(kPrefillThreads),
-                           a.images * image + kPrefillWaves * sizeof(int), st, a, (int)t);
+        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA>), grid, dim3(prefill_threads(D)), a.images * image + behind,
+                           st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
