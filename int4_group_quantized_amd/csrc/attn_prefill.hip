@@ -4,9 +4,10 @@
 //   token t sees: causal, its own sequence only, optionally within a window or
 //   with a prefix that every token sees.
 //
-// A workgroup of four or eight waves serves 128 query rows of one kv head: the tokens
-// of one tile times the heads of the group (row = token * group + head), so
-// that every key and value read serves the whole group.  One pass over the
+// A workgroup of four or eight waves serves 128 query rows of one kv head, or 64
+// where that leaves CUs idle: the tokens of one tile times the heads of the group
+// (row = token * group + head), so that every key and value read serves the whole
+// group.  One pass over the
 // visible tiles of 64 positions keeps the running maximum and sum of the
 // softmax; scores and outputs stay in registers.
 //
@@ -19,18 +20,18 @@
 // 16(m/16) + 8(m/4%2) + 4(m/8%2) + m%4: register r then is key 16(r/8) + 8h + r%8.
 //
 // Dimensions 192 and 256: one wave's outputs and queries of 32 rows take most of
-// the registers, so two waves share the rows (SHARE = 2, eight waves).  Each
-// takes half of a tile's keys in the first product and half of the output
+// the registers, so two waves share the rows (SHARE = 2); so they do in
+// workgroups of 64 rows, to be done sooner.  Each takes half of a tile's keys in the first product and half of the output
 // dimensions in the second; between them the weights meet in LDS, with the
 // maximum they were taken from.  4,096 tokens of 16 heads of 256 (4 kv heads)
 // take 191 us, with one wave per SIMD 214; 3,044 tokens of five sequences, 8
-// heads on one kv head, with a distance bias, 48 and 85.  With fewer workgroups
-// than CUs the same was tried at dim 64 and 128: 5 to 15% slower.
+// heads on one kv head, with a distance bias, 48 and 85.  128 rows by eight waves
+// at dim 64 and 128, one workgroup per CU: 5 to 15% slower than by four.
 //
 // Bound by the matrix cores, the softmax's vector work and LDS reads together:
 // 8,192 tokens of 32 heads of 128 (8 kv heads, 550 GFLOP) take 614 us, 896
 // TFLOP/s; without either product, the loads, the maximum or the exponentials it
-// would be 2 to 15% less.  Few tokens are bound by latency: 34 tokens take 7.4 us.
+// would be 2 to 15% less.  Few tokens are bound by latency: 34 tokens take 6.5 us.
 //
 // Tiles go straight from memory into LDS images, one ahead with two images (two
 // workgroups per CU) and up to three ahead with four (one per CU, where there are
@@ -51,45 +52,78 @@ namespace q4 {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kPrefillRows = 128;  // of a workgroup, 32 per wave or pair of waves
-// Waves that share 32 rows, and threads of a workgroup.
-__host__ __device__ constexpr int prefill_share(int dim) { return dim > 128 ? 2 : 1; }
-__host__ __device__ constexpr int prefill_threads(int dim) { return 2 * kPrefillRows * prefill_share(dim); }
-constexpr int kPrefillBlocks = 512;     // workgroups that splits make at most: two per CU
-constexpr double kSecondLaunch = 5.0;   // us, launch and join of short partial results
+// Waves that share 32 of a workgroup's rows, and threads of a workgroup.
+__host__ __device__ constexpr int prefill_share(int dim, int rows) { return dim > 128 || rows == 64 ? 2 : 1; }
+__host__ __device__ constexpr int prefill_threads(int dim, int rows) { return 2 * rows * prefill_share(dim, rows); }
+constexpr int kPrefillAlone = 256;      // workgroups that have a CU to themselves
+constexpr double kSecondLaunch = 4.0;   // us, launch and join of short partial results
+constexpr double kJoinRound = 1.0;      // us, each further kJoin of them
 // Tokens per workgroup.
-__host__ __device__ inline int prefill_tokens(int group) { return kPrefillRows / group; }
+__host__ __device__ inline int prefill_tokens(int rows, int group) { return rows / group; }
 
-static long prefill_tiles(long tokens, long count, int group) {
-    const int tb = prefill_tokens(group);
+static long prefill_tiles(long tokens, long count, int rows, int group) {
+    const int tb = prefill_tokens(rows, group);
     const long a = tokens / tb + count;  // sum of ceil(n_s / tb) at most
     return a < tokens ? a : tokens;      // each tile has a token
 }
 
+// How a call is cut up.
+struct PrefillPlan {
+    int rows;      // query rows of a workgroup
+    int splits;    // of the positions
+    double time;   // estimate, us
+};
+
 // Splits of the positions.  A workgroup alone on its CU takes a time c per tile
-// (1.1, 1.4 and 2.4 us at dim 64, 128 and 256); n splits of L tiles take
-// c L / n, the second launch and n times what writing and reading one partial
-// output per row costs (v, at about 4 TB/s): least at n = sqrt(c L / v), and
-// worth it where it saves more than the launch.  Measured, dim 128, 16 heads:
-// 34 tokens on 8,000 positions 20.7 us with 32 splits, 23.9 with 63, 25.1 with
-// 16; 300 tokens on 720 19.8 with 4, 22.1 with 8, 28.5 whole; 20 tokens on 740
-// 22.3 whole, 14.4 with 3, 12.0 with 6; 1,000 tokens 29.1 whole, 29.7 with 4.
-static int prefill_splits(long tokens, long count, int heads, int kv_heads, int dim, long max_length) {
-    const long blocks = prefill_tiles(tokens, count, heads / kv_heads) * kv_heads;
-    const long length = (max_length + kTileKeys - 1) / kTileKeys;
-    const long most = kPrefillBlocks / blocks < length ? kPrefillBlocks / blocks : length;
-    if (most < 2) return 1;
-    const double c = 0.6 + dim / 150.0, v = 8e-6 / 4.0 * (double)tokens * heads * dim;
+// (1.1, 1.4 and 2.3 us at dim 64, 128 and 256; 85% of that with 64 rows); n
+// splits of L tiles take c L / n, the second launch, its rounds of kJoin parts
+// and n times what writing and reading one partial output per row costs (v, at
+// about 4 TB/s): least at n = sqrt(c L / v), or where the last round is full.
+// Measured, dim 128, 16 heads: 34 tokens on 8,000 positions 20.7 us with 32
+// splits, 23.9 with 63, 25.1 with 16; 300 tokens on 720 19.8 with 4, 22.1 with
+// 8, 28.5 whole; 20 tokens on 740 22.3 whole, 14.4 with 3, 12.0 with 6; 40
+// tokens of 8 heads on 8,000 18.6 with 42, 16.4 with 32.  A second launch taken
+// for 5 us left 100 tokens on 300 whole (13.2 us, 11.5 split), for 3 it split
+// 1,000 tokens (30.3 us, 24.1 whole).
+static PrefillPlan prefill_split(int rows, long blocks, long length, long tokens, int heads, int dim) {
+    // Two workgroups per CU have room beyond dim 128 only in time, one after the other.
+    const long room = (dim > 128 ? 1 : 2) * kPrefillAlone / blocks, most = room < length ? room : length;
+    const double c = (0.6 + dim / 150.0) * (rows == 64 ? 0.85 : 1.0), v = 8e-6 / 4.0 * (double)tokens * heads * dim;
+    PrefillPlan plan = {rows, 1, c * (double)length};
+    if (most < 2) return plan;
     long n = (long)(std::sqrt(c * (double)length / v) + 0.5);
     n = n < 1 ? 1 : n > most ? most : n;
-    const long per = (length + n - 1) / n;
-    n = (length + per - 1) / per;  // as many as that many tiles each make
-    const double saved = c * (double)(length - per) - v * (double)n;
-    return saved > kSecondLaunch ? (int)n : 1;
+    for (const long want : {n, (n - 1) / kJoin * kJoin}) {
+        if (want < 2) continue;
+        const long per = (length + want - 1) / want;
+        const long made = (length + per - 1) / per;  // as many as that many tiles each make
+        const double time =
+            c * (double)per + v * (double)made + kSecondLaunch + kJoinRound * (double)((made - 1) / kJoin);
+        if (time < plan.time) plan = {rows, (int)made, time};
+    }
+    return plan;
+}
+
+// 64 or 128 rows.  Where workgroups of 64 rows have a CU each, a tile takes them
+// less time than those of 128 (two waves share 32 rows instead of one): 1,000
+// tokens of 16 heads of 128 23.7 against 27.7 us, 34 tokens 6.5 against 7.4.
+// They read the keys and values twice as often, and leave room for fewer
+// splits: 200 tokens of 32 heads on 4,000 positions 38.3 against 34.0.  So a
+// call that would be split takes them only with up to 64 workgroups (16 tokens
+// on 16,000 positions 19.9 against 21.3; 34 tokens of 32 heads on 4 kv heads
+// on 8,000 24.0 against 27.2).
+static PrefillPlan prefill_plan(long tokens, long count, int heads, int kv_heads, int dim, long max_length) {
+    const int group = heads / kv_heads;
+    const long length = (max_length + kTileKeys - 1) / kTileKeys;
+    const long large = prefill_tiles(tokens, count, 128, group) * kv_heads;
+    const long small = prefill_tiles(tokens, count, 64, group) * kv_heads;
+    const PrefillPlan plan = prefill_split(128, large, length, tokens, heads, dim);
+    if (dim == 96 || small > (plan.splits > 1 ? kPrefillAlone / 4 : kPrefillAlone)) return plan;
+    return prefill_split(64, small, length, tokens, heads, dim);
 }
 
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length) {
-    const int splits = prefill_splits(tokens, count, heads, kv_heads, dim, max_length);
+    const int splits = prefill_plan(tokens, count, heads, kv_heads, dim, max_length).splits;
     // The counters of the decode call come first, so that both can share one.
     return splits == 1 ? 0 : ((int64_t)splits * tokens * heads * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
@@ -104,8 +138,9 @@ struct PrefillTile {
 
 // Tile t of the `tiles` of sequence s, whose rows are first .. last - 1.  A
 // sequence's last tokens, which see the most positions, come first.
+template <int ROWS>
 __device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s, int first, int last, int tiles, int t) {
-    const int tb = prefill_tokens(a.group);
+    const int tb = prefill_tokens(ROWS, a.group);
     const int at = (tiles - 1 - t) * tb;
     PrefillTile r;
     r.s = s;
@@ -117,16 +152,17 @@ __device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s,
 }
 
 // Tile number `item`.
+template <int ROWS>
 __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item) {
     const int lane = threadIdx.x & 63;
-    const int tb = prefill_tokens(a.group);
+    const int tb = prefill_tokens(ROWS, a.group);
     PrefillTile none;
     none.s = -1;
     none.token = none.n = none.pos = none.len = 0;
     if (a.count == 1) {
         const int st = min(max(a.q_starts[0], 0), a.rows), en = min(max(a.q_starts[1], st), a.rows);
         const int n = (en - st + tb - 1) / tb;
-        return item < n ? prefill_tile_of(a, 0, st, en, n, item) : none;
+        return item < n ? prefill_tile_of<ROWS>(a, 0, st, en, n, item) : none;
     }
     int before = 0;
     for (int s0 = 0; s0 < a.count; s0 += 64) {
@@ -141,8 +177,8 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
         if (hit) {
             const int l = __builtin_ctzll(hit);
             const int tiles = __builtin_amdgcn_readlane(n, l);
-            return prefill_tile_of(a, s0 + l, __builtin_amdgcn_readlane(st, l), __builtin_amdgcn_readlane(en, l), tiles,
-                                   item - (before + __builtin_amdgcn_readlane(c.upto, l) - tiles));
+            return prefill_tile_of<ROWS>(a, s0 + l, __builtin_amdgcn_readlane(st, l), __builtin_amdgcn_readlane(en, l),
+                                         tiles, item - (before + __builtin_amdgcn_readlane(c.upto, l) - tiles));
         }
         before += c.last;
     }
@@ -215,10 +251,10 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // the wave starts its rows again here, after the fast loop and with nothing of it
 // live, because the same handling inside that loop cost it 100 registers
 // (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
-template <int D, bool EXTRA>
+template <int D, bool EXTRA, int SHARE>
 __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
                                                         int split, int kvh, int wave, int k_begin, int k_end) {
-    constexpr int SHARE = prefill_share(D), OUT = D / (2 * SHARE);  // output dimensions of a lane
+    constexpr int OUT = D / (2 * SHARE);  // output dimensions of a lane
     const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
     const int o0 = (2 * (wave % SHARE) + (lane >> 5)) * OUT;
     const PrefillRow q = prefill_row(a, it, prefix, kvh, wave / SHARE * 32 + n);
@@ -309,12 +345,11 @@ __device__ __forceinline__ void wait_and_meet() {
 }
 
 // LDS of a workgroup behind its images.
-template <int SHARE>
+template <int WAVES, bool SHARED>
 struct PrefillShared {
-    static constexpr int WAVES = 4 * SHARE;
-    u4 weights[SHARE > 1 ? WAVES : 0][2][64];  // a wave's half of a tile's weights, as operands
-    float base[SHARE > 1 ? WAVES : 0][32];     // and the maximum that they were taken from
-    float sum[SHARE > 1 ? WAVES : 0][32];      // a wave's share of the rows' sums
+    u4 weights[SHARED ? WAVES : 0][2][64];  // a wave's half of a tile's weights, as operands
+    float base[SHARED ? WAVES : 0][32];     // and the maximum that they were taken from
+    float sum[SHARED ? WAVES : 0][32];      // a wave's share of the rows' sums
     int found[WAVES];                          // a wave has seen infinities or NaN where a row is masked
 };
 
@@ -325,9 +360,10 @@ __device__ __forceinline__ void lds_meet() {
     asm volatile("" ::: "memory");
 }
 
-template <int D, bool EXTRA>
-__global__ void __launch_bounds__(prefill_threads(D), 2) attn_prefill_kernel(AttnArgs a, int tile0) {
-    constexpr int SHARE = prefill_share(D), THREADS = prefill_threads(D);
+template <int D, bool EXTRA, int ROWS>
+__global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 64 ? 1 : 2)
+    attn_prefill_kernel(AttnArgs a, int tile0) {
+    constexpr int SHARE = prefill_share(D, ROWS), THREADS = prefill_threads(D, ROWS), WAVES = THREADS / 64;
     constexpr int KEYS = 2 / SHARE;        // blocks of 32 keys of a wave
     constexpr int DIMS = D / (32 * SHARE);  // and of 32 output dimensions
     const int splits = a.splits;
@@ -342,12 +378,12 @@ __global__ void __launch_bounds__(prefill_threads(D), 2) attn_prefill_kernel(Att
         ids = a.c.table[min((int)(threadIdx.x & 63), a.c.cols - 1)];
         ids_first = 0;
     }
-    const PrefillTile it = prefill_tile(a, tile0 + blockIdx.z);
+    const PrefillTile it = prefill_tile<ROWS>(a, tile0 + blockIdx.z);
     if (it.s < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
     const int part = wave % SHARE, rows0 = wave / SHARE * 32;
-    PrefillShared<SHARE>& shared = *reinterpret_cast<PrefillShared<SHARE>*>(lds + a.images * IMAGE);
+    auto& shared = *reinterpret_cast<PrefillShared<WAVES, (SHARE > 1)>*>(lds + a.images * IMAGE);
 
     const int prefix = a.prefix ? a.prefix[it.s] : 0;
     const PrefillRow q = prefill_row(a, it, prefix, kvh, rows0 + n);
@@ -568,7 +604,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 2) attn_prefill_kernel(Att
             // Operand reads run ahead of the products: KW steps of K, and VW of V before
             // the softmax, as many as registers hold without spilling (a spilled
             // register's reload would wait for the tiles under way).
-            constexpr int STEPS = D / 16, KW = STEPS == 4 || (D > 192 && EXTRA) ? 2 : STEPS == 6 ? 3 : 4, VW = (SHARE > 1 ? D <= 192 : D <= 128 && !EXTRA) ? 2 : 1;
+            constexpr int STEPS = D / 16, KW = STEPS == 4 || (D > 192 && EXTRA) ? 2 : STEPS == 6 ? 3 : 4;
+            constexpr int VW = (SHARE > 1 ? D <= 192 : !EXTRA) ? 2 : 1;
             u4 kf[KW][KEYS];
 #pragma unroll
             for (int d = 0; d < KW; ++d)
@@ -586,7 +623,8 @@ __global__ void __launch_bounds__(prefill_threads(D), 2) attn_prefill_kernel(Att
                     if (d + KW < STEPS) kf[d % KW][b] = im[k_chunk<D>(32 * b + km, 2 * (d + KW) + h)];
                 }
                 if constexpr (SPREAD) {
-                    if (d % SHARE == 0) load_piece(next, d / SHARE);
+                    constexpr int EVERY = STEPS / (2 * STAGE);
+                    if (d % EVERY == 0) load_piece(next, d / EVERY);
                 }
             }
             // V operands in the order of use: the wave's own keys first.
@@ -725,9 +763,9 @@ __global__ void __launch_bounds__(prefill_threads(D), 2) attn_prefill_kernel(Att
     __syncthreads();
     int any_found = 0;
 #pragma unroll
-    for (int w = 0; w < 4 * SHARE; ++w) any_found |= shared.found[w];
+    for (int w = 0; w < WAVES; ++w) any_found |= shared.found[w];
     if (any_found) {
-        prefill_rows_one_by_one<D, EXTRA>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
+        prefill_rows_one_by_one<D, EXTRA, SHARE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
     if constexpr (SHARE > 1) l += shared.sum[wave ^ 1][n];
@@ -778,19 +816,19 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     store_joined(join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits), a.out + r * D);
 }
 
-template <int D, bool EXTRA>
+template <int D, bool EXTRA, int ROWS>
 static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     constexpr size_t image = 2 * kTileKeys * D * sizeof(uint16_t);
-    constexpr size_t behind = sizeof(PrefillShared<prefill_share(D)>);
+    constexpr size_t behind = sizeof(PrefillShared<prefill_threads(D, ROWS) / 64, (prefill_share(D, ROWS) > 1)>);
     // Two workgroups of four waves per CU hide each other's waits where there are
     // enough of them; fewer workgroups, and those of eight waves, get as many
     // images as a CU's LDS holds, up to four (three tiles ahead).
-    const long tiles = prefill_tiles(a.rows, a.count, a.group);
-    const bool two = prefill_share(D) == 1 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
+    const long tiles = prefill_tiles(a.rows, a.count, ROWS, a.group);
+    const bool two = prefill_threads(D, ROWS) == 256 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
     const int fit = (int)(((two ? dev.max_lds / 2 : dev.max_lds) - behind) / image);
     a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
-    auto kernel = &attn_prefill_kernel<D, EXTRA>;
-    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, EXTRA>>::value[dev.device];
+    auto kernel = &attn_prefill_kernel<D, EXTRA, ROWS>;
+    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, EXTRA, ROWS>>::value[dev.device];
     if (!ready.load(std::memory_order_acquire)) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
@@ -802,7 +840,7 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
-        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA>), grid, dim3(prefill_threads(D)), a.images * image + behind,
+        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA, ROWS>), grid, dim3(prefill_threads(D, ROWS)), a.images * image + behind,
                            st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -813,9 +851,14 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
 template <int D>
 static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     a.inv_group = 1.0f / (float)a.group;
-    a.splits = prefill_splits(a.rows, a.count, a.heads, a.c.kv_heads, D, a.max_length);
+    const PrefillPlan plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, a.max_length);
+    a.splits = plan.splits;
     const bool extra = a.softcap > 0.0f || a.slopes;
-    hipError_t e = extra ? launch_tiles<D, true>(a, dev, st) : launch_tiles<D, false>(a, dev, st);
+    hipError_t e = hipSuccess;
+    if constexpr (D != 96) {  // three blocks of 32 dimensions do not share out
+        if (plan.rows == 64) e = extra ? launch_tiles<D, true, 64>(a, dev, st) : launch_tiles<D, false, 64>(a, dev, st);
+    }
+    if (plan.rows == 128) e = extra ? launch_tiles<D, true, 128>(a, dev, st) : launch_tiles<D, false, 128>(a, dev, st);
     if (e != hipSuccess || a.splits == 1) return e;
     const long rows = (long)a.rows * a.heads;
     hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
