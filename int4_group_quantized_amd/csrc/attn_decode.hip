@@ -283,11 +283,10 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
                 float x = score<EXTRA>(s[u][i], sp, key - (len - 1));
                 if (!whole) x = key >= start && key < len && id.v[u >> 1] >= 0 ? x : Q4_NEG_INF;
                 s[u][i] = x;
-                top = fmaxf(top, x);
+                top = top_of(top, x);
             }
         }
-        top = fmaxf(top, lane_swap16(top));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        top = top_of_halves(top_of_rows(top));
         const float m_new = fmaxf(m, top);
         const float base = m_new == Q4_NEG_INF ? 0.0f : m_new;
         const float f = exp2_hw(m - base);

@@ -304,12 +304,6 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
     }
 }
 
-// max(a, b) of two matrix results: the median with +inf.  fmaxf would first pass
-// each of them through an instruction of its own to quieten signalling NaN.
-__device__ __forceinline__ float max_of(float a, float b) {
-    return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
-}
-
 // 16 bytes per lane from memory into LDS: lane i's to byte `to` + 16 i.  In
 // assembly because the compiler, which sees that images follow each other in
 // one array, would let every LDS read wait for all such loads under way; the
@@ -683,14 +677,17 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                     }
                 }
             }
-            float tops[16];
+            // Four chains, of three operands an instruction.
+            float tops[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) tops[i] = KEYS > 1 ? max_of(s[0][i], s[KEYS - 1][i]) : s[0][i];
+            for (int c = 0; c < 4; ++c) {
+                const auto v = [&](int i) { return s[i / 4][4 * (i % 4) + c]; };
+                tops[c] = v(0);
 #pragma unroll
-            for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-                for (int i = 0; i < w; ++i) tops[i] = fmaxf(tops[i], tops[i + w]);
-            float top = fmaxf(tops[0], __shfl_xor(tops[0], 32, 64));
+                for (int i = 1; i + 1 < 4 * KEYS; i += 2) tops[c] = top_of(top_of(tops[c], v(i)), v(i + 1));
+                tops[c] = top_of(tops[c], v(4 * KEYS - 1));
+            }
+            float top = top_of_halves(top_of(top_of(tops[0], tops[1]), top_of(tops[2], tops[3])));
             if constexpr (!EXTRA) top *= sp.scale2;
             // The maximum that the exponents are taken from follows the true one only
             // when it is more than 2^8 behind: weights then stay below 2^8, and the

@@ -22,6 +22,23 @@ __device__ __forceinline__ float part_weight(float m, float top) {
     return m == Q4_NEG_INF ? 0.0f : exp2_hw(m - top);
 }
 
+// The larger of two, NaN if either is: one instruction for two or three operands,
+// where fmaxf first passes each matrix result through one of its own to quieten
+// signalling NaN (35 more for the 32 scores of a lane).
+__device__ __forceinline__ float top_of(float a, float b) {
+    return __builtin_elementwise_maximum(a, b);
+}
+
+// The maximum of lanes i and i ^ 32, and of i and i ^ 16, in registers.
+__device__ __forceinline__ float top_of_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return top_of(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float top_of_rows(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return top_of(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
 // Partial results pass between workgroups that may run on different XCDs, whose
 // L2 caches are not coherent with each other: they are written through to and
 // read from memory (agent scope).  A workgroup publishes them by waiting for its
