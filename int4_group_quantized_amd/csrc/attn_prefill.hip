@@ -25,13 +25,14 @@
 // dimensions in the second; between them the weights meet in LDS, with the
 // maximum they were taken from.  4,096 tokens of 16 heads of 256 (4 kv heads)
 // take 191 us, with one wave per SIMD 214; 3,044 tokens of five sequences, 8
-// heads on one kv head, with a distance bias, 48 and 85.  128 rows by eight waves
+// heads on one kv head, with a distance bias, 46 and 85.  128 rows by eight waves
 // at dim 64 and 128, one workgroup per CU: 5 to 15% slower than by four.
 //
-// Bound by the matrix cores, the softmax's vector work and LDS reads together:
-// 8,192 tokens of 32 heads of 128 (8 kv heads, 550 GFLOP) take 614 us, 896
-// TFLOP/s; without either product, the loads, the maximum or the exponentials it
-// would be 2 to 15% less.  Few tokens are bound by latency: 34 tokens take 6.5 us.
+// Bound by the matrix cores and the softmax's vector work together: 8,192 tokens
+// of 32 heads of 128 (8 kv heads, 550 GFLOP) take 562 us, 978 TFLOP/s, matrix
+// cores busy 55% of the cycles; without either product, the loads or the
+// exponentials it would be 2 to 15% less, with half of the LDS operand reads 3%.
+// Few tokens are bound by latency: 34 tokens take 6.4 us.
 //
 // Tiles go straight from memory into LDS images, one ahead with two images (two
 // workgroups per CU) and up to three ahead with four (one per CU, where there are
@@ -42,7 +43,7 @@
 // (k_chunk).
 //
 // Few tokens on a long cache leave most CUs idle, so the visible tiles are
-// then cut into equal splits joined by a second launch (prefill_splits).
+// then cut into equal splits joined by a second launch (prefill_split).
 #include "attn_softmax.hpp"
 
 #include <cmath>
@@ -69,9 +70,9 @@ static long prefill_tiles(long tokens, long count, int rows, int group) {
 
 // How a call is cut up.
 struct PrefillPlan {
-    int rows;      // query rows of a workgroup
-    int splits;    // of the positions
-    double time;   // estimate, us
+    int rows;     // query rows of a workgroup
+    int splits;   // of the positions
+    double time;  // estimate, us
 };
 
 // Splits of the positions.  A workgroup alone on its CU takes a time c per tile
@@ -86,7 +87,8 @@ struct PrefillPlan {
 // for 5 us left 100 tokens on 300 whole (13.2 us, 11.5 split), for 3 it split
 // 1,000 tokens (30.3 us, 24.1 whole).
 static PrefillPlan prefill_split(int rows, long blocks, long length, long tokens, int heads, int dim) {
-    // Two workgroups per CU have room beyond dim 128 only in time, one after the other.
+    // Beyond dim 128 a CU's LDS holds one workgroup: 128 tokens of 16 heads of 256 on
+    // 4,000 positions take 33 us in 256 workgroups, 44 in 512.
     const long room = (dim > 128 ? 1 : 2) * kPrefillAlone / blocks, most = room < length ? room : length;
     const double c = (0.6 + dim / 150.0) * (rows == 64 ? 0.85 : 1.0), v = 8e-6 / 4.0 * (double)tokens * heads * dim;
     PrefillPlan plan = {rows, 1, c * (double)length};
@@ -344,7 +346,7 @@ struct PrefillShared {
     u4 weights[SHARED ? WAVES : 0][2][64];  // a wave's half of a tile's weights, as operands
     float base[SHARED ? WAVES : 0][32];     // and the maximum that they were taken from
     float sum[SHARED ? WAVES : 0][32];      // a wave's share of the rows' sums
-    int found[WAVES];                          // a wave has seen infinities or NaN where a row is masked
+    int found[WAVES];                       // a wave has seen infinities or NaN where a row is masked
 };
 
 // The same for LDS operations only.
@@ -358,13 +360,13 @@ template <int D, bool EXTRA, int ROWS>
 __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 64 ? 1 : 2)
     attn_prefill_kernel(AttnArgs a, int tile0) {
     constexpr int SHARE = prefill_share(D, ROWS), THREADS = prefill_threads(D, ROWS), WAVES = THREADS / 64;
-    constexpr int KEYS = 2 / SHARE;        // blocks of 32 keys of a wave
-    constexpr int DIMS = D / (32 * SHARE);  // and of 32 output dimensions
-    const int splits = a.splits;
-    constexpr int C = D / 8;             // 16-byte chunks of a K row
+    constexpr int KEYS = 2 / SHARE;                 // blocks of 32 keys of a wave
+    constexpr int DIMS = D / (32 * SHARE);          // and of 32 output dimensions
+    constexpr int C = D / 8;                        // 16-byte chunks of a K row
     constexpr int STAGE = kTileKeys * C / THREADS;  // chunks per thread and tile, for K and for V
-    constexpr int IMAGE = 2 * kTileKeys * C;  // chunks of a tile's image
-    extern __shared__ u4 lds[];               // a.images of them, used in turn, and PrefillShared
+    constexpr int IMAGE = 2 * kTileKeys * C;        // chunks of a tile's image
+    extern __shared__ u4 lds[];                     // a.images of them, used in turn, and PrefillShared
+    const int splits = a.splits;
     const int kvh = blockIdx.x, split = blockIdx.y;
     // One sequence's first table entries, requested before anything else is known.
     int ids = -1, ids_first = -64;
