@@ -466,6 +466,71 @@ def test_prefill_masked_positions_stay_out(dev, junk):
     assert np.all(np.abs(o - want) <= H * np.abs(want) + TINY + (2 * H) * mag + n * TINY * 8)
 
 
+# Sequences without tokens count as possible workgroups: with 40 of them and 8 kv heads a call takes the form
+# for many (128 rows each), without them the one for few (64 rows).
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("options", [{}, dict(softcap=20.0, slopes=True, window=150), dict(prefix=[30, 0, 420])])
+def test_prefill_many_workgroups(dev, dim, page, options):
+    empty = [0] * 40
+    options = dict(options)
+    if "prefix" in options:
+        options["prefix"] = options["prefix"] + empty
+    prefill_case(dev, dim + page + 1, [40, 1, 90] + empty, [40, 130, 500] + empty, 16, 8, dim, page,
+                 absent=[(2, 1)], **options)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("empty", [0, 10])
+def test_prefill_split_forms(dev, dim, empty):
+    prefill_case(dev, dim + empty, [9, 7] + [0] * empty, [2500, 300] + [0] * empty, 16, 8, dim, 64)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("empty", [0, 40])
+@pytest.mark.parametrize("rising", [True, False])
+def test_prefill_scores_that_grow_or_shrink(dev, dim, empty, rising):
+    """Maxima that move by far more than the weights' range, up to the last position or from the first."""
+    rng = np.random.default_rng(dim + empty)
+    n, kv = 460, 8 if empty else 1
+    lengths = [n] + [0] * empty
+    pool = Pool(rng, lengths, kv, 64, dim)
+    for j in range(n):
+        grown = 1 + (j if rising else n - 1 - j) / 12
+        pool.k[pool.table[0, j // 64], :, j % 64] *= np.float16(grown)
+    starts = [0] + [70] * (empty + 1)
+    q = rng.standard_normal((70, 2 * kv, dim)).astype(np.float16)
+    out = q4.q4g128_attn_prefill(torch.from_numpy(q).to(dev), *pool.on(dev), i32(starts, dev), i32(lengths, dev),
+                                 scale=0.3)
+    check_attention(out, q, pool, starts, lengths, 0.3, "moving maxima")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("empty", [0, 40])
+@pytest.mark.parametrize("bad", [(70, 99), (3, 40), (63, 64)])
+def test_prefill_masked_infinities_in_every_form(dev, dim, empty, bad):
+    rng = np.random.default_rng(dim + empty + bad[0])
+    n, kv = 100, 8 if empty else 1
+    lengths = [n] + [0] * empty
+    pool = Pool(rng, lengths, kv, 32, dim)
+    starts = [0] + [n] * (empty + 1)
+    q = rng.standard_normal((n, 2 * kv, dim)).astype(np.float16)
+    clean_k, clean_v = pool.k.copy(), pool.v.copy()
+    dims = [5, dim // 2 - 1, dim - 1]
+    for j in bad:
+        pool.v[pool.table[0, j // 32], :, dims, j % 32] = np.inf
+    out = q4.q4g128_attn_prefill(torch.from_numpy(q).to(dev), *pool.on(dev), i32(starts, dev), i32(lengths, dev),
+                                 scale=0.1)
+    o = out.float().cpu().numpy()
+    assert np.all(o[bad[0]:, :, dims] == np.inf)
+    pool.k, pool.v = clean_k, clean_v
+    o[bad[0]:, :, dims] = 0
+    want, mag, _ = ref.attention(q, pool.k, pool.v, pool.table, starts, lengths, 0.1)
+    want[bad[0]:, :, dims] = 0
+    assert np.all(np.isfinite(o))
+    assert np.all(np.abs(o - want) <= H * np.abs(want) + TINY + (2 * H) * mag + n * TINY * 8)
+
+
 def test_prefill_agrees_with_decode(dev):
     """The last token of a prompt is the same question to both calls."""
     rng = np.random.default_rng(28)
