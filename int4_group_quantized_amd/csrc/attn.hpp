@@ -63,6 +63,8 @@ struct AttnArgs {
     const int* q_starts;
     const int* prefix;     // or NULL
     int count;             // sequences
+    int tile;              // tokens of a workgroup
+    float inv_tile;        // 1 / tile
     int splits;            // parts that the positions are cut into
     float inv_group;       // 1 / group
     int images;            // tiles that fit into the launch's LDS, 2 to 4

@@ -60,7 +60,7 @@ constexpr int kPrefillAlone = 256;      // workgroups that have a CU to themselv
 constexpr double kSecondLaunch = 4.0;   // us, launch and join of short partial results
 constexpr double kJoinRound = 1.0;      // us, each further kJoin of them
 // Tokens per workgroup.
-__host__ __device__ inline int prefill_tokens(int rows, int group) { return rows / group; }
+static int prefill_tokens(int rows, int group) { return rows / group; }
 
 static long prefill_tiles(long tokens, long count, int rows, int group) {
     const int tb = prefill_tokens(rows, group);
@@ -131,56 +131,71 @@ int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_
 }
 
 struct PrefillTile {
-    int s;      // sequence, or -1
-    int token;  // first token of the tile (row of q)
-    int n;      // tokens in the tile
-    int pos;    // position of the first token (may be negative)
-    int len;    // positions of the sequence
+    int s;       // sequence, or -1
+    int token;   // first token of the tile (row of q)
+    int n;       // tokens in the tile
+    int pos;     // position of the first token (may be negative)
+    int len;     // positions of the sequence
+    int prefix;  // positions that all of its tokens see
 };
+
+// x / a.tile rounded up, x < 2^21: the quotient of x - 1/2 keeps 1 / 256 from
+// every whole number, four times its error.
+__device__ __forceinline__ int prefill_tiles_of(const AttnArgs& a, int x) {
+    return (int)(((float)(x + a.tile) - 0.5f) * a.inv_tile);
+}
 
 // Tile t of the `tiles` of sequence s, whose rows are first .. last - 1.  A
 // sequence's last tokens, which see the most positions, come first.
-template <int ROWS>
-__device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s, int first, int last, int tiles, int t) {
-    const int tb = prefill_tokens(ROWS, a.group);
-    const int at = (tiles - 1 - t) * tb;
+__device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s, int first, int last, int len,
+                                                       int prefix, int tiles, int t) {
+    const int at = (tiles - 1 - t) * a.tile;
     PrefillTile r;
     r.s = s;
     r.token = first + at;
-    r.n = min(tb, last - r.token);
-    r.len = min(max(a.lengths[s], 0), a.max_length);
+    r.n = min(a.tile, last - r.token);
+    r.len = min(max(len, 0), a.max_length);
     r.pos = r.len - (last - first) + at;
+    r.prefix = prefix;
     return r;
 }
 
-// Tile number `item`.
-template <int ROWS>
+// Tile number `item`.  A sequence's length and prefix are read with its rows,
+// not after them (readfirstlane and the empty assembly keep the compiler from
+// moving the reads to where they are needed: 0.1 to 0.3 us).
 __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item) {
     const int lane = threadIdx.x & 63;
-    const int tb = prefill_tokens(ROWS, a.group);
     PrefillTile none;
     none.s = -1;
-    none.token = none.n = none.pos = none.len = 0;
+    none.token = none.n = none.pos = none.len = none.prefix = 0;
     if (a.count == 1) {
-        const int st = min(max(a.q_starts[0], 0), a.rows), en = min(max(a.q_starts[1], st), a.rows);
-        const int n = (en - st + tb - 1) / tb;
-        return item < n ? prefill_tile_of<ROWS>(a, 0, st, en, n, item) : none;
+        const auto of = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
+        const int prefix = a.prefix ? of(a.prefix[0]) : 0;
+        const int st = min(max(first, 0), a.rows), en = min(max(last, st), a.rows);
+        const int n = prefill_tiles_of(a, en - st);
+        return item < n ? prefill_tile_of(a, 0, st, en, len, prefix, n, item) : none;
     }
     int before = 0;
     for (int s0 = 0; s0 < a.count; s0 += 64) {
-        int st = 0, en = 0;
+        int st = 0, en = 0, len = 0, prefix = 0;
         if (s0 + lane < a.count) {
-            st = min(max(a.q_starts[s0 + lane], 0), a.rows);
-            en = min(max(a.q_starts[s0 + lane + 1], st), a.rows);
+            st = a.q_starts[s0 + lane];
+            en = a.q_starts[s0 + lane + 1];
+            len = a.lengths[s0 + lane];
+            if (a.prefix) prefix = a.prefix[s0 + lane];
         }
-        const int n = (en - st + tb - 1) / tb;
+        asm volatile("" : "+v"(st), "+v"(en), "+v"(len), "+v"(prefix));
+        st = min(max(st, 0), a.rows);
+        en = min(max(en, st), a.rows);
+        const int n = prefill_tiles_of(a, en - st);
         const LaneScan c = lane_scan(n);
         const uint64_t hit = __ballot(n > 0 && item < before + c.upto && item >= before + c.upto - n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
-            const int tiles = __builtin_amdgcn_readlane(n, l);
-            return prefill_tile_of<ROWS>(a, s0 + l, __builtin_amdgcn_readlane(st, l), __builtin_amdgcn_readlane(en, l),
-                                         tiles, item - (before + __builtin_amdgcn_readlane(c.upto, l) - tiles));
+            const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            return prefill_tile_of(a, s0 + l, of(st), of(en), of(len), of(prefix), of(n),
+                                   item - (before + of(c.upto) - of(n)));
         }
         before += c.last;
     }
@@ -374,14 +389,14 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         ids = a.c.table[min((int)(threadIdx.x & 63), a.c.cols - 1)];
         ids_first = 0;
     }
-    const PrefillTile it = prefill_tile<ROWS>(a, tile0 + blockIdx.z);
+    const PrefillTile it = prefill_tile(a, tile0 + blockIdx.z);
     if (it.s < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
     const int part = wave % SHARE, rows0 = wave / SHARE * 32;
     auto& shared = *reinterpret_cast<PrefillShared<WAVES, (SHARE > 1)>*>(lds + a.images * IMAGE);
 
-    const int prefix = a.prefix ? a.prefix[it.s] : 0;
+    const int prefix = it.prefix;
     const PrefillRow q = prefill_row(a, it, prefix, kvh, rows0 + n);
     const int head = q.head, token = q.token, qpos = q.pos, hi = q.see.hi, lo = q.see.lo;
     const bool live = q.live;
@@ -852,6 +867,8 @@ static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStre
     a.inv_group = 1.0f / (float)a.group;
     const PrefillPlan plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, a.max_length);
     a.splits = plan.splits;
+    a.tile = prefill_tokens(plan.rows, a.group);
+    a.inv_tile = 1.0f / (float)a.tile;
     const bool extra = a.softcap > 0.0f || a.slopes;
     hipError_t e = hipSuccess;
     if constexpr (D != 96) {  // three blocks of 32 dimensions do not share out
