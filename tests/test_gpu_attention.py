@@ -292,6 +292,14 @@ def test_decode_joined_in_groups(dev):
     assert torch.equal(first, decode_case(dev, 40, [20000, 3, 0, 9000], 17, 1, 64, 64))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window", [0, 2900])
+def test_decode_long_uneven(dev, dim, window):
+    """More than eight tiles for each workgroup of a kv head: parts are evened out."""
+    decode_case(dev, 14 + dim, [3000, 100, 0, 2500, 1, 4000, 64, 65], 32, 32, dim, 64, window=window)
+    decode_case(dev, 15 + dim, [700] * 7 + [8000], 33, 33, dim, 16, window=window)
+
+
 def test_decode_many_sequences(dev):
     rng = np.random.default_rng(2)
     decode_case(dev, 2, [int(n) for n in rng.integers(0, 40, 150)] + [3000], 2, 1, 64, 16)
