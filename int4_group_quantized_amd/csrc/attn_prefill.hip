@@ -29,7 +29,7 @@
 // at dim 64 and 128, one workgroup per CU: 5 to 15% slower than by four.
 //
 // Bound by the matrix cores and the softmax's vector work together: 8,192 tokens
-// of 32 heads of 128 (8 kv heads, 550 GFLOP) take 562 us, 978 TFLOP/s, matrix
+// of 32 heads of 128 (8 kv heads, 550 GFLOP) take 553 us, 994 TFLOP/s, matrix
 // cores busy 55% of the cycles; without either product, the loads or the
 // exponentials it would be 2 to 15% less, with half of the LDS operand reads 3%.
 // Few tokens are bound by latency: 34 tokens take 6.4 us.
