@@ -32,11 +32,13 @@ namespace q4 {
 constexpr int kAppendThreads = 256;
 constexpr int kValueTokens = 64;
 constexpr int kAppendAhead = 4;      // heads whose rows a team requests together
-// Teams beyond which a team serves more heads (2, 4, 8, ... of one token), so
-// that sines and cosines are formed less often.  8,192 tokens of 40 query and key
-// heads (302 MB): one head per team 100 us, 4 heads 66 us, 8 heads 64 us, 16
-// heads 68 us, 32 heads 82 us; fewer teams than this gain nothing from it.
-constexpr long kAppendTeams = 65536;
+// Waves beyond which a team serves more heads (2, 4 or 8 of one token), so that
+// sines and cosines are formed less often, and the most heads.  40 query and key
+// heads, one per team against as chosen: 8,192 tokens of 128 100 and 66 us (4
+// heads 66, 16 68, 32 82), 700 of 128 13.7 and 10.7, 1,404 of 256 56 and 32; a
+// limit of 2,048 waves takes 300 of 256 from 9.9 to 10.9, one of 16,384 to 13.1.
+constexpr long kAppendWaves = 4096;
+constexpr int kAppendMost = 8;
 constexpr int kValuePitch = kValueTokens + 10;  // halves; 37 dwords, so a token's dimensions fall on different banks
 // Tokens per workgroup of values: kValueTokens where that gives kValueBlocks
 // workgroups, else kValueFew (one token of each of 64 sequences: 3.7 us with 8,
@@ -220,7 +222,8 @@ static hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
     constexpr int TEAMS = kAppendThreads / (D <= 64 ? 16 : D <= 128 ? 32 : 64);
     const int rows = a.heads + a.c.kv_heads;
     int hb = 1;
-    while ((long)a.tokens * ((rows + hb - 1) / hb) > kAppendTeams && hb < rows) hb *= 2;
+    constexpr long SLOTS = kAppendWaves * 64 * TEAMS / kAppendThreads;
+    while ((long)a.tokens * ((rows + hb - 1) / hb) > SLOTS && hb < rows && hb < kAppendMost) hb *= 2;
     // A launch takes at most 2^32 - 1 threads.
     while ((long)a.tokens * ((rows + hb - 1) / hb) > (1L << 23) * TEAMS && hb < rows) hb *= 2;
     const long full = ((long)a.tokens + kValueTokens - 1) / kValueTokens * a.c.kv_heads;

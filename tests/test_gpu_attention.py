@@ -170,6 +170,14 @@ def test_append_many_heads(dev):
     check_append(dev, np.random.default_rng(8), run_of(0, 40, 70), 35, 5, 128, 64, 128, norm=True)
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("tokens", [210, 420, 830])
+def test_append_several_heads_of_a_token_together(dev, dim, tokens):
+    """Enough tokens that 2, 4 or 8 heads share a token's sines, 45 heads that do not divide by them."""
+    rng = np.random.default_rng(dim + tokens)
+    check_append(dev, rng, run_of(0, 5, tokens), 40, 5, dim, 64, 16, interleaved=tokens == 420, norm=True)
+
+
 def test_append_one_token_of_each_sequence(dev):
     rng = np.random.default_rng(3)
     check_append(dev, rng, [(s, int(p)) for s, p in enumerate(rng.integers(0, 700, 16))], 16, 4, 128, 64, 128,
