@@ -453,6 +453,12 @@ def test_prefill_few_tokens_on_a_long_cache(dev):
     prefill_case(dev, 24, [3, 20, 1], [2500, 40, 1300], 4, 2, 128, 16, softcap=10.0, slopes=True)
 
 
+@pytest.mark.parametrize("window", [1, 100, 1000, 3000, 5990])
+def test_prefill_few_tokens_on_a_long_cache_with_a_window(dev, window):
+    prefill_case(dev, 30 + window, [9, 40], [6000, 2000], 4, 2, 64, 64, window=window)
+    prefill_case(dev, 31 + window, [5], [6000], 8, 1, 256, 32, window=window, prefix=[700])
+
+
 def test_prefill_absent_pages(dev):
     prefill_case(dev, 25, [60, 20], [200, 20], 4, 1, 64, 16, absent=[(0, 0), (0, 3), (0, 12), (1, 0), (1, 1)])
     prefill_case(dev, 26, [5], [3000], 4, 1, 64, 64, absent=[(0, 0), (0, 20), (0, 46)])
