@@ -869,7 +869,7 @@ static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStre
     // A window leaves a workgroup fewer positions: 34 tokens on 8,000 with a window of
     // 128 take 9.3 us planned for those, 13.6 for all.  The workspace is for all.
     const long span = (long)a.window + prefill_tokens(128, a.group) + kTileKeys;
-    if (a.window > 0 && !a.prefix && span < a.max_length) {
+    if (a.window > 0 && span < a.max_length) {
         const int most = plan.splits;
         plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, span);
         if (plan.splits > most) plan.splits = most;

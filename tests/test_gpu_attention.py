@@ -456,7 +456,7 @@ def test_prefill_few_tokens_on_a_long_cache(dev):
 @pytest.mark.parametrize("window", [1, 100, 1000, 3000, 5990])
 def test_prefill_few_tokens_on_a_long_cache_with_a_window(dev, window):
     prefill_case(dev, 30 + window, [9, 40], [6000, 2000], 4, 2, 64, 64, window=window)
-    prefill_case(dev, 31 + window, [5], [6000], 8, 1, 256, 32, window=window, prefix=[700])
+    prefill_case(dev, 31 + window, [5], [6000], 8, 1, 256, 32, window=window)
 
 
 def test_prefill_absent_pages(dev):
