@@ -40,11 +40,13 @@ constexpr int kAppendAhead = 4;      // heads whose rows a team requests togethe
 constexpr long kAppendWaves = 4096;
 constexpr int kAppendMost = 8;
 constexpr int kValuePitch = kValueTokens + 10;  // halves; 37 dwords, so a token's dimensions fall on different banks
-// Tokens per workgroup of values: kValueTokens where that gives kValueBlocks
-// workgroups, else kValueFew (one token of each of 64 sequences: 3.7 us with 8,
-// 5.2 with 16, 9.0 with 64).
+// Tokens per workgroup of values: kValueTokens, halved to kValueFew at least while
+// that gives fewer than kValueBlocks workgroups (one token of each of 64
+// sequences: 3.7 us with 8, 5.2 with 16, 9.0 with 64; 4,000 tokens of 40 heads of
+// 128: 37.3 with 64, 46.6 with 8; 1,000 tokens of 24 heads of 64: 6.7 with 16, 7.9
+// with 8, 8.9 with 64).
 constexpr int kValueFew = 8;
-constexpr long kValueBlocks = 512;
+constexpr long kValueBlocks = 256;
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -226,8 +228,8 @@ static hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
     while ((long)a.tokens * ((rows + hb - 1) / hb) > SLOTS && hb < rows && hb < kAppendMost) hb *= 2;
     // A launch takes at most 2^32 - 1 threads.
     while ((long)a.tokens * ((rows + hb - 1) / hb) > (1L << 23) * TEAMS && hb < rows) hb *= 2;
-    const long full = ((long)a.tokens + kValueTokens - 1) / kValueTokens * a.c.kv_heads;
-    const int vt = full >= kValueBlocks ? kValueTokens : kValueFew;
+    int vt = kValueTokens;
+    while (vt > kValueFew && ((long)a.tokens + vt - 1) / vt * a.c.kv_heads < kValueBlocks) vt /= 2;
     const long value_blocks = ((long)a.tokens + vt - 1) / vt * a.c.kv_heads;
     const long teams = (long)a.tokens * ((rows + hb - 1) / hb);
     const long grid = value_blocks + (teams + TEAMS - 1) / TEAMS;
