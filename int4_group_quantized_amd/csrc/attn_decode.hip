@@ -195,7 +195,7 @@ __device__ __forceinline__ h8 load_h8(const uint16_t* p) {
     return __builtin_bit_cast(h8, *reinterpret_cast<const u4*>(p));
 }
 
-template <int D, bool EXTRA>
+template <int D, int OPTIONS>
 __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_kernel(AttnArgs a, int target) {
     constexpr int OP = D + 4;  // pitch of a row of partial outputs in LDS
     __shared__ float part_o[kDecodeWaves][16][OP];
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
             if (n >= nrows) qf[s] = (h8)(_Float16)0.0f;
         }
     }
-    const ScoreParams sp = score_params<EXTRA>(a, head0 + (n < nrows ? n : 0));
+    const ScoreParams sp = score_params<OPTIONS>(a, head0 + (n < nrows ? n : 0));
 
     f4 acc[D / 16];
 #pragma unroll
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = kb + 32 * (u >> 1) + 8 * g + 4 * (u & 1) + i;
-                float x = score<EXTRA>(s[u][i], sp, key - (len - 1));
+                float x = score<OPTIONS>(s[u][i], sp, key - (len - 1));
                 if (!whole) x = key >= start && key < len && id.v[u >> 1] >= 0 ? x : Q4_NEG_INF;
                 s[u][i] = x;
                 top = top_of(top, x);
@@ -442,13 +442,13 @@ static hipError_t launch_decode(const AttnArgs& a, hipStream_t st) {
     const int target = decode_target(pairs);
     const long most = ((long)a.max_length + kTileKeys * decode_least(D) - 1) / (kTileKeys * decode_least(D));
     const long grid = (long)target + a.rows < most * a.rows ? (long)target + a.rows : most * a.rows;
-    const bool extra = a.softcap > 0.0f || a.slopes;
     const dim3 blocks(pairs, (unsigned)(grid < kDecodeGridY ? grid : kDecodeGridY),
                       (unsigned)((grid + kDecodeGridY - 1) / kDecodeGridY));
-    if (extra)
-        hipLaunchKernelGGL((attn_decode_kernel<D, true>), blocks, dim3(kDecodeThreads), 0, st, a, target);
-    else
-        hipLaunchKernelGGL((attn_decode_kernel<D, false>), blocks, dim3(kDecodeThreads), 0, st, a, target);
+    const int options = attn_options(a);
+    auto kernel = options == kNoOptions ? &attn_decode_kernel<D, kNoOptions>
+                  : options == kOptions ? &attn_decode_kernel<D, kOptions>
+                                        : &attn_decode_kernel<D, kLargeCapOptions>;
+    hipLaunchKernelGGL(kernel, blocks, dim3(kDecodeThreads), 0, st, a, target);
     return hipGetLastError();
 }
 

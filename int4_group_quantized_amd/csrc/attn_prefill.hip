@@ -268,14 +268,14 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // the wave starts its rows again here, after the fast loop and with nothing of it
 // live, because the same handling inside that loop cost it 100 registers
 // (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
-template <int D, bool EXTRA, int SHARE>
+template <int D, int OPTIONS, int SHARE>
 __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
                                                         int split, int kvh, int wave, int k_begin, int k_end) {
     constexpr int OUT = D / (2 * SHARE);  // output dimensions of a lane
     const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
     const int o0 = (2 * (wave % SHARE) + (lane >> 5)) * OUT;
     const PrefillRow q = prefill_row(a, it, prefix, kvh, wave / SHARE * 32 + n);
-    const ScoreParams sp = score_params<EXTRA>(a, q.head);
+    const ScoreParams sp = score_params<OPTIONS>(a, q.head);
     const _Float16* qp = reinterpret_cast<const _Float16*>(a.q) + ((size_t)q.token * a.heads + q.head) * D + d0;
     const int* row = a.c.table + (size_t)it.s * a.c.cols;
     const int pmask = (1 << a.c.shift) - 1;
@@ -295,7 +295,7 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
         for (int i = 0; i < D / 2; ++i) dot = __builtin_fmaf((float)qp[i], (float)kp[i], dot);
         dot += __shfl_xor(dot, 32, 64);
         if (key < q.see.lo || key >= q.see.hi) continue;
-        const float s = score<EXTRA>(dot, sp, key - q.pos);
+        const float s = score<OPTIONS>(dot, sp, key - q.pos);
         const float m_new = fmaxf(m, s), base = m_new == Q4_NEG_INF ? 0.0f : m_new;
         const float f = exp2_hw(m - base), p = exp2_hw(s - base);
         l = l * f + p;
@@ -371,10 +371,11 @@ __device__ __forceinline__ void lds_meet() {
     asm volatile("" ::: "memory");
 }
 
-template <int D, bool EXTRA, int ROWS>
+template <int D, int OPTIONS, int ROWS>
 __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 64 ? 1 : 2)
     attn_prefill_kernel(AttnArgs a, int tile0) {
     constexpr int SHARE = prefill_share(D, ROWS), THREADS = prefill_threads(D, ROWS), WAVES = THREADS / 64;
+    constexpr bool EXTRA = OPTIONS != kNoOptions;
     constexpr int KEYS = 2 / SHARE;                 // blocks of 32 keys of a wave
     constexpr int DIMS = D / (32 * SHARE);          // and of 32 output dimensions
     constexpr int C = D / 8;                        // 16-byte chunks of a K row
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
             if (!live) qf[s] = (h8)(_Float16)0.0f;
         }
     }
-    const ScoreParams sp = score_params<EXTRA>(a, head);
+    const ScoreParams sp = score_params<OPTIONS>(a, head);
     const int pmask = (1 << a.c.shift) - 1;
     const int* row = a.c.table + (size_t)it.s * a.c.cols;
 
@@ -655,11 +656,11 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
             // (scale > 0), and scale and maximum enter the exponent in one
             // multiply-add.
             if constexpr (EXTRA) {
-                if (a.softcap > 0.0f) {
+                if (OPTIONS == kLargeCapOptions || a.softcap > 0.0f) {
 #pragma unroll
                     for (int b = 0; b < KEYS; ++b)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) s[b][i] = capped(s[b][i], sp);
+                        for (int i = 0; i < 16; ++i) s[b][i] = capped<OPTIONS == kLargeCapOptions>(s[b][i], sp);
                 } else {
 #pragma unroll
                     for (int b = 0; b < KEYS; ++b)
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) any_found |= shared.found[w];
     if (any_found) {
-        prefill_rows_one_by_one<D, EXTRA, SHARE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
+        prefill_rows_one_by_one<D, OPTIONS, SHARE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
     if constexpr (SHARE > 1) l += shared.sum[wave ^ 1][n];
@@ -830,7 +831,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     store_joined(join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits), a.out + r * D);
 }
 
-template <int D, bool EXTRA, int ROWS>
+template <int D, int OPTIONS, int ROWS>
 static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     constexpr size_t image = 2 * kTileKeys * D * sizeof(uint16_t);
     constexpr size_t behind = sizeof(PrefillShared<prefill_threads(D, ROWS) / 64, (prefill_share(D, ROWS) > 1)>);
@@ -841,8 +842,8 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const bool two = prefill_threads(D, ROWS) == 256 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
     const int fit = (int)(((two ? dev.max_lds / 2 : dev.max_lds) - behind) / image);
     a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
-    auto kernel = &attn_prefill_kernel<D, EXTRA, ROWS>;
-    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, EXTRA, ROWS>>::value[dev.device];
+    auto kernel = &attn_prefill_kernel<D, OPTIONS, ROWS>;
+    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, OPTIONS, ROWS>>::value[dev.device];
     if (!ready.load(std::memory_order_acquire)) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
@@ -854,12 +855,20 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
-        hipLaunchKernelGGL((attn_prefill_kernel<D, EXTRA, ROWS>), grid, dim3(prefill_threads(D, ROWS)), a.images * image + behind,
+        hipLaunchKernelGGL((attn_prefill_kernel<D, OPTIONS, ROWS>), grid, dim3(prefill_threads(D, ROWS)), a.images * image + behind,
                            st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+template <int D, int OPTIONS>
+static hipError_t launch_rows(const AttnArgs& a, int rows, const DeviceInfo& dev, hipStream_t st) {
+    if constexpr (D != 96) {  // three blocks of 32 dimensions do not share out
+        if (rows == 64) return launch_tiles<D, OPTIONS, 64>(a, dev, st);
+    }
+    return launch_tiles<D, OPTIONS, 128>(a, dev, st);
 }
 
 template <int D>
@@ -877,12 +886,12 @@ static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStre
     a.splits = plan.splits;
     a.tile = prefill_tokens(plan.rows, a.group);
     a.inv_tile = 1.0f / (float)a.tile;
-    const bool extra = a.softcap > 0.0f || a.slopes;
     hipError_t e = hipSuccess;
-    if constexpr (D != 96) {  // three blocks of 32 dimensions do not share out
-        if (plan.rows == 64) e = extra ? launch_tiles<D, true, 64>(a, dev, st) : launch_tiles<D, false, 64>(a, dev, st);
+    switch (attn_options(a)) {
+        case kNoOptions: e = launch_rows<D, kNoOptions>(a, plan.rows, dev, st); break;
+        case kOptions: e = launch_rows<D, kOptions>(a, plan.rows, dev, st); break;
+        case kLargeCapOptions: e = launch_rows<D, kLargeCapOptions>(a, plan.rows, dev, st); break;
     }
-    if (plan.rows == 128) e = extra ? launch_tiles<D, true, 128>(a, dev, st) : launch_tiles<D, false, 128>(a, dev, st);
     if (e != hipSuccess || a.splits == 1) return e;
     const long rows = (long)a.rows * a.heads;
     hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);

@@ -146,36 +146,60 @@ __device__ __forceinline__ void store_joined(const JoinedRow<D>& r, uint16_t* ou
     }
 }
 
+// The kernels' instantiations by what their scores need: scale only, a cap or a
+// bias, a large cap (and perhaps a bias).
+constexpr int kNoOptions = 0, kOptions = 1, kLargeCapOptions = 2;
+constexpr float kLargeCap = 64.0f;  // see capped
+inline int attn_options(const AttnArgs& a) {
+    return a.softcap > kLargeCap ? kLargeCapOptions : a.softcap > 0.0f || a.slopes ? kOptions : kNoOptions;
+}
+
 // A dot product as a base-2 score: scale * log2(e) * dot, or with the options'
 // cap and bias.
 struct ScoreParams {
     float scale2;  // scale * log2(e)
-    float cap_in;  // 2 log2(e) * scale / softcap
+    float cap_in;  // 2 log2(e) * scale / softcap, finite
     float cap2;    // softcap * log2(e)
     float slope2;  // slope * log2(e)
 };
 
-template <bool EXTRA>
+template <int OPTIONS>
 __device__ __forceinline__ ScoreParams score_params(const AttnArgs& a, int head) {
     ScoreParams p;
     p.scale2 = a.scale * kLog2e;
-    p.cap_in = EXTRA ? 2.0f * kLog2e * a.scale / a.softcap : 0.0f;  // without a cap unused
+    // Held finite, so that under the smallest caps a product of zero stays zero;
+    // without a cap unused.
+    p.cap_in = OPTIONS != kNoOptions ? fminf(2.0f * kLog2e * a.scale / a.softcap, __FLT_MAX__) : 0.0f;
     p.cap2 = a.softcap * kLog2e;
-    p.slope2 = EXTRA && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
+    p.slope2 = OPTIONS != kNoOptions && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
     return p;
 }
 
-// softcap tanh(scale dot / softcap) log2(e), from tanh(x) = 1 - 2 / (e^(2x) + 1):
-// its absolute error is about 2^-23, so the score's is about softcap * 2^-23.
+// softcap tanh(x) log2(e), x = scale dot / softcap, from tanh(x) = 1 - 2 / (e^(2x)
+// + 1): off by a few 2^-23 whatever x is, so the score by softcap times that,
+// 2.3e-5 under a cap of 64, a twentieth of the weights' rounding.  Under larger
+// caps it would pass the scores themselves (0.1 under a cap of 10^6), so LARGE
+// takes the series x - x^3/3 + 2x^5/15 below |2 log2(e) x| = 0.33, off by 2^-22 of x
+// there; above, the first form is off by less than 2^-18 of x.  Both forms for every
+// cap: 4,096 tokens of 16 heads of 128 148 us, of 64 127; one 121 and 93.  Chosen in
+// the kernel instead of by its instantiation: with a bias only 123 and 111 us.
+template <bool LARGE>
 __device__ __forceinline__ float capped(float dot, const ScoreParams& p) {
-    return __builtin_fmaf(-2.0f * p.cap2, __builtin_amdgcn_rcpf(exp2_hw(dot * p.cap_in) + 1.0f), p.cap2);
+    const float z = dot * p.cap_in;
+    const float far = __builtin_fmaf(-2.0f * p.cap2, __builtin_amdgcn_rcpf(exp2_hw(z) + 1.0f), p.cap2);
+    if constexpr (!LARGE) return far;
+    constexpr float A = 1.0f / (3.0f * 4.0f * kLog2e * kLog2e);
+    constexpr float B = 2.0f / (15.0f * 16.0f * kLog2e * kLog2e * kLog2e * kLog2e);
+    const float y = dot * p.scale2, t = z * z;
+    return __builtin_fabsf(z) < 0.33f ? __builtin_fmaf(y, t * __builtin_fmaf(t, B, -A), y) : far;
 }
 
 // distance = key position - query position
-template <bool EXTRA>
+template <int OPTIONS>
 __device__ __forceinline__ float score(float dot, const ScoreParams& p, int distance) {
-    if constexpr (!EXTRA) return dot * p.scale2;
-    const float s = p.cap2 > 0.0f ? capped(dot, p) : dot * p.scale2;
+    if constexpr (OPTIONS == kNoOptions) return dot * p.scale2;
+    constexpr bool LARGE = OPTIONS == kLargeCapOptions;
+    const float s = LARGE || p.cap2 > 0.0f ? capped<LARGE>(dot, p) : dot * p.scale2;
     return __builtin_fmaf(p.slope2, (float)distance, s);
 }
 
