@@ -309,7 +309,7 @@ Q4_API q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens
  * weights enter the second product as fp16 numbers in [0, 1], out is rounded
  * once to fp16.  A query that sees nothing gives zeros.  What a masked
  * position or an absent page holds never reaches a result, NaN included.
- *   scale > 0; softcap >= 0 (0: none); window >= 0 (0: none).
+ *   scale > 0; softcap >= 0 (0: none); both finite; window >= 0 (0: none).
  */
 typedef struct q4g128_attn_options {
     float scale;

@@ -3,6 +3,7 @@
 // launchers and status reporting.
 #include "q4g128.h"
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -169,7 +170,9 @@ q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const
         max_length > cache->table_cols * cache->page)
         return Q4_ESHAPE;
     // written so that NaN fails
-    if (!(o->scale > 0.0f) || !(o->softcap >= 0.0f) || o->window < 0 || (o->prefix && o->window > 0)) return Q4_EINVAL;
+    if (!(o->scale > 0.0f && o->scale <= FLT_MAX) || !(o->softcap >= 0.0f && o->softcap <= FLT_MAX) || o->window < 0 ||
+        (o->prefix && o->window > 0))
+        return Q4_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(o->slopes, 4) ||
         !aligned(o->prefix, 4) || !aligned(workspace, 16))
         return Q4_EALIGN;
