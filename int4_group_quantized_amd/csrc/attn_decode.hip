@@ -312,17 +312,21 @@ __global__ void __launch_bounds__(kDecodeThreads, D <= 128 ? 2 : 1) attn_decode_
         const float m_new = fmaxf(m, top);
         const float base = m_new == Q4_NEG_INF ? 0.0f : m_new;
         const float f = exp2_hw(m - base);
+        // The weights are summed as they enter the second product, rounded: they then
+        // sum to one, and the mean of equal values is that value.
         h8 pf[2];
-        float sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p = exp2_hw(s[u][i] - base);
-                sum += p;
-                pf[u >> 1][4 * (u & 1) + i] = (_Float16)p;
-            }
+            for (int i = 0; i < 4; ++i) pf[u >> 1][4 * (u & 1) + i] = (_Float16)exp2_hw(s[u][i] - base);
         }
+        const h2 one = {(_Float16)1.0f, (_Float16)1.0f};
+        float sum = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum = __builtin_amdgcn_fdot2((h2){pf[h][2 * e], pf[h][2 * e + 1]}, one, sum, false);
         l = l * f + sum;
         m = m_new;
         if (!whole) {
