@@ -750,9 +750,14 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                         pf[1] = as_h8(shared.weights[wave ^ 1][1][lane]);
                         if (__any(theirs != m)) {
                             follow(fmaxf(m, theirs));
-                            const _Float16 f = (_Float16)part_weight(theirs, m);
-                            pf[0] *= f;
-                            pf[1] *= f;
+                            // In two factors: weights reach 2^8, so that under a single one, which
+                            // fp16 ends at 2^-24, weights of up to 2^-17 would be lost while their
+                            // sum stays.  Where nothing is seen the weights are zeros.
+                            const float apart = theirs == Q4_NEG_INF ? 0.0f : theirs - m;
+                            const float near = fmaxf(apart, -14.0f);
+                            const _Float16 f = (_Float16)exp2_hw(near), f2 = (_Float16)exp2_hw(apart - near);
+                            pf[0] = pf[0] * f * f2;
+                            pf[1] = pf[1] * f * f2;
                         }
                     }
                 }

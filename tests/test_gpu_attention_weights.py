@@ -1,9 +1,9 @@
-"""The softmax weights' own arithmetic: what they sum to."""
+"""The softmax weights' own arithmetic: what they sum to, and what small ones keep."""
 import numpy as np
 import pytest
 
 from gpu_helpers import note
-from test_gpu_attention import Pool, dev, i32  # noqa: F401  (dev: fixture)
+from test_gpu_attention import H, TINY, Pool, dev, i32  # noqa: F401  (dev: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,40 @@ def test_equal_values_under_weights_rounded_alike(dev, dim, value, off, length):
     for out in (q4.q4g128_attn_decode(qd, *c, n, scale=float(np.log(2.0))),
                 q4.q4g128_attn_prefill(qd, *c, i32([0, 1], dev), n, scale=float(np.log(2.0)))):
         assert torch.all(out == np.float16(value)), (out.float() - value).abs().max()
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("tokens,many", [(5, False), (5, True), (40, True)])
+@pytest.mark.parametrize("low_half", [0, 1])
+def test_small_weights_beside_a_jump_of_the_maximum(dev, dim, tokens, many, low_half):  # noqa: F811
+    """One half of a tile's keys lies 2^7.75 above the running maximum, the other 2^24.9: the first half's weights,
+    2^-17.15 of the largest, stay (weights are rounded to 2^-25 of it), for the output dimensions of either wave
+    where two share the rows.  40 tokens beside many empty sequences: the form of 128 rows."""
+    rng = np.random.default_rng(dim)
+    empty = [0] * (80 if many else 0)
+    page, kv = 64, 8 if many else 1
+    n = 128 + tokens  # a tile of zeros, the tile with the jump, and the tokens themselves
+    score = np.full(n, -60.0)
+    score[:64] = 0.0
+    half = slice(64, 96) if low_half == 0 else slice(96, 128)
+    score[64:128] = 24.9
+    score[half] = 7.75
+    value = np.zeros((n, dim))
+    value[half] = rng.uniform(20000, 60000, (32, dim))
+    pool = Pool(rng, [n] + empty, kv, page, dim)
+    for j in range(n):
+        pool.k[pool.table[0, j // page], :, j % page] = 0
+        pool.k[pool.table[0, j // page], :, j % page, 0] = score[j]
+        pool.v[pool.table[0, j // page], :, :, j % page] = value[j]
+    q = np.zeros((tokens, kv, dim), dtype=np.float16)
+    q[:, :, 0] = 1
+    scale = np.log(2.0)
+    starts = [0] + [tokens] * (len(empty) + 1)
+    s = np.float64(score.astype(np.float16))
+    v = np.float64(value.astype(np.float16))
+    w = 2.0 ** (s[:128] - s[:128].max())  # the tokens' own positions weigh 2^-85
+    want = w @ v[:128] / w.sum()
+    err = H * want + 2 * H * want + n * TINY * v.max() / w.sum()
+    out = q4.q4g128_attn_prefill(torch.from_numpy(q).to(dev), *pool.on(dev), i32(starts, dev), i32([n] + empty, dev),
+                                 scale=float(scale)).float().cpu().numpy()
+    assert np.all(np.abs(out - want) <= err), (np.abs(out - want) / err).max()
