@@ -5,7 +5,7 @@ shapes and contiguity, then passes raw device pointers, sizes and the
 current HIP stream of the tensors' device to the C ABI of the same name
 (include/q4g128.h).  All arithmetic runs in the library's HIP kernels; there
 is no fallback path.  Importing this package fails loudly if the library is
-not built.
+not built, and the cache and attention calls if their compiled binding is not.
 
 PyTorch provides device memory and streams: fp16 arguments are torch.float16
 tensors (the C ABI receives their bit patterns), codes/packed are torch.uint8,
@@ -120,12 +120,25 @@ def _load():
 
 _lib = _load()
 
-# The cache and attention calls' checks and calls are compiled (csrc/binding.cpp);
-# their module links to the library loaded above.
+
+class _NoBinding:
+    """In place of the compiled module: its calls say why it could not be loaded."""
+
+    def __init__(self, error: ImportError):
+        self.error = error
+
+    def __getattr__(self, call):
+        raise ImportError(f"q4g128_{call}: {self.error}: build the binding with "
+                          "`python int4_group_quantized_amd/build.py`") from self.error
+
+
+# The cache and attention calls' checks and calls are compiled (csrc/binding.cpp),
+# for one torch and Python; their module links to the library loaded above.
+# The products do without it.
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError(f"{e}: build the binding with `python int4_group_quantized_amd/build.py`") from e
+    _binding = _NoBinding(e)
 
 
 def library() -> ctypes.CDLL:
