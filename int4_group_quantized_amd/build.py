@@ -1,5 +1,5 @@
-"""Build libq4g128.so (the C-ABI library) and the compiled part of the Python
-binding in-tree with hipcc for gfx950.
+"""Build libq4g128.so (the C-ABI library) and, where torch is installed, the
+compiled part of the Python binding in-tree with hipcc for gfx950.
 
 Usage:  python int4_group_quantized_amd/build.py   (or call build_library()).
 Run it as a script, not as a module of the package: importing the package
@@ -97,12 +97,30 @@ def _link(objs, name: str, path: str, verbose: bool) -> None:
     os.replace(tmp, path)
 
 
+def _torch_root():
+    """torch's directory if it has the C++ headers, else None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    return root if os.path.exists(os.path.join(root, "include", "ATen", "ATen.h")) else None
+
+
 def _build_binding(verbose: bool) -> None:
     import sysconfig
 
+    root = _torch_root()
+    if root is None:
+        # The C-ABI library needs no torch.  A binding of an earlier build would be
+        # of other sources.
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+        print("torch or its C++ headers are not here: the Python binding of the cache and attention calls "
+              "is not built", flush=True)
+        return
     import torch
 
-    root = os.path.dirname(os.path.abspath(torch.__file__))
     include = os.path.join(root, "include")
     obj = os.path.join(BUILD_DIR, BINDING_SOURCE + ".o")
     _run([hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
@@ -130,7 +148,8 @@ def _run(cmd, what: str, verbose: bool) -> None:
 
 
 def build_library(verbose: bool = False) -> str:
-    """Compile and link libq4g128.so, the diagnostics library and the binding; returns the first one's path."""
+    """Compile and link libq4g128.so, the diagnostics library and, if torch is there, the binding; returns the
+    first one's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = SOURCES + DIAG_SOURCES
     with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
