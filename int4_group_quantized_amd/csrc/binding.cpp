@@ -122,6 +122,17 @@ at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, const Sa
     return t;
 }
 
+// Whether the elements of a page follow each other.  The stride of a size of one
+// means nothing.
+bool page_contiguous(const at::Tensor& t) {
+    int64_t next = 1;
+    for (int i = 3; i >= 1; --i) {
+        if (t.size(i) != 1 && t.stride(i) != next) return false;
+        next *= t.size(i);
+    }
+    return true;
+}
+
 // The cache descriptor.  Pages may be strided (a slice of a larger pool); each
 // page itself is contiguous.
 q4g128_kv_cache cache_of(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table) {
@@ -136,8 +147,7 @@ q4g128_kv_cache cache_of(const at::Tensor& k, const at::Tensor& v, const at::Ten
     if (v.size(0) != pages || v.size(1) != heads || v.size(2) != dim || v.size(3) != page)
         value_error("v_cache must have shape %s (got %s)", shape_text({pages, heads, dim, page}).c_str(),
                                 shape_text(v.sizes()).c_str());
-    if (k.stride(1) != page * dim || k.stride(2) != dim || k.stride(3) != 1 || v.stride(1) != page * dim ||
-        v.stride(2) != page || v.stride(3) != 1)
+    if (!page_contiguous(k) || !page_contiguous(v))
         value_error("each page of k_cache and v_cache must be contiguous");
     if (table.dim() != 2) value_error("table must be [sequences][table_cols]");
     check(table, "table", at::kInt, table.sizes());
@@ -147,8 +157,9 @@ q4g128_kv_cache cache_of(const at::Tensor& k, const at::Tensor& v, const at::Ten
     c.v = static_cast<uint16_t*>(v.data_ptr());
     c.table = static_cast<const int32_t*>(table.data_ptr());
     c.pages = pages;
-    c.k_stride = k.stride(0);
-    c.v_stride = v.stride(0);
+    // One page has no next page: any stride will do.
+    c.k_stride = pages > 1 ? k.stride(0) : heads * page * dim;
+    c.v_stride = pages > 1 ? v.stride(0) : heads * page * dim;
     c.sequences = table.size(0);
     c.table_cols = table.size(1);
     c.kv_heads = (int32_t)heads;
