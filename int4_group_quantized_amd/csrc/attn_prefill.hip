@@ -324,11 +324,16 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
 // 16 bytes per lane from memory into LDS: lane i's to byte `to` + 16 i.  In
 // assembly because the compiler, which sees that images follow each other in
 // one array, would let every LDS read wait for all such loads under way; the
-// waits are wait_and_meet's.  The instruction has no destination register, and
-// nothing else in these kernels uses m0.
+// waits are wait_and_meet's.  The instruction has no destination register.  m0, a
+// reserved register, cannot be declared as overwritten; nothing else in these
+// kernels uses it, which tests/test_attention_assembly.py checks.
 // First form: from base + the lane's offset in bytes, base the same in all lanes.
+// A vector instruction may have written base just before (a value read from a
+// lane, a spilled one too), and the compiler does not look into the assembly: the
+// five wait states that a memory operation then needs are the move's and the
+// no-operation's.  They cost 0.3% of 8,192 tokens' time, 1.6% at dim 64.
 __device__ __forceinline__ void load_lds(const uint16_t* base, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(to), "v"(offset), "s"(base)
                  : "memory");
