@@ -305,8 +305,10 @@ Q4_API q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens
  *     if slopes != NULL:        s_j += slopes[head] * (j - p)
  *     out = sum_j softmax(s)_j v_j
  * It sees j <= p, with window > 0 only j > p - window, and in the prompt call
- * also every j < prefix[s].  Scores, softmax statistics and sums are fp32; the
- * weights enter the second product as fp16 numbers in [0, 1], out is rounded
+ * also every j < prefix[s].  Scores, softmax statistics and sums are fp32.  The
+ * weights enter the second product rounded to fp16, in units of 2 to a running
+ * maximum of the base-2 scores: at most 1 in the decode call, at most 2^8 in the
+ * prompt call, whose maximum may lag; they are summed as rounded.  out is rounded
  * once to fp16.  A query that sees nothing gives zeros.  What a masked
  * position or an absent page holds never reaches a result, NaN included.
  *   scale > 0; softcap >= 0 (0: none); both finite; window >= 0 (0: none).
