@@ -264,10 +264,10 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // other, never touching what a row does not see: for tiles that hold infinities
 // or NaN in masked places, where the matrix products would multiply them by
 // zero.  Lanes n and n + 32 share row n, half the dimensions each (waves that share
-// it split the output dimensions too).  Far slower;
-// the wave starts its rows again here, after the fast loop and with nothing of it
-// live, because the same handling inside that loop cost it 100 registers
-// (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
+// it split the output dimensions too).  Far slower; all waves of a workgroup that
+// has met such a tile start their rows again here, after the fast loop and with
+// nothing of it live, because the same handling inside that loop cost it 100
+// registers (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
 template <int D, int OPTIONS, int SHARE>
 __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
                                                         int split, int kvh, int wave, int k_begin, int k_end) {
