@@ -226,13 +226,13 @@ static hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
     int hb = 1;
     constexpr long SLOTS = kAppendWaves * 64 * TEAMS / kAppendThreads;
     while ((long)a.tokens * ((rows + hb - 1) / hb) > SLOTS && hb < rows && hb < kAppendMost) hb *= 2;
-    // A launch takes at most 2^32 - 1 threads.
-    while ((long)a.tokens * ((rows + hb - 1) / hb) > (1L << 23) * TEAMS && hb < rows) hb *= 2;
     int vt = kValueTokens;
     while (vt > kValueFew && ((long)a.tokens + vt - 1) / vt * a.c.kv_heads < kValueBlocks) vt /= 2;
     const long value_blocks = ((long)a.tokens + vt - 1) / vt * a.c.kv_heads;
     const long teams = (long)a.tokens * ((rows + hb - 1) / hb);
     const long grid = value_blocks + (teams + TEAMS - 1) / TEAMS;
+    // A launch takes at most 2^32 - 1 threads; rows and queries for more than that
+    // would take over 288 GB.
     if (grid > (1L << 24) - 1) return hipErrorInvalidValue;
     hipLaunchKernelGGL((rope_append_kernel<D>), dim3((unsigned)grid), dim3(kAppendThreads), 0, st, a,
                        (int)value_blocks, vt, hb);
