@@ -29,10 +29,11 @@
 // at dim 64 and 128, one workgroup per CU: 5 to 15% slower than by four.
 //
 // Bound by the matrix cores and the softmax's vector work together: 8,192 tokens
-// of 32 heads of 128 (8 kv heads, 550 GFLOP) take 553 us, 994 TFLOP/s, matrix
-// cores busy 55% of the cycles; without either product, the loads or the
-// exponentials it would be 2 to 15% less, with half of the LDS operand reads 3%.
-// Few tokens are bound by latency: 34 tokens take 6.4 us.
+// of 32 heads of 128 (8 kv heads, 550 GFLOP) take 555 us call after call, 990
+// TFLOP/s (580 to 670 in the first calls after a pause, while the clock settles);
+// a counter run had the matrix cores busy 53% of the cycles.  Without either
+// product, the loads or the exponentials it would be 2 to 15% less, with half of
+// the LDS operand reads 3%.  Few tokens are bound by latency: 34 tokens take 6.4 us.
 //
 // Tiles go straight from memory into LDS images, one ahead with two images (two
 // workgroups per CU) and up to three ahead with four (one per CU, where there are

@@ -7,8 +7,9 @@
 // to fp16.  Values are rounded and written only.
 //
 // Memory bound: a token reads (heads + 2 kv_heads) * dim fp32 values and writes
-// as many fp16 ones.  8,192 tokens of 48 heads of 128 (302 MB) take 62.7 us, 4.8
-// TB/s; a 4 GiB copy runs at 4.6.  One token takes 2.5 us, bound by the launch.
+// as many fp16 ones.  8,192 tokens of 48 heads of 128 (302 MB) take 62.6 us, 4.8
+// TB/s; a 4 GiB copy runs at 4.6.  One token takes 2.6 us a launch among others of
+// a graph (3.2 from start to end in a kernel trace), bound by the launch.
 //
 // Angles: position * inv_freq is formed in turns in 64 bits and reduced to
 // [-1/2, 1/2] before it becomes a float.  In fp32 the product alone is off by
