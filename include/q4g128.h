@@ -82,6 +82,7 @@ typedef int32_t q4_status;
 #define Q4G128_MAX_GROUP 64
 #define Q4G128_MAX_TOKENS 1048576
 #define Q4G128_MAX_SEQUENCES 65536
+#define Q4G128_MAX_DRAFT 64
 #define Q4G128_ATTN_COUNTER_BYTES 4096
 
 /*
@@ -237,8 +238,8 @@ Q4_API q4_status q4g128_gemv_int8(const int8_t* q, const uint16_t* scales, const
                            float* y, int64_t n, int64_t k, void* stream);
 
 /*
- * Attention between the fused projection and o_proj: three calls over one
- * paged key-value cache.
+ * Attention between the fused projection and o_proj: calls over one paged
+ * key-value cache.
  *
  * The cache is a pool of pages of `page` token positions each; page number
  * table[s][i] holds positions i*page .. i*page + page-1 of sequence s.
@@ -299,16 +300,28 @@ Q4_API q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens
                              const uint16_t* k_norm, float eps, uint16_t* q, void* stream);
 
 /*
- * What the two attention calls compute for a query at position p of its
+ * q4g128_rope_append_slots -- the same with the cache position apart from the
+ * rotary one: a head is turned by positions[t] and written to position slots[t]
+ * (a tree's drafted tokens of one depth share the first and not the second).
+ */
+Q4_API q4_status q4g128_rope_append_slots(const float* qkv, int64_t ld, int64_t tokens, int32_t heads,
+                             const q4g128_kv_cache* cache, const int32_t* seq,
+                             const int32_t* positions, const int32_t* slots, const float* inv_freq,
+                             int32_t rot, int32_t interleaved, float mscale, const uint16_t* q_norm,
+                             const uint16_t* k_norm, float eps, uint16_t* q, void* stream);
+
+/*
+ * What the attention calls compute for a query at position p of its
  * sequence, over the positions j that it sees:
  *     s_j = scale * (q . k_j);  if softcap > 0: s_j = softcap * tanh(s_j / softcap)
  *     if slopes != NULL:        s_j += slopes[head] * (j - p)
  *     out = sum_j softmax(s)_j v_j
  * It sees j <= p, with window > 0 only j > p - window, and in the prompt call
- * also every j < prefix[s].  Scores, softmax statistics and sums are fp32.  The
+ * also every j < prefix[s]; the tree call says what drafted tokens see.  Scores,
+ * softmax statistics and sums are fp32.  The
  * weights enter the second product rounded to fp16, in units of 2 to a running
  * maximum of the base-2 scores: at most 1 in the decode call, at most 2^8 in the
- * prompt call, whose maximum may lag; they are summed as rounded.  out is rounded
+ * others, whose maximum may lag; they are summed as rounded.  out is rounded
  * once to fp16.  A query that sees nothing gives zeros.  What a masked
  * position or an absent page holds never reaches a result, NaN included.
  *   scale > 0; softcap >= 0 (0: none); both finite; window >= 0 (0: none).
@@ -360,6 +373,49 @@ Q4_API q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* c
                              int64_t tokens, int64_t count, int32_t heads,
                              const q4g128_attn_options* options, uint16_t* out,
                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * q4g128_attn_tree -- drafted tokens of one or more sequences: a decode step of
+ * several tokens per sequence, which the cache is read once for.
+ *   q, out [tokens][heads][dim] fp16; rows q_starts[s] .. q_starts[s+1]-1 (int32
+ *   [count + 1], ascending) are the drafted tokens of sequence s, its last cached
+ *   positions: with n of them, drafted token k is position base + k, base =
+ *   lengths[s] - n.  Rows of no sequence are left as they were.
+ *   masks: uint64 [tokens], or NULL.  A token sees every position below base, and
+ *   drafted token k of its sequence where bit k of its mask is set (its own bit
+ *   like any other).  Windows and slopes go by a token's place, base + max(bits set
+ *   among its sequence's tokens, 1) - 1: for a tree's masks (a token's ancestors and
+ *   itself) base + its depth, the position that it is to be turned by; positions below base
+ *   are their own places.  NULL: each token sees those before it, as in
+ *   q4g128_attn_prefill.  No token sees the 65th or a later drafted token of a mask.
+ *   max_new: an upper bound on a sequence's drafted tokens, 1 to Q4G128_MAX_DRAFT;
+ *   it sizes the launch, and rows of later tokens are left as they were.
+ *   options->prefix must be NULL.  max_length, workspace as in q4g128_attn_decode,
+ *   of q4g128_attn_tree_workspace() bytes.
+ */
+Q4_API int64_t q4g128_attn_tree_workspace(int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_new);
+Q4_API q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache,
+                             const int32_t* q_starts, const int32_t* lengths,
+                             const uint64_t* masks, int64_t max_new, int64_t max_length,
+                             int64_t tokens, int64_t count, int32_t heads,
+                             const q4g128_attn_options* options, uint16_t* out, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/*
+ * q4g128_cache_keep -- the accepted tokens of each draft moved together: for i <
+ * n = keep_starts[s+1] - keep_starts[s], position starts[s] + keep[keep_starts[s] +
+ * i] of sequence s becomes position starts[s] + i, keys and values of all kv heads.
+ *   starts int32 [count]: the committed positions of each sequence; keep_starts
+ *   int32 [count + 1], ascending from 0 to total; keep int32 [total], for each
+ *   sequence the numbers of its accepted drafted tokens, strictly ascending from 0 on
+ *   (what other numbers leave in the sequence's positions is unspecified).  A token whose
+ *   old or new position is outside the table or has no page is not moved.  No two
+ *   sequences of a call may share a page that a token is moved in.
+ *   total 0: nothing is enqueued (keep may be NULL).
+ */
+Q4_API q4_status q4g128_cache_keep(const q4g128_kv_cache* cache, const int32_t* starts,
+                             const int32_t* keep_starts, const int32_t* keep, int64_t total,
+                             int64_t count, void* stream);
 
 /* Static, NUL-terminated description of a status code. */
 Q4_API const char* q4g128_status_string(q4_status status);

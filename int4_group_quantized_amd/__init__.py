@@ -32,6 +32,7 @@ MAX_BATCH = 16
 INT8_MAX_K = 8192
 MAX_GROUPED = 65536
 ATTN_COUNTER_BYTES = 4096
+MAX_DRAFT = 64
 
 
 class GemvDesc(ctypes.Structure):
@@ -63,10 +64,14 @@ EXPORTED = (
     "q4g128_gemm_prefill_epilogue",
     "q4g128_gemv_int8",
     "q4g128_rope_append",
+    "q4g128_rope_append_slots",
+    "q4g128_cache_keep",
     "q4g128_attn_decode_workspace",
     "q4g128_attn_decode",
     "q4g128_attn_prefill_workspace",
     "q4g128_attn_prefill",
+    "q4g128_attn_tree_workspace",
+    "q4g128_attn_tree",
     "q4g128_status_string",
     "q4g128_last_hip_error",
 )
@@ -100,6 +105,11 @@ def _load():
     i32, f32 = ctypes.c_int32, ctypes.c_float
     cache, options = ctypes.POINTER(KvCache), ctypes.POINTER(AttnOptions)
     lib.q4g128_rope_append.argtypes = [vp, i64, i64, i32, cache, vp, vp, vp, i32, i32, f32, vp, vp, f32, vp, vp]
+    lib.q4g128_rope_append_slots.argtypes = [vp, i64, i64, i32, cache, vp, vp, vp, vp, i32, i32, f32, vp, vp, f32, vp,
+                                             vp]
+    lib.q4g128_cache_keep.argtypes = [cache, vp, vp, vp, i64, i64, vp]
+    lib.q4g128_attn_tree_workspace.argtypes = [i32, i32, i32, i64]
+    lib.q4g128_attn_tree.argtypes = [vp, cache, vp, vp, vp, i64, i64, i64, i64, i32, options, vp, vp, i64, vp]
     lib.q4g128_attn_decode_workspace.argtypes = [i64, i32, i32]
     lib.q4g128_attn_decode.argtypes = [vp, cache, vp, i64, i64, i32, options, vp, vp, i64, vp]
     lib.q4g128_attn_prefill_workspace.argtypes = [i64, i64, i32, i32, i32, i64]
@@ -107,9 +117,9 @@ def _load():
     for name in ("q4g128_pack", "q4g128_quantize", "q4g128_gemv", "q4g128_gemv_grouped", "q4g128_gemm_small_batch",
                  "q4g128_gemm_prefill",
                  "q4g128_gemv_int8", "q4g128_gemm_prefill_epilogue", "q4g128_rope_append", "q4g128_attn_decode",
-                 "q4g128_attn_prefill"):
+                 "q4g128_attn_prefill", "q4g128_rope_append_slots", "q4g128_cache_keep", "q4g128_attn_tree"):
         getattr(lib, name).restype = ctypes.c_int32
-    for name in ("q4g128_attn_decode_workspace", "q4g128_attn_prefill_workspace"):
+    for name in ("q4g128_attn_decode_workspace", "q4g128_attn_prefill_workspace", "q4g128_attn_tree_workspace"):
         getattr(lib, name).restype = ctypes.c_int64
     lib.q4g128_status_string.argtypes = [ctypes.c_int32]
     lib.q4g128_status_string.restype = ctypes.c_char_p
@@ -351,21 +361,22 @@ def _answer(got, where):
 
 
 def q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq=None, q_norm=None, k_norm=None,
-                       eps=1e-6, interleaved=False, mscale=1.0, q=None, stream=None) -> torch.Tensor:
+                       eps=1e-6, interleaved=False, mscale=1.0, q=None, stream=None, slots=None) -> torch.Tensor:
     """Head norm, rotary position and cache write of new tokens; returns q fp16 [T][heads][dim].
 
     qkv: fp32 [T][>= (heads + 2 kv_heads) dim], rows may be strided (a product's output: columns after the
     value heads are left alone).  k_cache fp16 [pages][kv_heads][page][dim], v_cache fp16
     [pages][kv_heads][dim][page], table int32 [sequences][cols]; a page is contiguous, the pages may be a strided
-    slice of a larger pool.  positions int32 [T]; seq int32 [T] (None: token t is of sequence t).  inv_freq fp32
+    slice of a larger pool.  positions int32 [T]; slots int32 [T]: the positions that are written, where they are not
+    those that heads are turned by (drafted tokens of a tree); seq int32 [T] (None: token t is of sequence t).  inv_freq fp32
     [rot / 2] (None: no rotation).  q_norm, k_norm fp16 [dim] or None.
     """
     if stream is not None:
         with torch.cuda.stream(stream):  # new memory is the stream's too
             return q4g128_rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq, q_norm, k_norm,
-                                      eps, interleaved, mscale, q)
+                                      eps, interleaved, mscale, q, slots=slots)
     return _answer(_binding.rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq, q_norm, k_norm,
-                                        eps, interleaved, mscale, q), "q4g128_rope_append")
+                                        eps, interleaved, mscale, q, slots), "q4g128_rope_append")
 
 
 def q4g128_attn_decode_workspace(batch, heads, dim) -> int:
@@ -410,6 +421,41 @@ def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=Non
                                        prefix, max_length, out, workspace)
     return _answer(_binding.attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale, softcap, window, slopes,
                                          prefix, max_length, out, workspace), "q4g128_attn_prefill")
+
+
+def q4g128_attn_tree_workspace(heads, kv_heads, dim, max_new) -> int:
+    """Bytes of workspace that q4g128_attn_tree needs."""
+    return _lib.q4g128_attn_tree_workspace(heads, kv_heads, dim, max_new)
+
+
+def q4g128_attn_tree(q, k_cache, v_cache, table, q_starts, lengths, masks=None, scale=None, softcap=0.0, window=0,
+                     slopes=None, max_new=None, max_length=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens packed over sequences: q fp16 [T][heads][dim] -> out, same shape.
+
+    Rows q_starts[s]..q_starts[s+1]-1 (int32 [S + 1]), at most 64 of a sequence, are the last of its lengths[s] cached
+    positions (int32 [S]).  masks int64 [T]: a token sees every position before its sequence's draft, and drafted
+    token k where bit k of its mask is set (a tree: its ancestors and itself); None: the tokens up to itself.
+    max_new: an upper bound on a sequence's tokens (default: 64, or T).  Other arguments as q4g128_attn_decode.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_attn_tree(q, k_cache, v_cache, table, q_starts, lengths, masks, scale, softcap, window, slopes,
+                                    max_new, max_length, out, workspace)
+    return _answer(_binding.attn_tree(q, k_cache, v_cache, table, q_starts, lengths, masks, scale, softcap, window,
+                                      slopes, max_new, max_length, out, workspace), "q4g128_attn_tree")
+
+
+def q4g128_cache_keep(k_cache, v_cache, table, starts, keep_starts, keep, stream=None) -> None:
+    """Accepted drafted tokens moved together, in place: position starts[s] + keep[i] becomes starts[s] + i.
+
+    starts int32 [S]: the committed positions of each sequence; keep int32 [n]: for sequence s the numbers
+    keep[keep_starts[s]:keep_starts[s + 1]] of its accepted tokens within the draft, strictly ascending; keep_starts
+    int32 [S + 1].
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_cache_keep(k_cache, v_cache, table, starts, keep_starts, keep)
+    _check(_binding.cache_keep(k_cache, v_cache, table, starts, keep_starts, keep), "q4g128_cache_keep")
 
 
 def q4g128_status_string(status: int) -> str:

@@ -11,7 +11,7 @@
 #include <utility>
 #include <vector>
 
-#include "attn.hpp"
+#include "attn_new.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -208,6 +208,42 @@ q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const
     return Q4_OK;
 }
 
+// Row numbers and masks of new tokens, against what a call writes.
+q4_status check_new(const int32_t* q_starts, const uint64_t* masks, int64_t tokens, int64_t count, const void* out,
+                    size_t outbytes, const void* workspace, size_t wsbytes) {
+    if (!aligned(q_starts, 4) || !aligned(masks, 8)) return Q4_EALIGN;
+    const size_t sbytes = (size_t)(count + 1) * 4, mbytes = (size_t)tokens * 8;
+    if (overlaps(out, outbytes, q_starts, sbytes) || overlaps(workspace, wsbytes, q_starts, sbytes) ||
+        (masks && (overlaps(out, outbytes, masks, mbytes) || overlaps(workspace, wsbytes, masks, mbytes))))
+        return Q4_EINVAL;
+    return Q4_OK;
+}
+
+// The rest of the two keep calls' checks, and their launch.  a->c is filled.
+q4_status keep_tokens(q4::KeepArgs* a, const int32_t* starts, const int32_t* keep_starts, const int32_t* keep,
+                      int64_t total, int64_t count, void* stream) {
+    if (!starts || !keep_starts || (!keep && total > 0) || total < 0 || count < 1) return Q4_EINVAL;
+    if (count > Q4G128_MAX_SEQUENCES || count > a->c.sequences || total > Q4G128_MAX_TOKENS) return Q4_ESHAPE;
+    if (!aligned(starts, 4) || !aligned(keep_starts, 4) || !aligned(keep, 4)) return Q4_EALIGN;
+    const size_t kbytes = pool_bytes(a->c, a->c.k_stride), vbytes = a->c.v ? pool_bytes(a->c, a->c.v_stride) : 0;
+    const size_t tbytes = (size_t)a->c.sequences * (size_t)a->c.cols * 4;
+    const void* in[] = {a->c.table, starts, keep_starts, keep};
+    const size_t inbytes[] = {tbytes, (size_t)count * 4, (size_t)(count + 1) * 4, (size_t)total * 4};
+    for (int i = 0; i < 4; ++i)
+        if (in[i] && (overlaps(a->c.k, kbytes, in[i], inbytes[i]) ||
+                      (vbytes > 0 && overlaps(a->c.v, vbytes, in[i], inbytes[i]))))
+            return Q4_EINVAL;
+    if (a->c.v && pools_meet(a->c)) return Q4_EINVAL;
+    if (total == 0) return Q4_OK;
+    a->starts = starts;
+    a->keep_starts = keep_starts;
+    a->keep = keep;
+    a->total = (int)total;
+    a->count = (int)count;
+    hipError_t e = q4::launch_cache_keep(*a, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -352,7 +388,16 @@ q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens, int32
                              const q4g128_kv_cache* cache, const int32_t* seq, const int32_t* positions,
                              const float* inv_freq, int32_t rot, int32_t interleaved, float mscale,
                              const uint16_t* q_norm, const uint16_t* k_norm, float eps, uint16_t* q, void* stream) {
-    if (!qkv || !positions || !q || tokens < 1) return Q4_EINVAL;
+    return q4g128_rope_append_slots(qkv, ld, tokens, heads, cache, seq, positions, positions, inv_freq, rot,
+                                    interleaved, mscale, q_norm, k_norm, eps, q, stream);
+}
+
+q4_status q4g128_rope_append_slots(const float* qkv, int64_t ld, int64_t tokens, int32_t heads,
+                                   const q4g128_kv_cache* cache, const int32_t* seq, const int32_t* positions,
+                                   const int32_t* slots, const float* inv_freq, int32_t rot, int32_t interleaved,
+                                   float mscale, const uint16_t* q_norm, const uint16_t* k_norm, float eps, uint16_t* q,
+                                   void* stream) {
+    if (!qkv || !positions || !slots || !q || tokens < 1) return Q4_EINVAL;
     q4::AppendArgs a;
     q4_status s = check_cache(cache, heads, &a.c);
     if (s != Q4_OK) return s;
@@ -361,20 +406,20 @@ q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens, int32
         ld > INT64_MAX / 8 / tokens)
         return Q4_ESHAPE;
     if ((rot > 0 && !inv_freq) || !(eps >= 0.0f)) return Q4_EINVAL;  // written so that NaN fails
-    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(seq, 4) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
-        !aligned(q_norm, 2) || !aligned(k_norm, 2))
+    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(seq, 4) || !aligned(positions, 4) || !aligned(slots, 4) ||
+        !aligned(inv_freq, 4) || !aligned(q_norm, 2) || !aligned(k_norm, 2))
         return Q4_EALIGN;
     const size_t qbytes = (size_t)tokens * (size_t)heads * (size_t)dim * 2, nbytes = (size_t)dim * 2;
-    const void* in[] = {qkv, seq, positions, inv_freq, q_norm, k_norm};
+    const void* in[] = {qkv, seq, positions, slots, inv_freq, q_norm, k_norm};
     const size_t inbytes[] = {((size_t)(tokens - 1) * (size_t)ld + (size_t)columns) * 4, (size_t)tokens * 4,
-                              (size_t)tokens * 4, (size_t)rot * 2, nbytes, nbytes};
+                              (size_t)tokens * 4, (size_t)tokens * 4, (size_t)rot * 2, nbytes, nbytes};
     if (pools_meet(a.c)) return Q4_EINVAL;
     const size_t kbytes = pool_bytes(a.c, a.c.k_stride), vbytes = pool_bytes(a.c, a.c.v_stride);
     const size_t tbytes = (size_t)a.c.sequences * (size_t)a.c.cols * 4;
     if (hits_cache(a.c, q, qbytes) || overlaps(a.c.k, kbytes, a.c.table, tbytes) ||
         overlaps(a.c.v, vbytes, a.c.table, tbytes))
         return Q4_EINVAL;
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 7; ++i)
         if (in[i] && (overlaps(q, qbytes, in[i], inbytes[i]) || overlaps(a.c.k, kbytes, in[i], inbytes[i]) ||
                       overlaps(a.c.v, vbytes, in[i], inbytes[i])))
             return Q4_EINVAL;
@@ -384,6 +429,7 @@ q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens, int32
     a.heads = heads;
     a.seq = seq;
     a.positions = positions;
+    a.slots = slots;
     a.inv_freq = inv_freq;
     a.rot = rot;
     a.interleaved = interleaved != 0;
@@ -394,6 +440,14 @@ q4_status q4g128_rope_append(const float* qkv, int64_t ld, int64_t tokens, int32
     a.q = q;
     hipError_t e = q4::launch_rope_append(a, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+q4_status q4g128_cache_keep(const q4g128_kv_cache* cache, const int32_t* starts, const int32_t* keep_starts,
+                            const int32_t* keep, int64_t total, int64_t count, void* stream) {
+    q4::KeepArgs a;
+    q4_status s = check_cache(cache, cache ? cache->kv_heads : 0, &a.c);
+    if (s != Q4_OK) return s;
+    return keep_tokens(&a, starts, keep_starts, keep, total, count, stream);
 }
 
 int64_t q4g128_attn_decode_workspace(int64_t batch, int32_t heads, int32_t dim) {
@@ -448,6 +502,36 @@ q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache, c
     s = current_device(&dev);
     if (s != Q4_OK) return s;
     hipError_t e = q4::launch_attn_prefill(a, dev, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+int64_t q4g128_attn_tree_workspace(int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_new) {
+    if (heads < 1 || kv_heads < 1 || max_new < 1) return Q4_EINVAL;
+    if (heads > Q4G128_MAX_HEADS || heads % kv_heads != 0 || heads / kv_heads > Q4G128_MAX_GROUP ||
+        !q4::attn_dim_supported(dim) || max_new > Q4G128_MAX_DRAFT)
+        return Q4_ESHAPE;
+    return q4::attn_tree_workspace(heads, kv_heads, dim, (int)max_new);
+}
+
+q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* q_starts,
+                           const int32_t* lengths, const uint64_t* masks, int64_t max_new, int64_t max_length,
+                           int64_t tokens, int64_t count, int32_t heads, const q4g128_attn_options* options,
+                           uint16_t* out, void* workspace, int64_t workspace_bytes, void* stream) {
+    q4::NewArgs x;
+    if (!q_starts) return Q4_EINVAL;
+    const int64_t need = cache ? q4g128_attn_tree_workspace(heads, cache->kv_heads, cache->dim, max_new) : Q4_EINVAL;
+    if (need < 0) return (q4_status)need;
+    if (options && options->prefix) return Q4_EINVAL;
+    q4_status s = check_attention(q, cache, lengths, max_length, tokens, count, heads, options, out, workspace,
+                                  workspace_bytes, need, &x.a);
+    if (s != Q4_OK) return s;
+    s = check_new(q_starts, masks, tokens, count, out, (size_t)tokens * (size_t)heads * (size_t)cache->dim * 2,
+                  workspace, (size_t)need);
+    if (s != Q4_OK) return s;
+    x.a.q_starts = q_starts;
+    x.masks = masks;
+    x.max_new = (int)max_new;
+    hipError_t e = q4::launch_attn_tree(x, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

@@ -34,7 +34,8 @@ struct AppendArgs {
     int heads;
     KvCache c;
     const int* seq;        // or NULL: token t is of sequence t
-    const int* positions;
+    const int* positions;  // that the heads are turned by
+    const int* slots;      // positions that they are written to
     const float* inv_freq;
     int rot;
     int interleaved;
@@ -70,14 +71,29 @@ struct AttnArgs {
     int images;            // tiles that fit into the launch's LDS, 2 to 4
 };
 
+// Accepted tokens of each sequence moved together.  A latent cache is one without
+// V, of one kv head.
+struct KeepArgs {
+    KvCache c;
+    const int* starts;       // [count]
+    const int* keep_starts;  // [count + 1]
+    const int* keep;         // [total]
+    int total;
+    int count;               // sequences
+};
+
 // Widths the attention kernels are compiled for.
 inline bool attn_dim_supported(int dim) { return dim == 64 || dim == 96 || dim == 128 || dim == 192 || dim == 256; }
 
 hipError_t launch_rope_append(const AppendArgs& a, hipStream_t st);
+hipError_t launch_cache_keep(const KeepArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t st);
 int64_t attn_decode_workspace(int64_t batch, int heads, int dim);
 hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length);
+struct NewArgs;  // attn_new.hpp
+hipError_t launch_attn_tree(const NewArgs& x, hipStream_t st);
+int64_t attn_tree_workspace(int heads, int kv_heads, int dim, int max_new);
 
 // The table's page for a position of sequence `row`, or -1 when the page is
 // absent.  pos must lie below cols << shift.

@@ -1,0 +1,252 @@
+// New tokens over a cache: what they see, and how the cached positions are shared
+// out to workgroups.  Used by the attention of drafted tokens (attn_tree.hip) and
+// the latent attention (latent_attn.hip).
+//
+// The n new tokens of a sequence are its last n cached positions, base .. base +
+// n - 1.  Without masks token i sees every position up to base + i.  With masks it
+// sees every position below base, and position base + k where bit k of its mask
+// is set; its place is then base + (bits set) - 1, at least base, which for a tree of
+// drafted tokens is base + its depth; windows and distances go by places.
+#pragma once
+
+#include "attn_softmax.hpp"
+
+namespace q4 {
+
+constexpr int kMaskTokens = 64;   // tokens that a mask can name
+constexpr int kPartSlots = 512;   // workgroups wanted per launch at most
+static_assert(2 * kPartSlots <= kAttnCounters, "a counter for each sequence of several parts, and for each group");
+
+struct NewArgs {
+    AttnArgs a;             // rows: new tokens of all sequences
+    const uint64_t* masks;  // [rows], or NULL
+    int max_new;            // most new tokens of a sequence
+    int target;             // parts wanted per kv head and row block
+};
+
+struct NewSeq {
+    int s;      // sequence, or -1
+    int row;    // its first row
+    int n;      // its rows
+    int len;    // cached positions
+    int base;   // position of its first new token (may be negative)
+};
+
+__device__ __forceinline__ NewSeq new_seq(const NewArgs& x, int s, int first, int last, int len) {
+    NewSeq r;
+    r.s = s;
+    r.row = min(max(first, 0), x.a.rows);
+    r.n = min(max(last, r.row), x.a.rows) - r.row;
+    r.len = min(max(len, 0), x.a.max_length);
+    r.base = r.len - r.n;
+    return r;
+}
+
+// First tile that any of its tokens may see, and the number of tiles.
+__device__ __forceinline__ int new_tiles(const NewArgs& x, const NewSeq& q, int& first) {
+    first = x.a.window > 0 ? max(q.base + 1 - x.a.window, 0) / kTileKeys : 0;
+    return q.n > 0 ? (q.len + kTileKeys - 1) / kTileKeys - first : 0;
+}
+
+__device__ __forceinline__ int bits_of(uint64_t v) { return __builtin_popcountll(v); }
+
+// Place of a token with this mask.
+__device__ __forceinline__ int place_of(const NewSeq& q, uint64_t mask) { return q.base + max(bits_of(mask), 1) - 1; }
+
+// What a row sees: positions lo <= j < hi, and base + k for the bits k of mask.
+struct SeenRow {
+    uint64_t mask;
+    int lo, hi;
+    int place;
+};
+
+// The first n bits.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+    return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
+}
+
+__device__ __forceinline__ SeenRow seen_row(const NewArgs& x, const NewSeq& q, int token) {
+    SeenRow r = {0, 0, 0, 0};
+    if (token >= q.n) return r;
+    if (x.masks) {
+        const uint64_t* mine = x.masks + q.row;
+        const uint64_t valid = low_bits(q.n);
+        r.mask = mine[token] & valid;
+        r.place = place_of(q, r.mask);
+        r.hi = max(q.base, 0);
+        if (x.a.window > 0 && x.a.window <= kMaskTokens) {
+            // places differ by 63 at most
+            for (int k = 0; k < min(q.n, kMaskTokens); ++k)
+                if (place_of(q, mine[k] & valid) <= r.place - x.a.window) r.mask &= ~((uint64_t)1 << k);
+        }
+    } else {
+        r.place = q.base + token;
+        r.hi = max(r.place + 1, 0);
+    }
+    r.lo = x.a.window > 0 ? max(r.place + 1 - x.a.window, 0) : 0;
+    return r;
+}
+
+// Which of the 64 positions from kb on the row sees.
+__device__ __forceinline__ uint64_t seen_word(const SeenRow& r, int kb, int base) {
+    uint64_t w = low_bits(r.hi - kb) & ~low_bits(r.lo - kb);
+    const int d = kb - base;  // bit d of the mask is position kb
+    if (d >= 0 && d < 64) w |= r.mask >> d;
+    if (d < 0 && d > -64) w |= r.mask << -d;
+    return w;
+}
+
+// A workgroup's part of one sequence's tiles.
+struct NewPart {
+    NewSeq q;
+    int part;     // of the sequence
+    int parts;    // parts of the sequence
+    int slot;     // workspace slot of its first part, if it has several
+    int split;    // sequences of several parts before this one
+    int group;    // groups of kJoin parts before this sequence's
+    int t_begin, t_end;
+};
+
+// Parts of a sequence beyond which groups of kJoin are joined first.
+constexpr int kNewGroups = 2 * kJoin;
+
+// Tiles of a part: the total over `target`, rounded up, so that there are at most
+// target + (sequences of several parts) parts of such sequences; at least `least`.
+__device__ __forceinline__ int new_chunk(int64_t total, int target, int least) {
+    const float quotient = (float)total / (float)target;
+    if (quotient > (float)(1 << 22)) return 1 << 26;  // more than any sequence has
+    int c = max((int)quotient - 1, least);            // at most two below
+    while ((int64_t)c * target < total) ++c;
+    return c;
+}
+
+// The part with number `item`; parts are numbered sequence by sequence.  Each wave
+// computes it for itself.  A sequence with new tokens but no positions has a part,
+// which writes zeros.  A sequence of several parts has more than total / target
+// tiles, so there are fewer than `target` of them, with fewer than 2 target parts.
+__device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int least) {
+    const AttnArgs& a = x.a;
+    const int lane = threadIdx.x & 63;
+    NewPart r;
+    r.q.s = -1;
+    r.part = r.parts = r.slot = r.split = r.group = r.t_begin = r.t_end = 0;
+    if (a.count == 1) {
+        const auto of = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
+        const NewSeq q = new_seq(x, 0, first, last, len);
+        int t0;
+        const int n = new_tiles(x, q, t0), chunk = new_chunk(n, x.target, least);
+        r.parts = q.n == 0 ? 0 : n > chunk ? (n + chunk - 1) / chunk : 1;
+        r.part = item;
+        r.t_begin = t0 + item * chunk;
+        r.t_end = min(t0 + n, r.t_begin + chunk);
+        if (item < r.parts) r.q = q;
+        return r;
+    }
+    const auto seq_of = [&](int s) {
+        NewSeq q = {-1, 0, 0, 0, 0};
+        if (s < a.count) q = new_seq(x, s, a.q_starts[s], a.q_starts[s + 1], a.lengths[s]);
+        return q;
+    };
+    int64_t total = 0;
+    for (int s0 = 0; s0 < a.count; s0 += 64) {
+        int t0;
+        total += lane_scan(new_tiles(x, seq_of(s0 + lane), t0)).last;
+    }
+    const int chunk = new_chunk(total, x.target, least);
+    int before = 0;  // parts of earlier sequences
+    for (int s0 = 0; s0 < a.count; s0 += 64) {
+        const NewSeq q = seq_of(s0 + lane);
+        int t0;
+        const int tiles = new_tiles(x, q, t0);
+        const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
+        const LaneScan s = lane_scan(n), several = lane_scan(n > 1 ? n : 0);
+        const int groups = n > kNewGroups ? (n + kJoin - 1) / kJoin : 0;
+        const LaneScan gs = lane_scan(groups);
+        const uint64_t hit = __ballot(n > 0 && item < before + s.upto && item >= before + s.upto - n);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            r.q.s = s0 + l;
+            r.q.row = of(q.row);
+            r.q.n = of(q.n);
+            r.q.len = of(q.len);
+            r.q.base = of(q.base);
+            r.parts = of(n);
+            r.part = item - (before + of(s.upto) - r.parts);
+            r.slot += of(several.upto - (n > 1 ? n : 0));
+            r.split += bits_of(__ballot(n > 1 && lane < l));
+            r.group += of(gs.upto - groups);
+            // Alike parts: the last one is no shorter than it has to be.
+            const int per = (of(tiles) + r.parts - 1) / r.parts;
+            r.t_begin = of(t0) + r.part * per;
+            r.t_end = min(of(t0 + tiles), r.t_begin + per);
+            return r;
+        }
+        r.slot += several.last;
+        r.split += bits_of(__ballot(n > 1));
+        r.group += gs.last;
+        before += s.last;
+    }
+    return r;
+}
+
+// Partial results: counters of finished parts, outputs [slots][pairs][R][dim], their
+// maxima and sums [slots][pairs][R][2], R rows of a workgroup.  There are fewer
+// than 2 target slots, and target * pairs is at most kPartSlots: where that leaves a
+// target of one nothing is split.
+struct NewWorkspace {
+    float* o;
+    float* ml;
+    int* counters;
+};
+
+__host__ __device__ inline long new_slots(int target) { return target > 1 ? 2 * (long)target : 0; }
+
+__device__ __forceinline__ NewWorkspace new_workspace(const NewArgs& x, int pairs, int rows, int dim) {
+    NewWorkspace w;
+    w.counters = reinterpret_cast<int*>(x.a.workspace);
+    w.o = x.a.workspace + kAttnCounters;
+    w.ml = w.o + new_slots(x.target) * pairs * rows * dim;
+    return w;
+}
+
+inline int64_t new_workspace_bytes(int target, long pairs, int rows, int dim) {
+    return (new_slots(target) * pairs * rows * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
+}
+
+// The last workgroup of a sequence and row block to finish joins its parts, in
+// order, whichever it is, and gives row r to store(r, joined) from one wave.  The
+// counters are zero again afterwards.  Called by every thread of a workgroup after
+// its last share_store; `nrows` rows from the workgroup's own slot on.
+template <int D, class Store>
+__device__ __forceinline__ void join_new_parts(const NewPart& it, const NewWorkspace& ws, int pairs, int pair, int rows,
+                                               int nrows, Store store) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const long row_at = ((long)it.slot * pairs + pair) * rows;  // of the first part
+    int parts = it.parts;
+    long stride = (long)pairs * rows;  // rows from part to part
+    if (parts > kNewGroups) {
+        // Many parts: groups of kJoin are joined first, each by its last workgroup,
+        // into the place of the group's first part.
+        const int first = it.part / kJoin * kJoin, members = min(kJoin, parts - first);
+        if (!parts_done(ws.counters + kPartSlots + (it.group + it.part / kJoin) * pairs + pair, members)) return;
+        for (int r = wave; r < nrows; r += waves) {
+            const long at = row_at + first * stride + r;
+            const JoinedRow<D> j = join_parts<D, true>(ws.o + at * D, ws.ml + at * 2, stride, members);
+#pragma unroll
+            for (int i = 0; i < JoinedRow<D>::PER; ++i) {
+                const int d = 2 * (lane + 64 * i);
+                if (d < D) share_store(ws.o + at * D + d, j.o[i].x, j.o[i].y);
+            }
+            if (lane == 0) share_store(ws.ml + at * 2, j.m, j.l);
+        }
+        parts = (parts + kJoin - 1) / kJoin;
+        stride *= kJoin;
+    }
+    if (!parts_done(ws.counters + it.split * pairs + pair, parts)) return;
+    for (int r = wave; r < nrows; r += waves)
+        store(r, join_parts<D, true>(ws.o + (row_at + r) * D, ws.ml + (row_at + r) * 2, stride, parts));
+}
+
+}  // namespace q4

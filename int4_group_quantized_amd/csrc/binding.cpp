@@ -18,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <map>
 #include <string>
@@ -177,10 +178,10 @@ PyObject* answer(q4_status status, const at::Tensor& out) {
 }
 
 // rope_append(qkv, k_cache, v_cache, table, positions, inv_freq, heads, seq,
-//             q_norm, k_norm, eps, interleaved, mscale, q)
+//             q_norm, k_norm, eps, interleaved, mscale, q, slots)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    expect(n, 14);
+    expect(n, 15);
     const at::Tensor &k = tensor(a[1], "k_cache"), &v = tensor(a[2], "v_cache"), &table = tensor(a[3], "table");
     const at::Tensor& qkv = tensor(a[0], "qkv");
     const q4g128_kv_cache c = cache_of(k, v, table);
@@ -208,6 +209,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* seq = optional<int32_t>(a[7], "seq", at::kInt, {tokens}, dev);
     const uint16_t* q_norm = optional<uint16_t>(a[8], "q_norm", at::kHalf, {c.dim}, dev);
     const uint16_t* k_norm = optional<uint16_t>(a[9], "k_norm", at::kHalf, {c.dim}, dev);
+    const int32_t* pos = static_cast<const int32_t*>(positions.data_ptr());
+    const int32_t* slots = optional<int32_t>(a[14], "slots", at::kInt, {tokens}, dev);
     const float eps = real(a[10]), mscale = real(a[12]);
     const int interleaved = PyObject_IsTrue(a[11]);
     if (interleaved < 0) throw python_error();
@@ -216,10 +219,9 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     // One row has no next row: any stride will do.
     const int64_t ld = tokens > 1 ? qkv.stride(0) : (columns + 3) / 4 * 4;
     const int32_t rot = pairs > INT32_MAX / 2 ? -1 : (int32_t)(2 * pairs);
-    return answer(q4g128_rope_append(static_cast<const float*>(qkv.data_ptr()), ld, tokens, heads, &c, seq,
-                                     static_cast<const int32_t*>(positions.data_ptr()), freq, rot, interleaved, mscale,
-                                     q_norm, k_norm, eps, static_cast<uint16_t*>(q.data_ptr()),
-                                     current_stream(dev.device)),
+    return answer(q4g128_rope_append_slots(static_cast<const float*>(qkv.data_ptr()), ld, tokens, heads, &c, seq, pos,
+                                           slots ? slots : pos, freq, rot, interleaved, mscale, q_norm, k_norm, eps,
+                                           static_cast<uint16_t*>(q.data_ptr()), current_stream(dev.device)),
                   q);
     END_HANDLE_TH_ERRORS
 }
@@ -335,10 +337,71 @@ PyObject* attn_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// attn_tree(q, k_cache, v_cache, table, q_starts, lengths, masks, scale, softcap,
+//           window, slopes, max_new, max_length, out, workspace)
+PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 15);
+    const at::Tensor& lengths = tensor(a[5], "lengths");
+    if (lengths.dim() != 1) value_error("lengths must be [sequences]");
+    const Attention t(a[0], a[1], a[2], a[3], a[5], lengths.size(0), a[7], a[8], a[9], a[10], Py_None, a[12]);
+    const at::Tensor& starts = tensor(a[4], "q_starts");
+    check(starts, "q_starts", at::kInt, {t.count + 1});
+    t.dev.add(starts);
+    const uint64_t* masks = optional<uint64_t>(a[6], "masks", at::kLong, {t.rows}, t.dev);
+    const int64_t max_new = a[11] == Py_None ? std::min<int64_t>(t.rows, Q4G128_MAX_DRAFT) : integer(a[11]);
+    const int64_t need = q4g128_attn_tree_workspace(t.heads, t.c.kv_heads, t.c.dim, max_new);
+    if (need < 0) return PyLong_FromLongLong(need);
+    const c10::DeviceGuard guard(t.dev.device);
+    const hipStream_t stream = current_stream(t.dev.device);
+    const at::Tensor out = output(a[13], "out", t.q.sizes(), t.dev);
+    const at::Tensor ws = workspace_of(a[14], need, t.dev, stream);
+    return answer(q4g128_attn_tree(t.qp(), &t.c, static_cast<const int32_t*>(starts.data_ptr()), t.lp(), masks, max_new,
+                                   t.max_length, t.rows, t.count, t.heads, &t.o,
+                                   static_cast<uint16_t*>(out.data_ptr()), ws.data_ptr(), ws.numel(), stream),
+                  out);
+    END_HANDLE_TH_ERRORS
+}
+
+// Numbers of accepted tokens: (starts, keep_starts, keep).
+struct Keep {
+    const at::Tensor &starts, &keep_starts, &keep;
+    int64_t count, total;
+    Keep(PyObject* s, PyObject* ks, PyObject* k, const SameDevice& dev)
+        : starts(tensor(s, "starts")), keep_starts(tensor(ks, "keep_starts")), keep(tensor(k, "keep")) {
+        if (starts.dim() != 1) value_error("starts must be [sequences]");
+        if (keep.dim() != 1) value_error("keep must be a vector");
+        count = starts.size(0);
+        total = keep.size(0);
+        check(starts, "starts", at::kInt, {count});
+        check(keep_starts, "keep_starts", at::kInt, {count + 1});
+        check(keep, "keep", at::kInt, {total});
+        dev.add(starts), dev.add(keep_starts), dev.add(keep);
+    }
+    static const int32_t* p(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
+};
+
+// cache_keep(k_cache, v_cache, table, starts, keep_starts, keep)
+PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 6);
+    const at::Tensor &k = tensor(a[0], "k_cache"), &v = tensor(a[1], "v_cache"), &table = tensor(a[2], "table");
+    const q4g128_kv_cache c = cache_of(k, v, table);
+    const SameDevice dev(k);
+    dev.add(v), dev.add(table);
+    const Keep t(a[3], a[4], a[5], dev);
+    const c10::DeviceGuard guard(dev.device);
+    return PyLong_FromLong(q4g128_cache_keep(&c, t.p(t.starts), t.p(t.keep_starts), t.p(t.keep), t.total, t.count,
+                                             current_stream(dev.device)));
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"rope_append", (PyCFunction)(void (*)(void))rope_append, METH_FASTCALL, nullptr},
     {"attn_decode", (PyCFunction)(void (*)(void))attn_decode, METH_FASTCALL, nullptr},
     {"attn_prefill", (PyCFunction)(void (*)(void))attn_prefill, METH_FASTCALL, nullptr},
+    {"attn_tree", (PyCFunction)(void (*)(void))attn_tree, METH_FASTCALL, nullptr},
+    {"cache_keep", (PyCFunction)(void (*)(void))cache_keep, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

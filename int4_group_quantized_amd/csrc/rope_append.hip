@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 // Page and offset of token t, or page -1.
 __device__ __forceinline__ int append_slot(const AppendArgs& a, int t, int& off) {
     const int s = a.seq ? a.seq[t] : t;
-    const int pos = a.positions[t];
+    const int pos = a.slots[t];
     off = pos & ((1 << a.c.shift) - 1);
     if ((unsigned)s >= (unsigned)a.c.sequences || pos < 0 || (pos >> a.c.shift) >= a.c.cols) return -1;
     return page_of(a.c, a.c.table + (size_t)s * a.c.cols, pos);
@@ -81,7 +81,7 @@ __device__ __forceinline__ void append_values(const AppendArgs& a, int tile, int
     // Columns are shifted by the first position's place in its run of eight, so
     // that a prompt's aligned runs start at multiples of eight columns wherever
     // it starts.
-    const int shift = a.positions[t0] & 7;
+    const int shift = a.slots[t0] & 7;
     const float* src = a.qkv + (size_t)t0 * a.ld + (size_t)(a.heads + a.c.kv_heads + head) * D;
     for (int i = tid; i < nt * (D / 4); i += kAppendThreads) {
         const int t = i / (D / 4), d = i % (D / 4) * 4;
