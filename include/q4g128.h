@@ -84,6 +84,8 @@ typedef int32_t q4_status;
 #define Q4G128_MAX_SEQUENCES 65536
 #define Q4G128_MAX_DRAFT 64
 #define Q4G128_ATTN_COUNTER_BYTES 4096
+#define Q4G128_LATENT_ROT 64
+#define Q4G128_LATENT_MAX_MAIN 1024
 
 /*
  * q4g128_pack -- two codes per byte.
@@ -416,6 +418,74 @@ Q4_API q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cach
 Q4_API q4_status q4g128_cache_keep(const q4g128_kv_cache* cache, const int32_t* starts,
                              const int32_t* keep_starts, const int32_t* keep, int64_t total,
                              int64_t count, void* stream);
+
+/*
+ * Latent attention: keys and values of all heads come from one row per position,
+ * `latent` columns and a rotary key part of Q4G128_LATENT_ROT that all heads share.
+ *   rows   fp16 [pages][page][latent + 64], page number and table as in
+ *   q4g128_kv_cache; stride: elements from one page to the next (at least
+ *   page*(latent+64), a multiple of 8).
+ *   latent in {128, 256, 512}; page a power of two in 16..256;
+ *   table_cols*page <= 2^31 - 256.
+ * The struct is host memory, read during the call and not kept.
+ */
+typedef struct q4g128_latent_cache {
+    uint16_t* rows;
+    const int32_t* table;  /* [sequences][table_cols] */
+    int64_t pages;
+    int64_t stride;
+    int64_t sequences;
+    int64_t table_cols;
+    int32_t latent;
+    int32_t page;
+} q4g128_latent_cache;
+
+/*
+ * q4g128_latent_append -- new tokens' rows into the cache, and their queries.
+ * Row t of kv (fp32, `ld` floats from row to row, a multiple of 4; further columns
+ * are left alone) holds `latent` columns x and 64 rotary ones r; the position
+ * slots[t] of sequence seq[t] (as in q4g128_rope_append) becomes
+ *     (x * norm / sqrt(mean(x^2) + eps)  (norm fp16 [latent] given; else x),
+ *      r turned by positions[t] as in q4g128_rope_append with rot = 64).
+ * The query of token t and head h is (q_main row, q_rot row turned alike): `main`
+ * and 64 floats at q_main + t*main_ld + h*main_head and q_rot + t*rot_ld +
+ * h*rot_head, strides multiples of 4.  For the absorbed form q_main holds the heads'
+ * products with their key weights (main = latent), for the expanded form the heads'
+ * own columns.
+ *   q [tokens][heads][main + 64] fp16 is written in full; main a multiple of 8, 8 to
+ *   Q4G128_LATENT_MAX_MAIN.  heads 0: no queries (their pointers are not used).
+ *   inv_freq [32], or NULL: nothing is turned or scaled.
+ */
+Q4_API q4_status q4g128_latent_append(const float* kv, int64_t ld, int64_t tokens,
+                             const q4g128_latent_cache* cache, const int32_t* seq,
+                             const int32_t* positions, const int32_t* slots, const float* inv_freq,
+                             int32_t interleaved, float mscale, const uint16_t* norm, float eps,
+                             const float* q_main, int64_t main_ld, int64_t main_head, int32_t main,
+                             const float* q_rot, int64_t rot_ld, int64_t rot_head, int32_t heads,
+                             uint16_t* q, void* stream);
+
+/* q4g128_latent_keep -- q4g128_cache_keep for a latent cache. */
+Q4_API q4_status q4g128_latent_keep(const q4g128_latent_cache* cache, const int32_t* starts,
+                             const int32_t* keep_starts, const int32_t* keep, int64_t total,
+                             int64_t count, void* stream);
+
+/*
+ * q4g128_latent_attn -- attention over the rows themselves (absorbed form):
+ *     out[t][h] = sum_j softmax_j(scale * q[t][h] . c_j) c_j[:latent]
+ *   q [tokens][heads][latent + 64], out [tokens][heads][latent] fp16; q_starts,
+ *   lengths, masks, max_new, max_length and workspace (q4g128_latent_attn_workspace()
+ *   bytes) as in q4g128_attn_tree; a head's value weights are applied to out by the
+ *   caller.  max_new is at most Q4G128_MAX_DRAFT with masks and at most
+ *   Q4G128_MAX_TOKENS without.  Numerics as stated for the attention calls.
+ *   heads at most Q4G128_MAX_HEADS; scale > 0, finite.
+ */
+Q4_API int64_t q4g128_latent_attn_workspace(int32_t heads, int32_t latent, int64_t max_new);
+Q4_API q4_status q4g128_latent_attn(const uint16_t* q, const q4g128_latent_cache* cache,
+                             const int32_t* q_starts, const int32_t* lengths,
+                             const uint64_t* masks, int64_t max_new, int64_t max_length,
+                             int64_t tokens, int64_t count, int32_t heads, float scale,
+                             uint16_t* out, void* workspace, int64_t workspace_bytes,
+                             void* stream);
 
 /* Static, NUL-terminated description of a status code. */
 Q4_API const char* q4g128_status_string(q4_status status);

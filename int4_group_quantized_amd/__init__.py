@@ -33,6 +33,7 @@ INT8_MAX_K = 8192
 MAX_GROUPED = 65536
 ATTN_COUNTER_BYTES = 4096
 MAX_DRAFT = 64
+LATENT_ROT = 64
 
 
 class GemvDesc(ctypes.Structure):
@@ -46,6 +47,13 @@ class KvCache(ctypes.Structure):
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("sequences", ctypes.c_int64),
                 ("table_cols", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
                 ("page", ctypes.c_int32)]
+
+
+class LatentCache(ctypes.Structure):
+    """struct q4g128_latent_cache of include/q4g128.h."""
+    _fields_ = [("rows", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("sequences", ctypes.c_int64), ("table_cols", ctypes.c_int64),
+                ("latent", ctypes.c_int32), ("page", ctypes.c_int32)]
 
 
 class AttnOptions(ctypes.Structure):
@@ -72,6 +80,10 @@ EXPORTED = (
     "q4g128_attn_prefill",
     "q4g128_attn_tree_workspace",
     "q4g128_attn_tree",
+    "q4g128_latent_append",
+    "q4g128_latent_keep",
+    "q4g128_latent_attn_workspace",
+    "q4g128_latent_attn",
     "q4g128_status_string",
     "q4g128_last_hip_error",
 )
@@ -110,6 +122,12 @@ def _load():
     lib.q4g128_cache_keep.argtypes = [cache, vp, vp, vp, i64, i64, vp]
     lib.q4g128_attn_tree_workspace.argtypes = [i32, i32, i32, i64]
     lib.q4g128_attn_tree.argtypes = [vp, cache, vp, vp, vp, i64, i64, i64, i64, i32, options, vp, vp, i64, vp]
+    latent = ctypes.POINTER(LatentCache)
+    lib.q4g128_latent_append.argtypes = [vp, i64, i64, latent, vp, vp, vp, vp, i32, f32, vp, f32, vp, i64, i64, i32, vp,
+                                         i64, i64, i32, vp, vp]
+    lib.q4g128_latent_keep.argtypes = [latent, vp, vp, vp, i64, i64, vp]
+    lib.q4g128_latent_attn_workspace.argtypes = [i32, i32, i64]
+    lib.q4g128_latent_attn.argtypes = [vp, latent, vp, vp, vp, i64, i64, i64, i64, i32, f32, vp, vp, i64, vp]
     lib.q4g128_attn_decode_workspace.argtypes = [i64, i32, i32]
     lib.q4g128_attn_decode.argtypes = [vp, cache, vp, i64, i64, i32, options, vp, vp, i64, vp]
     lib.q4g128_attn_prefill_workspace.argtypes = [i64, i64, i32, i32, i32, i64]
@@ -117,9 +135,11 @@ def _load():
     for name in ("q4g128_pack", "q4g128_quantize", "q4g128_gemv", "q4g128_gemv_grouped", "q4g128_gemm_small_batch",
                  "q4g128_gemm_prefill",
                  "q4g128_gemv_int8", "q4g128_gemm_prefill_epilogue", "q4g128_rope_append", "q4g128_attn_decode",
-                 "q4g128_attn_prefill", "q4g128_rope_append_slots", "q4g128_cache_keep", "q4g128_attn_tree"):
+                 "q4g128_attn_prefill", "q4g128_rope_append_slots", "q4g128_cache_keep", "q4g128_attn_tree",
+                 "q4g128_latent_append", "q4g128_latent_keep", "q4g128_latent_attn"):
         getattr(lib, name).restype = ctypes.c_int32
-    for name in ("q4g128_attn_decode_workspace", "q4g128_attn_prefill_workspace", "q4g128_attn_tree_workspace"):
+    for name in ("q4g128_attn_decode_workspace", "q4g128_attn_prefill_workspace", "q4g128_attn_tree_workspace",
+                 "q4g128_latent_attn_workspace"):
         getattr(lib, name).restype = ctypes.c_int64
     lib.q4g128_status_string.argtypes = [ctypes.c_int32]
     lib.q4g128_status_string.restype = ctypes.c_char_p
@@ -456,6 +476,51 @@ def q4g128_cache_keep(k_cache, v_cache, table, starts, keep_starts, keep, stream
         with torch.cuda.stream(stream):
             return q4g128_cache_keep(k_cache, v_cache, table, starts, keep_starts, keep)
     _check(_binding.cache_keep(k_cache, v_cache, table, starts, keep_starts, keep), "q4g128_cache_keep")
+
+
+def q4g128_latent_append(kv, cache, table, positions, inv_freq, seq=None, slots=None, norm=None, eps=1e-6,
+                         interleaved=False, mscale=1.0, q_main=None, q_rot=None, q=None, stream=None):
+    """New tokens' latent rows into the cache; returns their queries fp16 [T][heads][main + 64], or None without any.
+
+    kv: fp32 [T][>= latent + 64], rows may be strided.  cache fp16 [pages][page][latent + 64], each page contiguous;
+    table int32 [sequences][cols].  positions, slots, seq as q4g128_rope_append; inv_freq fp32 [32] or None (nothing is
+    turned); norm fp16 [latent] or None.  q_main fp32 [T][heads][main] and q_rot fp32 [T][heads][64], both or none, may
+    be views of larger tensors.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_latent_append(kv, cache, table, positions, inv_freq, seq, slots, norm, eps, interleaved, mscale,
+                                        q_main, q_rot, q)
+    return _answer(_binding.latent_append(kv, cache, table, positions, inv_freq, seq, slots, norm, eps, interleaved,
+                                          mscale, q_main, q_rot, q), "q4g128_latent_append")
+
+
+def q4g128_latent_keep(cache, table, starts, keep_starts, keep, stream=None) -> None:
+    """q4g128_cache_keep for a latent cache."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_latent_keep(cache, table, starts, keep_starts, keep)
+    _check(_binding.latent_keep(cache, table, starts, keep_starts, keep), "q4g128_latent_keep")
+
+
+def q4g128_latent_attn_workspace(heads, latent, max_new) -> int:
+    """Bytes of workspace that q4g128_latent_attn needs."""
+    return _lib.q4g128_latent_attn_workspace(heads, latent, max_new)
+
+
+def q4g128_latent_attn(q, cache, table, q_starts, lengths, scale, masks=None, max_new=None, max_length=None, out=None,
+                       workspace=None, stream=None) -> torch.Tensor:
+    """Attention over the latent rows themselves: q fp16 [T][heads][latent + 64] -> out fp16 [T][heads][latent].
+
+    q_starts, lengths, masks and max_new as q4g128_attn_tree; without masks a sequence may have any number of rows, and
+    max_new is T by default.  Other arguments as q4g128_attn_decode.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_latent_attn(q, cache, table, q_starts, lengths, scale, masks, max_new, max_length, out,
+                                      workspace)
+    return _answer(_binding.latent_attn(q, cache, table, q_starts, lengths, scale, masks, max_new, max_length, out,
+                                        workspace), "q4g128_latent_attn")
 
 
 def q4g128_status_string(status: int) -> str:

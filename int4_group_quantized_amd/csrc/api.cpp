@@ -11,7 +11,7 @@
 #include <utility>
 #include <vector>
 
-#include "attn_new.hpp"
+#include "latent.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -206,6 +206,38 @@ q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const
     a->q_starts = nullptr;
     a->count = (int)sequences;
     return Q4_OK;
+}
+
+// Checks a latent cache and fills the kernels' form of it: a cache without V, of
+// one kv head.
+q4_status check_latent(const q4g128_latent_cache* c, q4::KvCache* out) {
+    if (!c || !c->rows || !c->table) return Q4_EINVAL;
+    if (c->pages < 1 || c->sequences < 1 || c->table_cols < 1) return Q4_EINVAL;
+    if (!q4::latent_supported(c->latent)) return Q4_ESHAPE;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return Q4_ESHAPE;
+    if (c->pages > Q4G128_MAX_N || c->sequences > Q4G128_MAX_N || c->table_cols > Q4G128_MAX_N / c->page)
+        return Q4_ESHAPE;
+    const int dim = c->latent + q4::kRot;
+    if (c->stride < (int64_t)c->page * dim || c->stride % 8 != 0 || c->stride > INT64_MAX / 4 / c->pages) return Q4_ESHAPE;
+    if (!aligned(c->rows, 16) || !aligned(c->table, 4)) return Q4_EALIGN;
+    out->k = c->rows;
+    out->v = nullptr;
+    out->table = c->table;
+    out->k_stride = c->stride;
+    out->v_stride = 0;
+    out->pages = (int)c->pages;
+    out->sequences = (int)c->sequences;
+    out->cols = (int)c->table_cols;
+    out->kv_heads = 1;
+    out->dim = dim;
+    out->shift = __builtin_ctz((unsigned)c->page);
+    return Q4_OK;
+}
+
+// Whether [p, p + bytes) meets a latent cache's rows or its table.
+bool hits_latent(const q4::KvCache& c, const void* p, size_t bytes) {
+    return overlaps(p, bytes, c.k, pool_bytes(c, c.k_stride)) ||
+           overlaps(p, bytes, c.table, (size_t)c.sequences * (size_t)c.cols * 4);
 }
 
 // Row numbers and masks of new tokens, against what a call writes.
@@ -532,6 +564,133 @@ q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, cons
     x.masks = masks;
     x.max_new = (int)max_new;
     hipError_t e = q4::launch_attn_tree(x, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+q4_status q4g128_latent_append(const float* kv, int64_t ld, int64_t tokens, const q4g128_latent_cache* cache,
+                               const int32_t* seq, const int32_t* positions, const int32_t* slots,
+                               const float* inv_freq, int32_t interleaved, float mscale, const uint16_t* norm, float eps,
+                               const float* q_main, int64_t main_ld, int64_t main_head, int32_t main,
+                               const float* q_rot, int64_t rot_ld, int64_t rot_head, int32_t heads, uint16_t* q,
+                               void* stream) {
+    if (!kv || !positions || !slots || tokens < 1 || heads < 0 || (heads > 0 && (!q_main || !q_rot || !q)))
+        return Q4_EINVAL;
+    q4::LatentAppendArgs a;
+    q4_status s = check_latent(cache, &a.c);
+    if (s != Q4_OK) return s;
+    const int64_t row = a.c.dim, wide = (int64_t)main + q4::kRot;
+    if (tokens > Q4G128_MAX_TOKENS || ld < row || ld % 4 != 0 || ld > INT64_MAX / 8 / tokens || heads > Q4G128_MAX_HEADS)
+        return Q4_ESHAPE;
+    if (heads > 0) {
+        if (main < 8 || main > Q4G128_LATENT_MAX_MAIN || main % 8 != 0) return Q4_ESHAPE;
+        // Strides are of views of one tensor, in either order of tokens and heads.
+        const int64_t most = INT64_MAX / 16 / tokens / heads;
+        if (main_ld < main || main_head < main || rot_ld < q4::kRot || rot_head < q4::kRot || main_ld % 4 != 0 ||
+            main_head % 4 != 0 || rot_ld % 4 != 0 || rot_head % 4 != 0 || main_ld > most || main_head > most ||
+            rot_ld > most || rot_head > most)
+            return Q4_ESHAPE;
+    }
+    if (!(eps >= 0.0f)) return Q4_EINVAL;  // written so that NaN fails
+    if (!aligned(kv, 16) || !aligned(seq, 4) || !aligned(positions, 4) || !aligned(slots, 4) || !aligned(inv_freq, 4) ||
+        !aligned(norm, 2) || (heads > 0 && (!aligned(q_main, 16) || !aligned(q_rot, 16) || !aligned(q, 16))))
+        return Q4_EALIGN;
+    const size_t n = (size_t)tokens, h = (size_t)heads, rows = pool_bytes(a.c, a.c.k_stride);
+    const size_t qbytes = n * h * (size_t)wide * 2;
+    const void* in[] = {kv, seq, positions, slots, inv_freq, norm, heads ? q_main : nullptr, heads ? q_rot : nullptr};
+    const size_t inbytes[] = {((n - 1) * (size_t)ld + (size_t)row) * 4, n * 4, n * 4, n * 4, (size_t)q4::kRot * 2,
+                              (size_t)cache->latent * 2,
+                              heads ? ((n - 1) * (size_t)main_ld + (h - 1) * (size_t)main_head + (size_t)main) * 4 : 0,
+                              heads ? ((n - 1) * (size_t)rot_ld + (h - 1) * (size_t)rot_head + q4::kRot) * 4 : 0};
+    if (overlaps(a.c.k, rows, a.c.table, (size_t)a.c.sequences * (size_t)a.c.cols * 4) ||
+        (heads > 0 && hits_latent(a.c, q, qbytes)))
+        return Q4_EINVAL;
+    for (int i = 0; i < 8; ++i)
+        if (in[i] && (overlaps(a.c.k, rows, in[i], inbytes[i]) || (heads > 0 && overlaps(q, qbytes, in[i], inbytes[i]))))
+            return Q4_EINVAL;
+    a.kv = kv;
+    a.ld = ld;
+    a.tokens = (int)tokens;
+    a.seq = seq;
+    a.positions = positions;
+    a.slots = slots;
+    a.inv_freq = inv_freq;
+    a.interleaved = interleaved != 0;
+    a.mscale = mscale;
+    a.norm = norm;
+    a.eps = eps;
+    a.q_main = q_main;
+    a.main_ld = main_ld;
+    a.main_head = main_head;
+    a.main = heads > 0 ? main : 0;
+    a.q_rot = q_rot;
+    a.rot_ld = rot_ld;
+    a.rot_head = rot_head;
+    a.heads = heads;
+    a.q = q;
+    hipError_t e = q4::launch_latent_append(a, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+q4_status q4g128_latent_keep(const q4g128_latent_cache* cache, const int32_t* starts, const int32_t* keep_starts,
+                             const int32_t* keep, int64_t total, int64_t count, void* stream) {
+    q4::KeepArgs a;
+    q4_status s = check_latent(cache, &a.c);
+    if (s != Q4_OK) return s;
+    return keep_tokens(&a, starts, keep_starts, keep, total, count, stream);
+}
+
+int64_t q4g128_latent_attn_workspace(int32_t heads, int32_t latent, int64_t max_new) {
+    if (heads < 1 || max_new < 1) return Q4_EINVAL;
+    if (heads > Q4G128_MAX_HEADS || !q4::latent_supported(latent) || max_new > Q4G128_MAX_TOKENS) return Q4_ESHAPE;
+    return q4::latent_attn_workspace(heads, latent, max_new);
+}
+
+q4_status q4g128_latent_attn(const uint16_t* q, const q4g128_latent_cache* cache, const int32_t* q_starts,
+                             const int32_t* lengths, const uint64_t* masks, int64_t max_new, int64_t max_length,
+                             int64_t tokens, int64_t count, int32_t heads, float scale, uint16_t* out, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    if (!q || !q_starts || !lengths || !out || tokens < 1 || count < 1 || max_length < 1) return Q4_EINVAL;
+    q4::NewArgs x;
+    q4_status s = check_latent(cache, &x.a.c);
+    if (s != Q4_OK) return s;
+    const int64_t need = q4g128_latent_attn_workspace(heads, cache->latent, max_new);
+    if (need < 0) return (q4_status)need;
+    if (tokens > Q4G128_MAX_TOKENS || count > Q4G128_MAX_SEQUENCES || count > cache->sequences ||
+        max_length > cache->table_cols * cache->page || (masks && max_new > Q4G128_MAX_DRAFT))
+        return Q4_ESHAPE;
+    if (!(scale > 0.0f && scale <= FLT_MAX)) return Q4_EINVAL;  // written so that NaN fails
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(workspace, 16)) return Q4_EALIGN;
+    if (!workspace || workspace_bytes < need) return Q4_EINVAL;
+    const size_t rows = (size_t)tokens * (size_t)heads;
+    const size_t qbytes = rows * (size_t)x.a.c.dim * 2, obytes = rows * (size_t)cache->latent * 2;
+    const size_t lbytes = (size_t)count * 4, wsbytes = (size_t)need;
+    if (hits_latent(x.a.c, out, obytes) || overlaps(out, obytes, q, qbytes) || overlaps(out, obytes, lengths, lbytes) ||
+        hits_latent(x.a.c, workspace, wsbytes) || overlaps(workspace, wsbytes, q, qbytes) ||
+        overlaps(workspace, wsbytes, out, obytes) || overlaps(workspace, wsbytes, lengths, lbytes))
+        return Q4_EINVAL;
+    s = check_new(q_starts, masks, tokens, count, out, obytes, workspace, wsbytes);
+    if (s != Q4_OK) return s;
+    x.a.q = q;
+    x.a.lengths = lengths;
+    x.a.max_length = (int)max_length;
+    x.a.rows = (int)tokens;
+    x.a.heads = heads;
+    x.a.group = heads;
+    x.a.scale = scale;
+    x.a.softcap = 0.0f;
+    x.a.window = 0;
+    x.a.slopes = nullptr;
+    x.a.prefix = nullptr;
+    x.a.out = out;
+    x.a.workspace = (float*)workspace;
+    x.a.q_starts = q_starts;
+    x.a.count = (int)count;
+    x.masks = masks;
+    x.max_new = (int)max_new;
+    q4::DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != Q4_OK) return s;
+    hipError_t e = q4::launch_latent_attn(x, dev, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

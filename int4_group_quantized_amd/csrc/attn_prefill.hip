@@ -46,6 +46,7 @@
 // Few tokens on a long cache leave most CUs idle, so the visible tiles are
 // then cut into equal splits joined by a second launch (prefill_split).
 #include "attn_softmax.hpp"
+#include "lds_loads.hpp"
 
 #include <cmath>
 #include <type_traits>
@@ -322,45 +323,6 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
     }
 }
 
-// 16 bytes per lane from memory into LDS: lane i's to byte `to` + 16 i.  In
-// assembly because the compiler, which sees that images follow each other in
-// one array, would let every LDS read wait for all such loads under way; the
-// waits are wait_and_meet's.  The instruction has no destination register.  m0, a
-// reserved register, cannot be declared as overwritten; nothing else in these
-// kernels uses it, which tests/test_attention_assembly.py checks.
-// First form: from base + the lane's offset in bytes, base the same in all lanes.
-// A vector instruction may have written base just before (a value read from a
-// lane, a spilled one too), and the compiler does not look into the assembly: the
-// five wait states that a memory operation then needs are the move's and the
-// no-operation's.  They cost 0.3% of 8,192 tokens' time, 1.6% at dim 64.
-__device__ __forceinline__ void load_lds(const uint16_t* base, uint32_t offset, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(to), "v"(offset), "s"(base)
-                 : "memory");
-}
-// A pointer that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
-    const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (const uint16_t*)((uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ void load_lds(const uint16_t* p, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(p) : "memory");
-}
-
-// Waits until at most NEWER of this wave's vector memory operations (which
-// complete in order) and none of its LDS operations are under way, then for the
-// workgroup.
-template <int NEWER>
-__device__ __forceinline__ void wait_and_meet() {
-    static_assert(NEWER < 64, "the counter has six bits");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((NEWER & 15) | 0x70 | (NEWER >> 4) << 14);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // LDS of a workgroup behind its images.
 template <int WAVES, bool SHARED>
 struct PrefillShared {
@@ -369,13 +331,6 @@ struct PrefillShared {
     float sum[SHARED ? WAVES : 0][32];      // a wave's share of the rows' sums
     int found[WAVES];                       // a wave has seen infinities or NaN where a row is masked
 };
-
-// The same for LDS operations only.
-__device__ __forceinline__ void lds_meet() {
-    asm volatile("" ::: "memory");
-    lds_barrier();
-    asm volatile("" ::: "memory");
-}
 
 template <int D, int OPTIONS, int ROWS>
 __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 64 ? 1 : 2)

@@ -396,12 +396,164 @@ PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The descriptor of a latent cache.  Pages may be strided.
+q4g128_latent_cache latent_of(const at::Tensor& rows, const at::Tensor& table) {
+    on_gpu(rows, "cache");
+    of_type(rows, "cache", at::kHalf);
+    if (rows.dim() != 3) value_error("cache must be [pages][page][latent + 64]");
+    const int64_t pages = rows.size(0), page = rows.size(1), dim = rows.size(2);
+    if ((dim != 1 && rows.stride(2) != 1) || (page != 1 && rows.stride(1) != dim))
+        value_error("each page of cache must be contiguous");
+    if (table.dim() != 2) value_error("table must be [sequences][table_cols]");
+    check(table, "table", at::kInt, table.sizes());
+    if (dim > INT32_MAX || page > INT32_MAX || dim < Q4G128_LATENT_ROT) value_error("cache must be [pages][page][latent + 64]");
+    q4g128_latent_cache c;
+    c.rows = static_cast<uint16_t*>(rows.data_ptr());
+    c.table = static_cast<const int32_t*>(table.data_ptr());
+    c.pages = pages;
+    c.stride = pages > 1 ? rows.stride(0) : page * dim;
+    c.sequences = table.size(0);
+    c.table_cols = table.size(1);
+    c.latent = (int32_t)(dim - Q4G128_LATENT_ROT);
+    c.page = (int32_t)page;
+    return c;
+}
+
+// One part of the queries, fp32 [tokens][heads][columns] with strides of its own.
+struct Part {
+    const float* p;
+    int64_t ld, head, columns;
+    Part(PyObject* o, const char* name, int64_t tokens, int64_t heads, const SameDevice& dev) {
+        const at::Tensor& t = tensor(o, name);
+        on_gpu(t, name);
+        of_type(t, name, at::kFloat);
+        dev.add(t);
+        if (t.dim() != 3 || t.size(0) != tokens || (heads >= 0 && t.size(1) != heads))
+            value_error("%s must be [T][heads][columns] (got %s)", name, shape_text(t.sizes()).c_str());
+        if (t.size(2) != 1 && t.stride(2) != 1) value_error("rows of %s must be contiguous", name);
+        p = static_cast<const float*>(t.data_ptr());
+        columns = t.size(2);
+        // A size of one has no next: any stride will do.
+        const int64_t any = (columns + 3) / 4 * 4;
+        ld = t.size(0) > 1 ? t.stride(0) : any;
+        head = t.size(1) > 1 ? t.stride(1) : any;
+    }
+};
+
+// latent_append(kv, cache, table, positions, inv_freq, seq, slots, norm, eps,
+//               interleaved, mscale, q_main, q_rot, q)
+PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 14);
+    const at::Tensor &kv = tensor(a[0], "kv"), &rows = tensor(a[1], "cache"), &table = tensor(a[2], "table");
+    const q4g128_latent_cache c = latent_of(rows, table);
+    on_gpu(kv, "kv");
+    of_type(kv, "kv", at::kFloat);
+    if (kv.dim() != 2) value_error("kv must be [T][columns]");
+    const int64_t tokens = kv.size(0), columns = kv.size(1);
+    if (columns < c.latent + Q4G128_LATENT_ROT) value_error("kv has %lld columns, fewer than latent + 64", (long long)columns);
+    if (kv.stride(1) != 1) value_error("rows of kv must be contiguous");
+    const SameDevice dev(kv);
+    dev.add(rows), dev.add(table);
+    const at::Tensor& positions = tensor(a[3], "positions");
+    check(positions, "positions", at::kInt, {tokens});
+    dev.add(positions);
+    const int32_t* pos = static_cast<const int32_t*>(positions.data_ptr());
+    const float* freq = optional<float>(a[4], "inv_freq", at::kFloat, {Q4G128_LATENT_ROT / 2}, dev);
+    const int32_t* seq = optional<int32_t>(a[5], "seq", at::kInt, {tokens}, dev);
+    const int32_t* slots = optional<int32_t>(a[6], "slots", at::kInt, {tokens}, dev);
+    const uint16_t* norm = optional<uint16_t>(a[7], "norm", at::kHalf, {c.latent}, dev);
+    const float eps = real(a[8]), mscale = real(a[10]);
+    const int interleaved = PyObject_IsTrue(a[9]);
+    if (interleaved < 0) throw python_error();
+    const int64_t ld = tokens > 1 ? kv.stride(0) : (columns + 3) / 4 * 4;
+    const c10::DeviceGuard guard(dev.device);
+    if ((a[11] == Py_None) != (a[12] == Py_None)) value_error("q_main and q_rot go together");
+    if (a[11] == Py_None) {
+        const q4_status status = q4g128_latent_append(
+            static_cast<const float*>(kv.data_ptr()), ld, tokens, &c, seq, pos, slots ? slots : pos, freq, interleaved, mscale,
+            norm, eps, nullptr, 0, 0, 0, nullptr, 0, 0, 0, nullptr, current_stream(dev.device));
+        if (status != Q4_OK) return PyLong_FromLong(status);
+        Py_RETURN_NONE;
+    }
+    const Part main(a[11], "q_main", tokens, -1, dev);
+    const int64_t heads = tensor(a[11], "q_main").size(1);
+    const Part rot(a[12], "q_rot", tokens, heads, dev);
+    if (rot.columns != Q4G128_LATENT_ROT) value_error("q_rot must have 64 columns");
+    if (heads < 1 || heads > Q4G128_MAX_HEADS || main.columns > Q4G128_LATENT_MAX_MAIN) return PyLong_FromLong(Q4_ESHAPE);
+    const at::Tensor q = output(a[13], "q", {tokens, heads, main.columns + Q4G128_LATENT_ROT}, dev);
+    return answer(q4g128_latent_append(static_cast<const float*>(kv.data_ptr()), ld, tokens, &c, seq, pos,
+                                       slots ? slots : pos, freq, interleaved, mscale, norm, eps, main.p, main.ld, main.head,
+                                       (int32_t)main.columns, rot.p, rot.ld, rot.head, (int32_t)heads,
+                                       static_cast<uint16_t*>(q.data_ptr()), current_stream(dev.device)),
+                  q);
+    END_HANDLE_TH_ERRORS
+}
+
+// latent_keep(cache, table, starts, keep_starts, keep)
+PyObject* latent_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 5);
+    const at::Tensor &rows = tensor(a[0], "cache"), &table = tensor(a[1], "table");
+    const q4g128_latent_cache c = latent_of(rows, table);
+    const SameDevice dev(rows);
+    dev.add(table);
+    const Keep t(a[2], a[3], a[4], dev);
+    const c10::DeviceGuard guard(dev.device);
+    return PyLong_FromLong(q4g128_latent_keep(&c, t.p(t.starts), t.p(t.keep_starts), t.p(t.keep), t.total, t.count,
+                                              current_stream(dev.device)));
+    END_HANDLE_TH_ERRORS
+}
+
+// latent_attn(q, cache, table, q_starts, lengths, scale, masks, max_new,
+//             max_length, out, workspace)
+PyObject* latent_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 11);
+    const at::Tensor &q = tensor(a[0], "q"), &rows = tensor(a[1], "cache"), &table = tensor(a[2], "table");
+    const q4g128_latent_cache c = latent_of(rows, table);
+    if (q.dim() != 3) value_error("q must be [T][heads][latent + 64]");
+    const int64_t tokens = q.size(0), heads = q.size(1);
+    check(q, "q", at::kHalf, {tokens, heads, c.latent + Q4G128_LATENT_ROT});
+    const SameDevice dev(rows);
+    const at::Tensor &starts = tensor(a[3], "q_starts"), &lengths = tensor(a[4], "lengths");
+    if (lengths.dim() != 1) value_error("lengths must be [sequences]");
+    const int64_t count = lengths.size(0);
+    check(lengths, "lengths", at::kInt, {count});
+    check(starts, "q_starts", at::kInt, {count + 1});
+    dev.add(q), dev.add(table), dev.add(starts), dev.add(lengths);
+    if (count > c.sequences)
+        value_error("table has %lld sequences, fewer than %lld", (long long)c.sequences, (long long)count);
+    const uint64_t* masks = optional<uint64_t>(a[6], "masks", at::kLong, {tokens}, dev);
+    const int64_t most = masks ? Q4G128_MAX_DRAFT : Q4G128_MAX_TOKENS;
+    const int64_t max_new = a[7] == Py_None ? std::min(tokens, most) : integer(a[7]);
+    const int64_t max_length = a[8] == Py_None ? c.table_cols * c.page : integer(a[8]);
+    const int32_t h = heads > INT32_MAX ? -1 : (int32_t)heads;
+    const int64_t need = q4g128_latent_attn_workspace(h, c.latent, max_new);
+    if (need < 0) return PyLong_FromLongLong(need);
+    const float scale = real(a[5]);
+    const c10::DeviceGuard guard(dev.device);
+    const hipStream_t stream = current_stream(dev.device);
+    const at::Tensor out = output(a[9], "out", {tokens, heads, c.latent}, dev);
+    const at::Tensor ws = workspace_of(a[10], need, dev, stream);
+    return answer(q4g128_latent_attn(static_cast<const uint16_t*>(q.data_ptr()), &c,
+                                     static_cast<const int32_t*>(starts.data_ptr()),
+                                     static_cast<const int32_t*>(lengths.data_ptr()), masks, max_new, max_length, tokens,
+                                     count, h, scale, static_cast<uint16_t*>(out.data_ptr()), ws.data_ptr(), ws.numel(),
+                                     stream),
+                  out);
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"rope_append", (PyCFunction)(void (*)(void))rope_append, METH_FASTCALL, nullptr},
     {"attn_decode", (PyCFunction)(void (*)(void))attn_decode, METH_FASTCALL, nullptr},
     {"attn_prefill", (PyCFunction)(void (*)(void))attn_prefill, METH_FASTCALL, nullptr},
     {"attn_tree", (PyCFunction)(void (*)(void))attn_tree, METH_FASTCALL, nullptr},
     {"cache_keep", (PyCFunction)(void (*)(void))cache_keep, METH_FASTCALL, nullptr},
+    {"latent_append", (PyCFunction)(void (*)(void))latent_append, METH_FASTCALL, nullptr},
+    {"latent_keep", (PyCFunction)(void (*)(void))latent_keep, METH_FASTCALL, nullptr},
+    {"latent_attn", (PyCFunction)(void (*)(void))latent_attn, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
