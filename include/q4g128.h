@@ -487,6 +487,42 @@ Q4_API q4_status q4g128_latent_attn(const uint16_t* q, const q4g128_latent_cache
                              uint16_t* out, void* workspace, int64_t workspace_bytes,
                              void* stream);
 
+/*
+ * q4g128_latent_expand -- keys and values of every head from latent rows, for the
+ * prompts of the expanded form: for each position j of sequence s with firsts[s] <=
+ * j < lengths[s] (firsts int32 [count], or NULL: 0; lengths above max_length count as
+ * max_length) and head h
+ *     k[j][h] = (W_k[h] c_j, r_j),  v[j][h] = W_v[h] c_j,
+ * c_j the `latent` columns and r_j the 64 rotary ones of its row.  The weights are
+ * int4 in the layout above, N = heads * 2 * value rows of K = latent columns, each
+ * head's `value` key rows before its value rows; each enters as fp16(code*scale+min)
+ * with one rounding, as in q4g128_gemm_prefill; sums are fp32, rounded once to fp16.
+ *   expanded: a q4g128_kv_cache with a kv head for every head and dim = value (64 or
+ *   128), whose keys are value + 64 wide: k [pages][heads][page][value + 64] (k_stride
+ *   at least heads*page*(value+64)), v [pages][heads][value][page].  Its table may be
+ *   the latent cache's, if their pages are alike.  heads at most
+ *   Q4G128_MAX_HEADS.  Positions without a page in either cache are not written, and
+ *   nothing but the positions named above is.  No two sequences may share a page of
+ *   `expanded` that both write.
+ */
+Q4_API q4_status q4g128_latent_expand(const q4g128_latent_cache* cache, const int32_t* lengths,
+                             const int32_t* firsts, int64_t max_length, int64_t count,
+                             const uint8_t* packed, const uint16_t* scales, const uint16_t* mins,
+                             const q4g128_kv_cache* expanded, void* stream);
+
+/*
+ * q4g128_latent_prefill -- q4g128_attn_prefill over expanded keys and values:
+ *   q [tokens][heads][value + 64], out [tokens][heads][value] fp16, each head with
+ *   keys and values of its own.  Causal, no options but the scale (> 0, finite).
+ *   Workspace: q4g128_latent_prefill_workspace() bytes, as in q4g128_attn_prefill.
+ */
+Q4_API int64_t q4g128_latent_prefill_workspace(int64_t tokens, int64_t count, int32_t heads,
+                             int32_t value, int64_t max_length);
+Q4_API q4_status q4g128_latent_prefill(const uint16_t* q, const q4g128_kv_cache* expanded,
+                             const int32_t* q_starts, const int32_t* lengths, int64_t max_length,
+                             int64_t tokens, int64_t count, float scale, uint16_t* out,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 Q4_API const char* q4g128_status_string(q4_status status);
 

@@ -84,6 +84,9 @@ EXPORTED = (
     "q4g128_latent_keep",
     "q4g128_latent_attn_workspace",
     "q4g128_latent_attn",
+    "q4g128_latent_expand",
+    "q4g128_latent_prefill_workspace",
+    "q4g128_latent_prefill",
     "q4g128_status_string",
     "q4g128_last_hip_error",
 )
@@ -128,6 +131,9 @@ def _load():
     lib.q4g128_latent_keep.argtypes = [latent, vp, vp, vp, i64, i64, vp]
     lib.q4g128_latent_attn_workspace.argtypes = [i32, i32, i64]
     lib.q4g128_latent_attn.argtypes = [vp, latent, vp, vp, vp, i64, i64, i64, i64, i32, f32, vp, vp, i64, vp]
+    lib.q4g128_latent_expand.argtypes = [latent, vp, vp, i64, i64, vp, vp, vp, cache, vp]
+    lib.q4g128_latent_prefill_workspace.argtypes = [i64, i64, i32, i32, i64]
+    lib.q4g128_latent_prefill.argtypes = [vp, cache, vp, vp, i64, i64, i64, f32, vp, vp, i64, vp]
     lib.q4g128_attn_decode_workspace.argtypes = [i64, i32, i32]
     lib.q4g128_attn_decode.argtypes = [vp, cache, vp, i64, i64, i32, options, vp, vp, i64, vp]
     lib.q4g128_attn_prefill_workspace.argtypes = [i64, i64, i32, i32, i32, i64]
@@ -136,10 +142,11 @@ def _load():
                  "q4g128_gemm_prefill",
                  "q4g128_gemv_int8", "q4g128_gemm_prefill_epilogue", "q4g128_rope_append", "q4g128_attn_decode",
                  "q4g128_attn_prefill", "q4g128_rope_append_slots", "q4g128_cache_keep", "q4g128_attn_tree",
-                 "q4g128_latent_append", "q4g128_latent_keep", "q4g128_latent_attn"):
+                 "q4g128_latent_append", "q4g128_latent_keep", "q4g128_latent_attn",
+                 "q4g128_latent_expand", "q4g128_latent_prefill"):
         getattr(lib, name).restype = ctypes.c_int32
     for name in ("q4g128_attn_decode_workspace", "q4g128_attn_prefill_workspace", "q4g128_attn_tree_workspace",
-                 "q4g128_latent_attn_workspace"):
+                 "q4g128_latent_attn_workspace", "q4g128_latent_prefill_workspace"):
         getattr(lib, name).restype = ctypes.c_int64
     lib.q4g128_status_string.argtypes = [ctypes.c_int32]
     lib.q4g128_status_string.restype = ctypes.c_char_p
@@ -521,6 +528,38 @@ def q4g128_latent_attn(q, cache, table, q_starts, lengths, scale, masks=None, ma
                                       workspace)
     return _answer(_binding.latent_attn(q, cache, table, q_starts, lengths, scale, masks, max_new, max_length, out,
                                         workspace), "q4g128_latent_attn")
+
+
+def q4g128_latent_expand(cache, table, lengths, packed, scales, mins, k_cache, v_cache, expanded_table, firsts=None,
+                         max_length=None, stream=None) -> None:
+    """Keys and values of every head from latent rows by int4 weights, into pages that q4g128_latent_prefill reads.
+
+    packed, scales, mins: the format of q4g128_quantize for [heads * 2 * value][latent], each head's key rows before its
+    value rows.  k_cache fp16 [pages][heads][page][value + 64], v_cache fp16 [pages][heads][value][page], expanded_table
+    int32 [sequences][cols] (value 64 or 128).  Positions firsts[s] (int32 [S]; None: 0) to lengths[s] - 1 are written.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_latent_expand(cache, table, lengths, packed, scales, mins, k_cache, v_cache, expanded_table,
+                                        firsts, max_length)
+    _check(_binding.latent_expand(cache, table, lengths, packed, scales, mins, k_cache, v_cache, expanded_table, firsts,
+                                  max_length), "q4g128_latent_expand")
+
+
+def q4g128_latent_prefill_workspace(tokens, count, heads, value, max_length) -> int:
+    """Bytes of workspace that q4g128_latent_prefill needs (0: none)."""
+    return _lib.q4g128_latent_prefill_workspace(tokens, count, heads, value, max_length)
+
+
+def q4g128_latent_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale, max_length=None, out=None, workspace=None,
+                          stream=None) -> torch.Tensor:
+    """Causal attention of prompt tokens over expanded keys and values: q fp16 [T][heads][value + 64] -> out fp16
+    [T][heads][value].  Caches as q4g128_latent_expand, other arguments as q4g128_attn_prefill."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return q4g128_latent_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale, max_length, out, workspace)
+    return _answer(_binding.latent_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale, max_length, out,
+                                           workspace), "q4g128_latent_prefill")
 
 
 def q4g128_status_string(status: int) -> str:

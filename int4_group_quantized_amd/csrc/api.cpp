@@ -132,39 +132,73 @@ q4_status check_cache(const q4g128_kv_cache* c, int64_t heads, q4::KvCache* out)
     out->sequences = (int)c->sequences;
     out->cols = (int)c->table_cols;
     out->kv_heads = c->kv_heads;
-    out->dim = c->dim;
+    out->dim = out->dim_v = c->dim;
     out->shift = __builtin_ctz((unsigned)c->page);
     return Q4_OK;
 }
 
-// Bytes from the first to past the last element of a pool.
-size_t pool_bytes(const q4::KvCache& c, long stride) {
-    return ((size_t)(c.pages - 1) * (size_t)stride + ((size_t)c.kv_heads * (size_t)c.dim << c.shift)) * 2;
+// Checks a cache of expanded keys (value + 64 columns) and values, one kv head per
+// head: dim is the values' width.
+q4_status check_expanded(const q4g128_kv_cache* c, q4::KvCache* out) {
+    if (!c || !c->k || !c->v || !c->table) return Q4_EINVAL;
+    if (c->pages < 1 || c->sequences < 1 || c->table_cols < 1 || c->kv_heads < 1) return Q4_EINVAL;
+    if (!q4::value_supported(c->dim) || c->kv_heads > Q4G128_MAX_HEADS) return Q4_ESHAPE;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0) return Q4_ESHAPE;
+    if (c->pages > Q4G128_MAX_N || c->sequences > Q4G128_MAX_N || c->table_cols > Q4G128_MAX_N / c->page)
+        return Q4_ESHAPE;
+    const int64_t cell = (int64_t)c->kv_heads * c->page;
+    if (c->k_stride < cell * (c->dim + q4::kRot) || c->v_stride < cell * c->dim || c->k_stride % 8 != 0 ||
+        c->v_stride % 8 != 0 || c->k_stride > INT64_MAX / 4 / c->pages || c->v_stride > INT64_MAX / 4 / c->pages)
+        return Q4_ESHAPE;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4)) return Q4_EALIGN;
+    out->k = c->k;
+    out->v = c->v;
+    out->table = c->table;
+    out->k_stride = c->k_stride;
+    out->v_stride = c->v_stride;
+    out->pages = (int)c->pages;
+    out->sequences = (int)c->sequences;
+    out->cols = (int)c->table_cols;
+    out->kv_heads = c->kv_heads;
+    out->dim = c->dim + q4::kRot;
+    out->dim_v = c->dim;
+    out->shift = __builtin_ctz((unsigned)c->page);
+    return Q4_OK;
 }
+
+// Bytes from the first to past the last element of a pool of rows `dim` wide.
+size_t pool_bytes(const q4::KvCache& c, long stride, int dim) {
+    return ((size_t)(c.pages - 1) * (size_t)stride + ((size_t)c.kv_heads * (size_t)dim << c.shift)) * 2;
+}
+size_t k_bytes(const q4::KvCache& c) { return pool_bytes(c, c.k_stride, c.dim); }
+size_t v_bytes(const q4::KvCache& c) { return c.v ? pool_bytes(c, c.v_stride, c.dim_v) : 0; }
+size_t table_bytes(const q4::KvCache& c) { return (size_t)c.sequences * (size_t)c.cols * 4; }
 
 // Whether the two pools share an element.  Pools whose pages interleave (parts
 // of one larger pool) overlap as ranges without sharing any.
 bool pools_meet(const q4::KvCache& c) {
-    if (!overlaps(c.k, pool_bytes(c, c.k_stride), c.v, pool_bytes(c, c.v_stride))) return false;
+    if (!overlaps(c.k, k_bytes(c), c.v, v_bytes(c))) return false;
     if (c.k_stride != c.v_stride) return true;
     const uintptr_t k = (uintptr_t)c.k, v = (uintptr_t)c.v;
-    const uintptr_t stride = (uintptr_t)c.k_stride * 2, page = ((uintptr_t)c.kv_heads * c.dim << c.shift) * 2;
-    const uintptr_t apart = (k > v ? k - v : v - k) % stride;
-    return apart < page || apart > stride - page;
+    const uintptr_t stride = (uintptr_t)c.k_stride * 2, cell = ((uintptr_t)c.kv_heads << c.shift) * 2;
+    // How far a page of V begins behind one of K.
+    const uintptr_t behind = v >= k ? (v - k) % stride : (stride - (k - v) % stride) % stride;
+    return behind < cell * c.dim || behind > stride - cell * c.dim_v;
 }
 
 // Whether [p, p + bytes) meets one of the cache's pools or its table.
 bool hits_cache(const q4::KvCache& c, const void* p, size_t bytes) {
-    return overlaps(p, bytes, c.k, pool_bytes(c, c.k_stride)) || overlaps(p, bytes, c.v, pool_bytes(c, c.v_stride)) ||
-           overlaps(p, bytes, c.table, (size_t)c.sequences * (size_t)c.cols * 4);
+    return overlaps(p, bytes, c.k, k_bytes(c)) || (c.v && overlaps(p, bytes, c.v, v_bytes(c))) ||
+           overlaps(p, bytes, c.table, table_bytes(c));
 }
 
 // Shared checks of the two attention calls; `rows` = batch or tokens.
 q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* lengths, int64_t max_length,
                           int64_t rows, int64_t sequences, int64_t heads, const q4g128_attn_options* o, uint16_t* out,
-                          void* workspace, int64_t workspace_bytes, int64_t workspace_needed, q4::AttnArgs* a) {
+                          void* workspace, int64_t workspace_bytes, int64_t workspace_needed, q4::AttnArgs* a,
+                          bool expanded = false) {
     if (!q || !lengths || !o || !out || rows < 1 || sequences < 1 || max_length < 1) return Q4_EINVAL;
-    q4_status s = check_cache(cache, heads, &a->c);
+    q4_status s = expanded ? check_expanded(cache, &a->c) : check_cache(cache, heads, &a->c);
     if (s != Q4_OK) return s;
     if (rows > Q4G128_MAX_TOKENS || sequences > Q4G128_MAX_SEQUENCES || sequences > cache->sequences ||
         max_length > cache->table_cols * cache->page)
@@ -177,15 +211,16 @@ q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const
         !aligned(o->prefix, 4) || !aligned(workspace, 16))
         return Q4_EALIGN;
     if (workspace_needed > 0 && (!workspace || workspace_bytes < workspace_needed)) return Q4_EINVAL;
-    const size_t qbytes = (size_t)rows * (size_t)heads * (size_t)cache->dim * 2;
+    const size_t qbytes = (size_t)rows * (size_t)heads * (size_t)a->c.dim * 2;
+    const size_t obytes = (size_t)rows * (size_t)heads * (size_t)a->c.dim_v * 2;
     const size_t seqbytes = (size_t)sequences * 4, wsbytes = (size_t)workspace_needed;
-    if (hits_cache(a->c, out, qbytes) || overlaps(out, qbytes, q, qbytes) || overlaps(out, qbytes, lengths, seqbytes) ||
-        (o->slopes && overlaps(out, qbytes, o->slopes, (size_t)heads * 4)) ||
-        (o->prefix && overlaps(out, qbytes, o->prefix, seqbytes)))
+    if (hits_cache(a->c, out, obytes) || overlaps(out, obytes, q, qbytes) || overlaps(out, obytes, lengths, seqbytes) ||
+        (o->slopes && overlaps(out, obytes, o->slopes, (size_t)heads * 4)) ||
+        (o->prefix && overlaps(out, obytes, o->prefix, seqbytes)))
         return Q4_EINVAL;
     if (wsbytes > 0 &&
         (hits_cache(a->c, workspace, wsbytes) || overlaps(workspace, wsbytes, q, qbytes) ||
-         overlaps(workspace, wsbytes, out, qbytes) || overlaps(workspace, wsbytes, lengths, seqbytes) ||
+         overlaps(workspace, wsbytes, out, obytes) || overlaps(workspace, wsbytes, lengths, seqbytes) ||
          (o->slopes && overlaps(workspace, wsbytes, o->slopes, (size_t)heads * 4)) ||
          (o->prefix && overlaps(workspace, wsbytes, o->prefix, seqbytes))))
         return Q4_EINVAL;
@@ -229,15 +264,9 @@ q4_status check_latent(const q4g128_latent_cache* c, q4::KvCache* out) {
     out->sequences = (int)c->sequences;
     out->cols = (int)c->table_cols;
     out->kv_heads = 1;
-    out->dim = dim;
+    out->dim = out->dim_v = dim;
     out->shift = __builtin_ctz((unsigned)c->page);
     return Q4_OK;
-}
-
-// Whether [p, p + bytes) meets a latent cache's rows or its table.
-bool hits_latent(const q4::KvCache& c, const void* p, size_t bytes) {
-    return overlaps(p, bytes, c.k, pool_bytes(c, c.k_stride)) ||
-           overlaps(p, bytes, c.table, (size_t)c.sequences * (size_t)c.cols * 4);
 }
 
 // Row numbers and masks of new tokens, against what a call writes.
@@ -257,8 +286,7 @@ q4_status keep_tokens(q4::KeepArgs* a, const int32_t* starts, const int32_t* kee
     if (!starts || !keep_starts || (!keep && total > 0) || total < 0 || count < 1) return Q4_EINVAL;
     if (count > Q4G128_MAX_SEQUENCES || count > a->c.sequences || total > Q4G128_MAX_TOKENS) return Q4_ESHAPE;
     if (!aligned(starts, 4) || !aligned(keep_starts, 4) || !aligned(keep, 4)) return Q4_EALIGN;
-    const size_t kbytes = pool_bytes(a->c, a->c.k_stride), vbytes = a->c.v ? pool_bytes(a->c, a->c.v_stride) : 0;
-    const size_t tbytes = (size_t)a->c.sequences * (size_t)a->c.cols * 4;
+    const size_t kbytes = k_bytes(a->c), vbytes = v_bytes(a->c), tbytes = table_bytes(a->c);
     const void* in[] = {a->c.table, starts, keep_starts, keep};
     const size_t inbytes[] = {tbytes, (size_t)count * 4, (size_t)(count + 1) * 4, (size_t)total * 4};
     for (int i = 0; i < 4; ++i)
@@ -446,8 +474,8 @@ q4_status q4g128_rope_append_slots(const float* qkv, int64_t ld, int64_t tokens,
     const size_t inbytes[] = {((size_t)(tokens - 1) * (size_t)ld + (size_t)columns) * 4, (size_t)tokens * 4,
                               (size_t)tokens * 4, (size_t)tokens * 4, (size_t)rot * 2, nbytes, nbytes};
     if (pools_meet(a.c)) return Q4_EINVAL;
-    const size_t kbytes = pool_bytes(a.c, a.c.k_stride), vbytes = pool_bytes(a.c, a.c.v_stride);
-    const size_t tbytes = (size_t)a.c.sequences * (size_t)a.c.cols * 4;
+    const size_t kbytes = k_bytes(a.c), vbytes = v_bytes(a.c);
+    const size_t tbytes = table_bytes(a.c);
     if (hits_cache(a.c, q, qbytes) || overlaps(a.c.k, kbytes, a.c.table, tbytes) ||
         overlaps(a.c.v, vbytes, a.c.table, tbytes))
         return Q4_EINVAL;
@@ -509,7 +537,7 @@ int64_t q4g128_attn_prefill_workspace(int64_t tokens, int64_t count, int32_t hea
         heads % kv_heads != 0 || heads / kv_heads > Q4G128_MAX_GROUP || !q4::attn_dim_supported(dim) ||
         max_length > Q4G128_MAX_N)
         return Q4_ESHAPE;
-    return q4::attn_prefill_workspace(tokens, count, heads, kv_heads, dim, max_length);
+    return q4::attn_prefill_workspace(tokens, count, heads, kv_heads, dim, dim, max_length);
 }
 
 q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* q_starts,
@@ -594,15 +622,15 @@ q4_status q4g128_latent_append(const float* kv, int64_t ld, int64_t tokens, cons
     if (!aligned(kv, 16) || !aligned(seq, 4) || !aligned(positions, 4) || !aligned(slots, 4) || !aligned(inv_freq, 4) ||
         !aligned(norm, 2) || (heads > 0 && (!aligned(q_main, 16) || !aligned(q_rot, 16) || !aligned(q, 16))))
         return Q4_EALIGN;
-    const size_t n = (size_t)tokens, h = (size_t)heads, rows = pool_bytes(a.c, a.c.k_stride);
+    const size_t n = (size_t)tokens, h = (size_t)heads, rows = k_bytes(a.c);
     const size_t qbytes = n * h * (size_t)wide * 2;
     const void* in[] = {kv, seq, positions, slots, inv_freq, norm, heads ? q_main : nullptr, heads ? q_rot : nullptr};
     const size_t inbytes[] = {((n - 1) * (size_t)ld + (size_t)row) * 4, n * 4, n * 4, n * 4, (size_t)q4::kRot * 2,
                               (size_t)cache->latent * 2,
                               heads ? ((n - 1) * (size_t)main_ld + (h - 1) * (size_t)main_head + (size_t)main) * 4 : 0,
                               heads ? ((n - 1) * (size_t)rot_ld + (h - 1) * (size_t)rot_head + q4::kRot) * 4 : 0};
-    if (overlaps(a.c.k, rows, a.c.table, (size_t)a.c.sequences * (size_t)a.c.cols * 4) ||
-        (heads > 0 && hits_latent(a.c, q, qbytes)))
+    if (overlaps(a.c.k, rows, a.c.table, table_bytes(a.c)) ||
+        (heads > 0 && hits_cache(a.c, q, qbytes)))
         return Q4_EINVAL;
     for (int i = 0; i < 8; ++i)
         if (in[i] && (overlaps(a.c.k, rows, in[i], inbytes[i]) || (heads > 0 && overlaps(q, qbytes, in[i], inbytes[i]))))
@@ -664,8 +692,8 @@ q4_status q4g128_latent_attn(const uint16_t* q, const q4g128_latent_cache* cache
     const size_t rows = (size_t)tokens * (size_t)heads;
     const size_t qbytes = rows * (size_t)x.a.c.dim * 2, obytes = rows * (size_t)cache->latent * 2;
     const size_t lbytes = (size_t)count * 4, wsbytes = (size_t)need;
-    if (hits_latent(x.a.c, out, obytes) || overlaps(out, obytes, q, qbytes) || overlaps(out, obytes, lengths, lbytes) ||
-        hits_latent(x.a.c, workspace, wsbytes) || overlaps(workspace, wsbytes, q, qbytes) ||
+    if (hits_cache(x.a.c, out, obytes) || overlaps(out, obytes, q, qbytes) || overlaps(out, obytes, lengths, lbytes) ||
+        hits_cache(x.a.c, workspace, wsbytes) || overlaps(workspace, wsbytes, q, qbytes) ||
         overlaps(workspace, wsbytes, out, obytes) || overlaps(workspace, wsbytes, lengths, lbytes))
         return Q4_EINVAL;
     s = check_new(q_starts, masks, tokens, count, out, obytes, workspace, wsbytes);
@@ -691,6 +719,75 @@ q4_status q4g128_latent_attn(const uint16_t* q, const q4g128_latent_cache* cache
     s = current_device(&dev);
     if (s != Q4_OK) return s;
     hipError_t e = q4::launch_latent_attn(x, dev, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+q4_status q4g128_latent_expand(const q4g128_latent_cache* cache, const int32_t* lengths, const int32_t* firsts,
+                               int64_t max_length, int64_t count, const uint8_t* packed, const uint16_t* scales,
+                               const uint16_t* mins, const q4g128_kv_cache* expanded, void* stream) {
+    if (!lengths || !packed || !scales || !mins || count < 1 || max_length < 1) return Q4_EINVAL;
+    q4::ExpandArgs a;
+    q4_status s = check_latent(cache, &a.c);
+    if (s != Q4_OK) return s;
+    s = check_expanded(expanded, &a.to);
+    if (s != Q4_OK) return s;
+    if (count > Q4G128_MAX_SEQUENCES || count > cache->sequences || count > expanded->sequences ||
+        max_length > cache->table_cols * cache->page || max_length > expanded->table_cols * expanded->page)
+        return Q4_ESHAPE;
+    if (!aligned(lengths, 4) || !aligned(firsts, 4) || !aligned(packed, 16) || !aligned(scales, 2) || !aligned(mins, 2))
+        return Q4_EALIGN;
+    const size_t n = (size_t)expanded->kv_heads * 2 * (size_t)expanded->dim, l = (size_t)cache->latent;
+    const size_t kbytes = k_bytes(a.to), vbytes = v_bytes(a.to);
+    const void* in[] = {lengths, firsts, packed, scales, mins, a.c.k, a.c.table, a.to.table};
+    const size_t inbytes[] = {(size_t)count * 4, (size_t)count * 4, n * l / 2, n * (l / 128) * 2, n * (l / 128) * 2,
+                              k_bytes(a.c), table_bytes(a.c), table_bytes(a.to)};
+    for (int i = 0; i < 8; ++i)
+        if (in[i] && (overlaps(a.to.k, kbytes, in[i], inbytes[i]) || overlaps(a.to.v, vbytes, in[i], inbytes[i])))
+            return Q4_EINVAL;
+    if (pools_meet(a.to)) return Q4_EINVAL;
+    a.lengths = lengths;
+    a.firsts = firsts;
+    a.max_length = (int)max_length;
+    a.count = (int)count;
+    a.packed = packed;
+    a.scales = scales;
+    a.mins = mins;
+    q4::DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != Q4_OK) return s;
+    hipError_t e = q4::launch_latent_expand(a, dev, (hipStream_t)stream);
+    return e == hipSuccess ? Q4_OK : device_error(e);
+}
+
+int64_t q4g128_latent_prefill_workspace(int64_t tokens, int64_t count, int32_t heads, int32_t value, int64_t max_length) {
+    if (tokens < 1 || count < 1 || heads < 1 || max_length < 1) return Q4_EINVAL;
+    if (tokens > Q4G128_MAX_TOKENS || count > Q4G128_MAX_SEQUENCES || heads > Q4G128_MAX_HEADS ||
+        !q4::value_supported(value) || max_length > Q4G128_MAX_N)
+        return Q4_ESHAPE;
+    return q4::attn_prefill_workspace(tokens, count, heads, heads, value + q4::kRot, value, max_length);
+}
+
+q4_status q4g128_latent_prefill(const uint16_t* q, const q4g128_kv_cache* expanded, const int32_t* q_starts,
+                                const int32_t* lengths, int64_t max_length, int64_t tokens, int64_t count, float scale,
+                                uint16_t* out, void* workspace, int64_t workspace_bytes, void* stream) {
+    q4::AttnArgs a;
+    if (!q_starts) return Q4_EINVAL;
+    const int32_t heads = expanded ? expanded->kv_heads : 0;
+    const int64_t need = expanded ? q4g128_latent_prefill_workspace(tokens, count, heads, expanded->dim, max_length)
+                                  : Q4_EINVAL;
+    if (need < 0) return (q4_status)need;
+    const q4g128_attn_options options = {scale, 0.0f, 0, nullptr, nullptr};
+    q4_status s = check_attention(q, expanded, lengths, max_length, tokens, count, heads, &options, out, workspace,
+                                  workspace_bytes, need, &a, true);
+    if (s != Q4_OK) return s;
+    s = check_new(q_starts, nullptr, tokens, count, out, (size_t)tokens * (size_t)heads * (size_t)expanded->dim * 2,
+                  workspace, (size_t)need);
+    if (s != Q4_OK) return s;
+    a.q_starts = q_starts;
+    q4::DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != Q4_OK) return s;
+    hipError_t e = q4::launch_attn_prefill(a, dev, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

@@ -15,7 +15,7 @@ constexpr int kAttnCounters = 1024;
 
 struct KvCache {
     uint16_t* k;        // [pages][kv_heads][page][dim]
-    uint16_t* v;        // [pages][kv_heads][dim][page]
+    uint16_t* v;        // [pages][kv_heads][dim_v][page]
     const int* table;   // [sequences][cols]
     long k_stride;      // elements from page to page
     long v_stride;
@@ -24,6 +24,7 @@ struct KvCache {
     int cols;
     int kv_heads;
     int dim;
+    int dim_v;          // dim, but for expanded latent rows
     int shift;          // log2(page)
 };
 
@@ -90,7 +91,8 @@ hipError_t launch_cache_keep(const KeepArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t st);
 int64_t attn_decode_workspace(int64_t batch, int heads, int dim);
 hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
-int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length);
+int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int dim_v,
+                               int64_t max_length);
 struct NewArgs;  // attn_new.hpp
 hipError_t launch_attn_tree(const NewArgs& x, hipStream_t st);
 int64_t attn_tree_workspace(int heads, int kv_heads, int dim, int max_new);

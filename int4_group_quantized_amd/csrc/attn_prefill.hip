@@ -88,11 +88,11 @@ struct PrefillPlan {
 // tokens of 8 heads on 8,000 18.6 with 42, 16.4 with 32.  A second launch taken
 // for 5 us left 100 tokens on 300 whole (13.2 us, 11.5 split), for 3 it split
 // 1,000 tokens (30.3 us, 24.1 whole).
-static PrefillPlan prefill_split(int rows, long blocks, long length, long tokens, int heads, int dim) {
+static PrefillPlan prefill_split(int rows, long blocks, long length, long tokens, int heads, int dim, int dim_v) {
     // Beyond dim 128 a CU's LDS holds one workgroup: 128 tokens of 16 heads of 256 on
     // 4,000 positions take 33 us in 256 workgroups, 44 in 512.
     const long room = (dim > 128 ? 1 : 2) * kPrefillAlone / blocks, most = room < length ? room : length;
-    const double c = (0.6 + dim / 150.0) * (rows == 64 ? 0.85 : 1.0), v = 8e-6 / 4.0 * (double)tokens * heads * dim;
+    const double c = (0.6 + dim / 150.0) * (rows == 64 ? 0.85 : 1.0), v = 8e-6 / 4.0 * (double)tokens * heads * dim_v;
     PrefillPlan plan = {rows, 1, c * (double)length};
     if (most < 2) return plan;
     long n = (long)(std::sqrt(c * (double)length / v) + 0.5);
@@ -116,20 +116,21 @@ static PrefillPlan prefill_split(int rows, long blocks, long length, long tokens
 // call that would be split takes them only with up to 64 workgroups (16 tokens
 // on 16,000 positions 19.9 against 21.3; 34 tokens of 32 heads on 4 kv heads
 // on 8,000 24.0 against 27.2).
-static PrefillPlan prefill_plan(long tokens, long count, int heads, int kv_heads, int dim, long max_length) {
+static PrefillPlan prefill_plan(long tokens, long count, int heads, int kv_heads, int dim, int dim_v, long max_length) {
     const int group = heads / kv_heads;
     const long length = (max_length + kTileKeys - 1) / kTileKeys;
     const long large = prefill_tiles(tokens, count, 128, group) * kv_heads;
     const long small = prefill_tiles(tokens, count, 64, group) * kv_heads;
-    const PrefillPlan plan = prefill_split(128, large, length, tokens, heads, dim);
+    const PrefillPlan plan = prefill_split(128, large, length, tokens, heads, dim, dim_v);
     if (dim == 96 || small > (plan.splits > 1 ? kPrefillAlone / 4 : kPrefillAlone)) return plan;
-    return prefill_split(64, small, length, tokens, heads, dim);
+    return prefill_split(64, small, length, tokens, heads, dim, dim_v);
 }
 
-int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int64_t max_length) {
-    const int splits = prefill_plan(tokens, count, heads, kv_heads, dim, max_length).splits;
+int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int dim_v,
+                               int64_t max_length) {
+    const int splits = prefill_plan(tokens, count, heads, kv_heads, dim, dim_v, max_length).splits;
     // The counters of the decode call come first, so that both can share one.
-    return splits == 1 ? 0 : ((int64_t)splits * tokens * heads * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
+    return splits == 1 ? 0 : ((int64_t)splits * tokens * heads * (dim_v + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
 
 struct PrefillTile {
@@ -270,10 +271,10 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // has met such a tile start their rows again here, after the fast loop and with
 // nothing of it live, because the same handling inside that loop cost it 100
 // registers (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
-template <int D, int OPTIONS, int SHARE>
+template <int D, int DV, int OPTIONS, int SHARE>
 __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
                                                         int split, int kvh, int wave, int k_begin, int k_end) {
-    constexpr int OUT = D / (2 * SHARE);  // output dimensions of a lane
+    constexpr int OUT = DV / (2 * SHARE);  // output dimensions of a lane
     const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
     const int o0 = (2 * (wave % SHARE) + (lane >> 5)) * OUT;
     const PrefillRow q = prefill_row(a, it, prefix, kvh, wave / SHARE * 32 + n);
@@ -291,7 +292,7 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
         const _Float16* kp = reinterpret_cast<const _Float16*>(a.c.k) + (size_t)page * a.c.k_stride +
                              (((size_t)kvh << a.c.shift) + (key & pmask)) * D + d0;
         const _Float16* vp = reinterpret_cast<const _Float16*>(a.c.v) + (size_t)page * a.c.v_stride +
-                             ((size_t)(kvh * D + o0) << a.c.shift) + (key & pmask);
+                             ((size_t)(kvh * DV + o0) << a.c.shift) + (key & pmask);
         float dot = 0.0f;
 #pragma unroll 4
         for (int i = 0; i < D / 2; ++i) dot = __builtin_fmaf((float)qp[i], (float)kp[i], dot);
@@ -307,8 +308,8 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
     }
     if (!q.live) return;
     const long at = ((long)split * a.rows + q.token) * a.heads + q.head;
-    float* po = a.workspace + kAttnCounters + at * D + o0;
-    _Float16* op = reinterpret_cast<_Float16*>(a.out) + ((size_t)q.token * a.heads + q.head) * D + o0;
+    float* po = a.workspace + kAttnCounters + at * DV + o0;
+    _Float16* op = reinterpret_cast<_Float16*>(a.out) + ((size_t)q.token * a.heads + q.head) * DV + o0;
     const bool partial = a.splits > 1;
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -317,7 +318,7 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
         else op[i] = (_Float16)(acc[i] * inv);
     }
     if (partial && o0 == 0) {
-        float* ml = a.workspace + kAttnCounters + (long)a.splits * a.rows * a.heads * D + at * 2;
+        float* ml = a.workspace + kAttnCounters + (long)a.splits * a.rows * a.heads * DV + at * 2;
         ml[0] = m;
         ml[1] = l;
     }
@@ -332,16 +333,18 @@ struct PrefillShared {
     int found[WAVES];                       // a wave has seen infinities or NaN where a row is masked
 };
 
-template <int D, int OPTIONS, int ROWS>
+template <int D, int DV, int OPTIONS, int ROWS>
 __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 64 ? 1 : 2)
     attn_prefill_kernel(AttnArgs a, int tile0) {
     constexpr int SHARE = prefill_share(D, ROWS), THREADS = prefill_threads(D, ROWS), WAVES = THREADS / 64;
     constexpr bool EXTRA = OPTIONS != kNoOptions;
     constexpr int KEYS = 2 / SHARE;                 // blocks of 32 keys of a wave
-    constexpr int DIMS = D / (32 * SHARE);          // and of 32 output dimensions
+    constexpr int DIMS = DV / (32 * SHARE);         // and of 32 output dimensions
     constexpr int C = D / 8;                        // 16-byte chunks of a K row
-    constexpr int STAGE = kTileKeys * C / THREADS;  // chunks per thread and tile, for K and for V
-    constexpr int IMAGE = 2 * kTileKeys * C;        // chunks of a tile's image
+    constexpr int STAGE = kTileKeys * C / THREADS;  // chunks per thread and tile, for K
+    constexpr int STAGE_V = kTileKeys * (DV / 8) / THREADS;  // and for V
+    constexpr int PIECES = STAGE + STAGE_V;
+    constexpr int IMAGE = kTileKeys * (C + DV / 8);          // chunks of a tile's image
     extern __shared__ u4 lds[];                     // a.images of them, used in turn, and PrefillShared
     const int splits = a.splits;
     const int kvh = blockIdx.x, split = blockIdx.y;
@@ -458,11 +461,11 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         const size_t p = (size_t)max(pg.p0, 0);
         Whole w;
         w.k = uniform(a.c.k + p * a.c.k_stride + (((size_t)kvh << a.c.shift) + off) * D);
-        w.v = uniform(a.c.v + p * a.c.v_stride + ((size_t)(kvh * D) << a.c.shift) + off);
+        w.v = uniform(a.c.v + p * a.c.v_stride + ((size_t)(kvh * DV) << a.c.shift) + off);
         w.to = lds_at + image * (IMAGE * 16);
         return w;
     };
-    auto load_piece = [&](const Whole& w, int j) {  // 0 <= j < 2 STAGE
+    auto load_piece = [&](const Whole& w, int j) {  // 0 <= j < PIECES
         if (j < STAGE) load_lds(w.k, k_at[j], w.to + 16 * THREADS * j);
         else load_lds(w.v + ((size_t)(THREADS / 8 * (j - STAGE)) << a.c.shift), v_at, w.to + 16 * THREADS * j);
     };
@@ -472,11 +475,11 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         if (a.c.shift >= 6) {
             const Whole w = whole(t, pg, image);
 #pragma unroll
-            for (int j = 0; j < 2 * STAGE; ++j) load_piece(w, j);
+            for (int j = 0; j < PIECES; ++j) load_piece(w, j);
         } else {
             // Quarters of 16 positions, each in a page of its own or shared.
             const size_t vpage = pg.of(v_c >> 1);
-            const uint16_t* vp = a.c.v + vpage * a.c.v_stride + ((size_t)(kvh * D + (tid >> 3)) << a.c.shift) +
+            const uint16_t* vp = a.c.v + vpage * a.c.v_stride + ((size_t)(kvh * DV + (tid >> 3)) << a.c.shift) +
                                  ((kb + 8 * v_c) & pmask);
 #pragma unroll
             for (int j = 0; j < STAGE; ++j) {
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                 load_lds(a.c.k + pg.of(key >> 4) * a.c.k_stride + (((size_t)kvh << a.c.shift) + ((kb + key) & pmask)) * D +
                              8 * (k_chunk<D>(key, x % C) - key * C),
                          to + 16 * THREADS * j);
-                load_lds(vp + ((size_t)(THREADS / 8 * j) << a.c.shift), to + kTileKeys * C * 16 + 16 * THREADS * j);
+                if (j < STAGE_V) load_lds(vp + ((size_t)(THREADS / 8 * j) << a.c.shift), to + kTileKeys * C * 16 + 16 * THREADS * j);
             }
         }
     };
@@ -531,11 +534,11 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         const int kb = t_use * kTileKeys, gone = gone_bits & 15;
         u4* im = lds + slot * IMAGE;
         slot = slot == ahead ? 0 : slot + 1;
-        // This tile's loads are done (2 STAGE operations per newer tile may be
+        // This tile's loads are done (PIECES operations per newer tile may be
         // under way), and everyone has read the image that the next request
         // overwrites.
-        if (t_load - t_use == 3) wait_and_meet<4 * STAGE>();
-        else if (t_load - t_use == 2) wait_and_meet<2 * STAGE>();
+        if (t_load - t_use == 3) wait_and_meet<2 * PIECES>();
+        else if (t_load - t_use == 2) wait_and_meet<PIECES>();
         else wait_and_meet<0>();
         Whole next;
         if constexpr (SPREAD) {
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         if (gone || kb + kTileKeys > it.len) {
             // Values past the end and of absent pages are cleared: their weight is
             // zero, but zero times what an unwritten slot holds may be NaN.
-            for (int i = tid; i < D * (kTileKeys / 8); i += THREADS) {
+            for (int i = tid; i < DV * (kTileKeys / 8); i += THREADS) {
                 const int dim = i >> 3, vc = i & 7;
                 const int keep = (gone >> (vc >> 1)) & 1 ? 0 : min(max(it.len - (kb + 8 * vc), 0), 8);
                 u4 mask;
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
             // Masked for some row.  A weight of zero hides a masked value only if the
             // value is finite: each wave looks at its share of the values.
 #pragma unroll
-            for (int i = 0; i < D * (kTileKeys / 8); i += THREADS) {
+            for (int i = 0; i < DV * (kTileKeys / 8); i += THREADS) {
                 const u4 v = im[kTileKeys * C + i + tid];
                 bad |= odd_halves(v.x) | odd_halves(v.y) | odd_halves(v.z) | odd_halves(v.w);
             }
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         if (kb >= any_hi) {
             if constexpr (SPREAD) {
 #pragma unroll
-                for (int j = 0; j < 2 * STAGE; ++j) load_piece(next, j);
+                for (int j = 0; j < PIECES; ++j) load_piece(next, j);
             }
             if constexpr (SHARE > 1) lds_meet();
         } else {
@@ -596,8 +599,8 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                     if (d + KW < STEPS) kf[d % KW][b] = im[k_chunk<D>(32 * b + km, 2 * (d + KW) + h)];
                 }
                 if constexpr (SPREAD) {
-                    constexpr int EVERY = STEPS / (2 * STAGE);
-                    if (d % EVERY == 0) load_piece(next, d / EVERY);
+                    constexpr int EVERY = STEPS / PIECES;
+                    if (d % EVERY == 0 && d / EVERY < PIECES) load_piece(next, d / EVERY);
                 }
             }
             // V operands in the order of use: the wave's own keys first.
@@ -746,7 +749,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) any_found |= shared.found[w];
     if (any_found) {
-        prefill_rows_one_by_one<D, OPTIONS, SHARE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
+        prefill_rows_one_by_one<D, DV, OPTIONS, SHARE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
     if constexpr (SHARE > 1) l += shared.sum[wave ^ 1][n];
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
     if (!live) return;
     if (splits == 1) {
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        uint16_t* op = a.out + ((size_t)token * a.heads + head) * D + 32 * DIMS * part;
+        uint16_t* op = a.out + ((size_t)token * a.heads + head) * DV + 32 * DIMS * part;
 #pragma unroll
         for (int d = 0; d < DIMS; ++d) {
 #pragma unroll
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         }
     } else {
         const long at = ((long)split * a.rows + token) * a.heads + head;
-        float* op = a.workspace + kAttnCounters + at * D + 32 * DIMS * part;
+        float* op = a.workspace + kAttnCounters + at * DV + 32 * DIMS * part;
 #pragma unroll
         for (int d = 0; d < DIMS; ++d) {
 #pragma unroll
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                     (f4){acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
         }
         if (h == 0 && part == 0) {
-            float* ml = a.workspace + kAttnCounters + (long)splits * a.rows * a.heads * D + at * 2;
+            float* ml = a.workspace + kAttnCounters + (long)splits * a.rows * a.heads * DV + at * 2;
             ml[0] = m;
             ml[1] = l;
         }
@@ -797,9 +800,9 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     store_joined(join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits), a.out + r * D);
 }
 
-template <int D, int OPTIONS, int ROWS>
+template <int D, int DV, int OPTIONS, int ROWS>
 static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
-    constexpr size_t image = 2 * kTileKeys * D * sizeof(uint16_t);
+    constexpr size_t image = kTileKeys * (D + DV) * sizeof(uint16_t);
     constexpr size_t behind = sizeof(PrefillShared<prefill_threads(D, ROWS) / 64, (prefill_share(D, ROWS) > 1)>);
     // Two workgroups of four waves per CU hide each other's waits where there are
     // enough of them; fewer workgroups, and those of eight waves, get as many
@@ -808,8 +811,8 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const bool two = prefill_threads(D, ROWS) == 256 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
     const int fit = (int)(((two ? dev.max_lds / 2 : dev.max_lds) - behind) / image);
     a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
-    auto kernel = &attn_prefill_kernel<D, OPTIONS, ROWS>;
-    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, OPTIONS, ROWS>>::value[dev.device];
+    auto kernel = &attn_prefill_kernel<D, DV, OPTIONS, ROWS>;
+    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, DV, OPTIONS, ROWS>>::value[dev.device];
     if (!ready.load(std::memory_order_acquire)) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
@@ -821,7 +824,7 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
-        hipLaunchKernelGGL((attn_prefill_kernel<D, OPTIONS, ROWS>), grid, dim3(prefill_threads(D, ROWS)), a.images * image + behind,
+        hipLaunchKernelGGL((attn_prefill_kernel<D, DV, OPTIONS, ROWS>), grid, dim3(prefill_threads(D, ROWS)), a.images * image + behind,
                            st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -829,42 +832,54 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     return hipSuccess;
 }
 
-template <int D, int OPTIONS>
+template <int D, int DV, int OPTIONS>
 static hipError_t launch_rows(const AttnArgs& a, int rows, const DeviceInfo& dev, hipStream_t st) {
     if constexpr (D != 96) {  // three blocks of 32 dimensions do not share out
-        if (rows == 64) return launch_tiles<D, OPTIONS, 64>(a, dev, st);
+        if (rows == 64) return launch_tiles<D, DV, OPTIONS, 64>(a, dev, st);
     }
-    return launch_tiles<D, OPTIONS, 128>(a, dev, st);
+    return launch_tiles<D, DV, OPTIONS, 128>(a, dev, st);
 }
 
-template <int D>
+template <int D, int DV = D>
 static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     a.inv_group = 1.0f / (float)a.group;
-    PrefillPlan plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, a.max_length);
+    PrefillPlan plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, DV, a.max_length);
     // A window leaves a workgroup fewer positions: 34 tokens on 8,000 with a window of
     // 128 take 9.3 us planned for those, 13.6 for all.  The workspace is for all.
     const long span = (long)a.window + prefill_tokens(128, a.group) + kTileKeys;
     if (a.window > 0 && span < a.max_length) {
         const int most = plan.splits;
-        plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, span);
+        plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, DV, span);
         if (plan.splits > most) plan.splits = most;
     }
     a.splits = plan.splits;
     a.tile = prefill_tokens(plan.rows, a.group);
     a.inv_tile = 1.0f / (float)a.tile;
     hipError_t e = hipSuccess;
-    switch (attn_options(a)) {
-        case kNoOptions: e = launch_rows<D, kNoOptions>(a, plan.rows, dev, st); break;
-        case kOptions: e = launch_rows<D, kOptions>(a, plan.rows, dev, st); break;
-        case kLargeCapOptions: e = launch_rows<D, kLargeCapOptions>(a, plan.rows, dev, st); break;
+    if constexpr (DV != D) {
+        e = launch_rows<D, DV, kNoOptions>(a, plan.rows, dev, st);
+    } else {
+        switch (attn_options(a)) {
+            case kNoOptions: e = launch_rows<D, DV, kNoOptions>(a, plan.rows, dev, st); break;
+            case kOptions: e = launch_rows<D, DV, kOptions>(a, plan.rows, dev, st); break;
+            case kLargeCapOptions: e = launch_rows<D, DV, kLargeCapOptions>(a, plan.rows, dev, st); break;
+        }
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const long rows = (long)a.rows * a.heads;
-    hipLaunchKernelGGL((attn_prefill_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attn_prefill_join_kernel<DV>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st) {
+    if (a.c.dim_v != a.c.dim) {
+        // Keys with a rotary part beside the values' width, without options.
+        switch (a.c.dim) {
+            case 128: return launch_prefill_attn<128, 64>(a, dev, st);
+            case 192: return launch_prefill_attn<192, 128>(a, dev, st);
+        }
+        return hipErrorInvalidValue;  // widths are validated before
+    }
     switch (a.c.dim) {
         case 64: return launch_prefill_attn<64>(a, dev, st);
         case 96: return launch_prefill_attn<96>(a, dev, st);

@@ -545,6 +545,101 @@ PyObject* latent_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The descriptor of a cache of expanded keys and values.
+q4g128_kv_cache expanded_of(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table) {
+    for (const auto& p : {std::make_pair(&k, "k_cache"), std::make_pair(&v, "v_cache")}) {
+        on_gpu(*p.first, p.second);
+        of_type(*p.first, p.second, at::kHalf);
+        if (p.first->dim() != 4)
+            value_error("k_cache must be [pages][heads][page][value + 64], v_cache [pages][heads][value][page]");
+    }
+    const int64_t pages = k.size(0), heads = k.size(1), page = k.size(2), dim = k.size(3) - Q4G128_LATENT_ROT;
+    if (dim < 0 || v.size(0) != pages || v.size(1) != heads || v.size(2) != dim || v.size(3) != page)
+        value_error("v_cache must have shape %s (got %s)", shape_text({pages, heads, dim, page}).c_str(),
+                    shape_text(v.sizes()).c_str());
+    if (!page_contiguous(k) || !page_contiguous(v))
+        value_error("each page of k_cache and v_cache must be contiguous");
+    if (table.dim() != 2) value_error("table must be [sequences][table_cols]");
+    check(table, "table", at::kInt, table.sizes());
+    if (heads > INT32_MAX || dim > INT32_MAX || page > INT32_MAX) value_error("cache too large");
+    q4g128_kv_cache c;
+    c.k = static_cast<uint16_t*>(k.data_ptr());
+    c.v = static_cast<uint16_t*>(v.data_ptr());
+    c.table = static_cast<const int32_t*>(table.data_ptr());
+    c.pages = pages;
+    c.k_stride = pages > 1 ? k.stride(0) : heads * page * (dim + Q4G128_LATENT_ROT);
+    c.v_stride = pages > 1 ? v.stride(0) : heads * page * dim;
+    c.sequences = table.size(0);
+    c.table_cols = table.size(1);
+    c.kv_heads = (int32_t)heads;
+    c.dim = (int32_t)dim;
+    c.page = (int32_t)page;
+    return c;
+}
+
+// latent_expand(cache, table, lengths, packed, scales, mins, k_cache, v_cache,
+//               expanded_table, firsts, max_length); no result
+PyObject* latent_expand(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 11);
+    const at::Tensor &rows = tensor(a[0], "cache"), &table = tensor(a[1], "table"), &lengths = tensor(a[2], "lengths");
+    const q4g128_latent_cache c = latent_of(rows, table);
+    const at::Tensor &k = tensor(a[6], "k_cache"), &v = tensor(a[7], "v_cache"), &to = tensor(a[8], "expanded_table");
+    const q4g128_kv_cache e = expanded_of(k, v, to);
+    const SameDevice dev(rows);
+    if (lengths.dim() != 1) value_error("lengths must be [sequences]");
+    const int64_t count = lengths.size(0), wide = (int64_t)e.kv_heads * 2 * e.dim;
+    check(lengths, "lengths", at::kInt, {count});
+    dev.add(table), dev.add(lengths), dev.add(k), dev.add(v), dev.add(to);
+    if (count > c.sequences || count > e.sequences) value_error("a table has fewer than %lld sequences", (long long)count);
+    const uint8_t* packed = optional<uint8_t>(a[3], "packed", at::kByte, {wide, c.latent / 2}, dev);
+    const uint16_t* scales = optional<uint16_t>(a[4], "scales", at::kHalf, {wide, c.latent / Q4G128_GROUP}, dev);
+    const uint16_t* mins = optional<uint16_t>(a[5], "mins", at::kHalf, {wide, c.latent / Q4G128_GROUP}, dev);
+    const int32_t* firsts = optional<int32_t>(a[9], "firsts", at::kInt, {count}, dev);
+    const int64_t held = std::min((int64_t)c.table_cols * c.page, (int64_t)e.table_cols * e.page);
+    const int64_t max_length = a[10] == Py_None ? held : integer(a[10]);
+    const c10::DeviceGuard guard(dev.device);
+    return PyLong_FromLong(q4g128_latent_expand(&c, static_cast<const int32_t*>(lengths.data_ptr()), firsts, max_length, count,
+                                                packed, scales, mins, &e, current_stream(dev.device)));
+    END_HANDLE_TH_ERRORS
+}
+
+// latent_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale,
+//                max_length, out, workspace)
+PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    expect(n, 10);
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_cache"), &v = tensor(a[2], "v_cache"),
+                     &table = tensor(a[3], "table"), &starts = tensor(a[4], "q_starts"), &lengths = tensor(a[5], "lengths");
+    const q4g128_kv_cache c = expanded_of(k, v, table);
+    const SameDevice dev(k);
+    if (q.dim() != 3) value_error("q must be [T][heads][value + 64]");
+    const int64_t tokens = q.size(0);
+    check(q, "q", at::kHalf, {tokens, c.kv_heads, c.dim + Q4G128_LATENT_ROT});
+    if (lengths.dim() != 1) value_error("lengths must be [sequences]");
+    const int64_t count = lengths.size(0);
+    check(lengths, "lengths", at::kInt, {count});
+    check(starts, "q_starts", at::kInt, {count + 1});
+    dev.add(q), dev.add(v), dev.add(table), dev.add(starts), dev.add(lengths);
+    if (count > c.sequences)
+        value_error("table has %lld sequences, fewer than %lld", (long long)c.sequences, (long long)count);
+    const float scale = real(a[6]);
+    const int64_t max_length = a[7] == Py_None ? (int64_t)c.table_cols * c.page : integer(a[7]);
+    const int64_t need = q4g128_latent_prefill_workspace(tokens, count, c.kv_heads, c.dim, max_length);
+    if (need < 0) return PyLong_FromLongLong(need);
+    const c10::DeviceGuard guard(dev.device);
+    const hipStream_t stream = current_stream(dev.device);
+    const at::Tensor out = output(a[8], "out", {tokens, c.kv_heads, c.dim}, dev);
+    const at::Tensor ws = workspace_of(a[9], need, dev, stream);
+    return answer(q4g128_latent_prefill(static_cast<const uint16_t*>(q.data_ptr()), &c,
+                                        static_cast<const int32_t*>(starts.data_ptr()),
+                                        static_cast<const int32_t*>(lengths.data_ptr()), max_length, tokens, count, scale,
+                                        static_cast<uint16_t*>(out.data_ptr()), ws.defined() ? ws.data_ptr() : nullptr,
+                                        ws.defined() ? ws.numel() : 0, stream),
+                  out);
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"rope_append", (PyCFunction)(void (*)(void))rope_append, METH_FASTCALL, nullptr},
     {"attn_decode", (PyCFunction)(void (*)(void))attn_decode, METH_FASTCALL, nullptr},
@@ -554,6 +649,8 @@ PyMethodDef methods[] = {
     {"latent_append", (PyCFunction)(void (*)(void))latent_append, METH_FASTCALL, nullptr},
     {"latent_keep", (PyCFunction)(void (*)(void))latent_keep, METH_FASTCALL, nullptr},
     {"latent_attn", (PyCFunction)(void (*)(void))latent_attn, METH_FASTCALL, nullptr},
+    {"latent_expand", (PyCFunction)(void (*)(void))latent_expand, METH_FASTCALL, nullptr},
+    {"latent_prefill", (PyCFunction)(void (*)(void))latent_prefill, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -36,8 +36,25 @@ struct LatentAppendArgs {
     uint16_t* q;
 };
 
+// Latent rows to keys and values; `to` has value + 64 columns of K (dim) and value
+// of V (dim_v) per head (kv_heads).
+struct ExpandArgs {
+    KvCache c;
+    const int* lengths;
+    const int* firsts;       // or NULL: all positions
+    int max_length;
+    int count;               // sequences
+    const uint8_t* packed;   // [heads * 2 value][latent / 2]
+    const uint16_t* scales;
+    const uint16_t* mins;
+    KvCache to;
+};
+
+inline bool value_supported(int value) { return value == 64 || value == 128; }
+
 hipError_t launch_latent_append(const LatentAppendArgs& a, hipStream_t st);
 hipError_t launch_latent_attn(const NewArgs& x, const DeviceInfo& dev, hipStream_t st);
+hipError_t launch_latent_expand(const ExpandArgs& a, const DeviceInfo& dev, hipStream_t st);
 int64_t latent_attn_workspace(int heads, int latent, long max_new);
 
 }  // namespace q4
