@@ -22,6 +22,8 @@ struct NewArgs {
     const uint64_t* masks;  // [rows], or NULL
     int max_new;            // most new tokens of a sequence
     int target;             // parts wanted per kv head and row block
+    int second;             // parts are joined by a second launch
+    int pairs;              // kv heads times row blocks of a sequence
 };
 
 struct NewSeq {
@@ -191,6 +193,50 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
     return r;
 }
 
+// A sequence's parts, for the second launch.
+struct NewParts {
+    NewSeq q;
+    int parts, slot;
+};
+__device__ __forceinline__ NewParts new_parts(const NewArgs& x, int s, int least) {
+    const AttnArgs& a = x.a;
+    const int lane = threadIdx.x & 63;
+    const auto seq_of = [&](int i) {
+        NewSeq q = {-1, 0, 0, 0, 0};
+        if (i < a.count) q = new_seq(x, i, a.q_starts[i], a.q_starts[i + 1], a.lengths[i]);
+        return q;
+    };
+    int64_t total = 0;
+    for (int s0 = 0; s0 < a.count; s0 += 64) {
+        int t0;
+        total += lane_scan(new_tiles(x, seq_of(s0 + lane), t0)).last;
+    }
+    const int chunk = new_chunk(total, x.target, least);
+    NewParts r;
+    r.slot = 0;
+    for (int s0 = 0;; s0 += 64) {
+        const NewSeq q = seq_of(s0 + lane);
+        int t0;
+        const int tiles = new_tiles(x, q, t0);
+        const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
+        const LaneScan several = lane_scan(n > 1 ? n : 0);
+        if (s >= s0 + 64) {
+            r.slot += several.last;
+            continue;
+        }
+        const int l = s - s0;
+        const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+        r.parts = of(n);
+        r.slot += of(several.upto - (n > 1 ? n : 0));
+        r.q.s = s;
+        r.q.row = of(q.row);
+        r.q.n = of(q.n);
+        r.q.len = of(q.len);
+        r.q.base = of(q.base);
+        return r;
+    }
+}
+
 // Partial results: counters of finished parts, outputs [slots][pairs][R][dim], their
 // maxima and sums [slots][pairs][R][2], R rows of a workgroup.  There are fewer
 // than 2 target slots, and target * pairs is at most kPartSlots: where that leaves a
@@ -248,5 +294,105 @@ __device__ __forceinline__ void join_new_parts(const NewPart& it, const NewWorks
     for (int r = wave; r < nrows; r += waves)
         store(r, join_parts<D, true>(ws.o + (row_at + r) * D, ws.ml + (row_at + r) * 2, stride, parts));
 }
+
+// Join by a second launch: a workgroup for RW rows of one sequence, of `rows_of(q)`
+// rows in all.  Weights first, a thread for each row and part, then four columns of a
+// row for each thread, all of its parts' requested together; where that leaves
+// threads, several take parts of one four.
+//   at(slot, row): place of the row in part `slot`; stride: from part to part, rows
+//   out(q, row): the output row
+constexpr int kJoinThreads = 256;
+// PARTS: most parts of a sequence, the launch's target and one.
+template <int D, int RW, int PARTS>
+struct JoinShared {
+    static constexpr int ITEMS = RW * (D / 4);
+    static constexpr int GROUPS = ITEMS >= kJoinThreads ? 1 : kJoinThreads / ITEMS;
+    float2 ml[RW][PARTS];  // maxima and sums; then weights
+    float sum[RW];
+    f4 part[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? ITEMS : 1];
+};
+template <int D, int RW, int PARTS, class At, class Out>
+__device__ __forceinline__ void join_rows(JoinShared<D, RW, PARTS>& sh, const NewWorkspace& ws, const NewParts& p, int row0, int rows,
+                                          long stride, At at, Out out) {
+    using Shared = JoinShared<D, RW, PARTS>;
+    constexpr int ITEMS = Shared::ITEMS, GROUPS = Shared::GROUPS, PER = (ITEMS + kJoinThreads - 1) / kJoinThreads;
+    const int tid = threadIdx.x, parts = p.parts;
+    const int n = min(RW, rows - row0);
+    for (int i = tid; i < n * parts; i += kJoinThreads) {
+        const int r = i / parts, k = i % parts;
+        sh.ml[r][k] = *reinterpret_cast<const float2*>(ws.ml + (at(p.slot, row0 + r) + k * stride) * 2);
+    }
+    __syncthreads();
+    for (int r = tid >> 6; r < n; r += kJoinThreads / 64) {
+        const int lane = tid & 63;
+        float top = Q4_NEG_INF, sum = 0.0f;
+        for (int k = lane; k < parts; k += 64) top = fmaxf(top, sh.ml[r][k].x);
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        for (int k = lane; k < parts; k += 64) {
+            const float2 v = sh.ml[r][k];
+            const float w = part_weight(v.x, top);
+            sum += v.y * w;
+            sh.ml[r][k].x = w;
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        if (lane == 0) sh.sum[r] = sum;
+    }
+    __syncthreads();
+    const int group = GROUPS > 1 ? tid / ITEMS : 0, first = GROUPS > 1 ? tid % ITEMS : tid;
+    f4 acc[PER];
+    const float* from[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int item = first + j * kJoinThreads, r = min(item / (D / 4), n - 1);
+        acc[j] = (f4){0, 0, 0, 0};
+        from[j] = ws.o + at(p.slot, row0 + r) * D + item % (D / 4) * 4;
+    }
+    constexpr int UNROLL = PER >= 4 ? 2 : 8;
+    if (group < GROUPS) {
+        for (int k0 = group; k0 < parts; k0 += GROUPS * UNROLL) {
+            f4 v[UNROLL][PER];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int k = k0 + u * GROUPS;
+                    v[u][j] = (f4){0, 0, 0, 0};
+                    if (k < parts) v[u][j] = *reinterpret_cast<const f4*>(from[j] + k * stride * D);
+                }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int k = k0 + u * GROUPS, r = min((first + j * kJoinThreads) / (D / 4), n - 1);
+                    if (k < parts) acc[j] += v[u][j] * sh.ml[r][k].x;
+                }
+        }
+    }
+    if constexpr (GROUPS > 1) {
+        if (group < GROUPS) sh.part[group][first] = acc[0];
+        __syncthreads();
+        if (group != 0) return;
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g) acc[0] += sh.part[g][first];
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int item = first + j * kJoinThreads, r = item / (D / 4);
+        if (r >= n) continue;
+        const float sum = sh.sum[r], inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+        uint2 w;
+        w.x = as_u32((h2){(_Float16)(acc[j][0] * inv), (_Float16)(acc[j][1] * inv)});
+        w.y = as_u32((h2){(_Float16)(acc[j][2] * inv), (_Float16)(acc[j][3] * inv)});
+        *reinterpret_cast<uint2*>(out(p.q, row0 + r) + item % (D / 4) * 4) = w;
+    }
+}
+
+// Rows of a workgroup of the second launch: as many as leave two workgroups per CU.
+inline int join_rows_per_group(long rows) { return rows >= 16 * 512 ? 16 : rows >= 4 * 512 ? 4 : 1; }
+
+// Whether there may be parts to join at all.
+inline bool new_second(const NewArgs& x, long tiles) { return x.target > 1 && tiles > 1; }
 
 }  // namespace q4

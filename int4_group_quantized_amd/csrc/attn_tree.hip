@@ -436,6 +436,7 @@ int64_t attn_tree_workspace(int heads, int kv_heads, int dim, int max_new) {
 template <int D, int RB>
 static hipError_t launch_tree_rows(NewArgs x, int pairs, hipStream_t st) {
     x.target = tree_target(pairs, D, RB);
+    x.second = 0;
     const int least = D <= 128 ? 2 : 1;
     const long tiles = ((long)x.a.max_length + kTileKeys - 1) / kTileKeys, most = (tiles + least - 1) / least * x.a.count;
     const long grid = (long)x.target + x.a.count < most ? (long)x.target + x.a.count : most;
