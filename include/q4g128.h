@@ -392,8 +392,10 @@ Q4_API q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* c
  *   q4g128_attn_prefill.  No token sees the 65th or a later drafted token of a mask.
  *   max_new: an upper bound on a sequence's drafted tokens, 1 to Q4G128_MAX_DRAFT;
  *   it sizes the launch, and rows of later tokens are left as they were.
- *   options->prefix must be NULL.  max_length, workspace as in q4g128_attn_decode,
- *   of q4g128_attn_tree_workspace() bytes.
+ *   options->prefix must be NULL.  max_length as in q4g128_attn_decode.  workspace:
+ *   q4g128_attn_tree_workspace() bytes, 16-byte aligned; its first
+ *   Q4G128_ATTN_COUNTER_BYTES are left alone, the rest may hold anything, so that the
+ *   calls of one stream can share one with q4g128_attn_decode.
  */
 Q4_API int64_t q4g128_attn_tree_workspace(int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_new);
 Q4_API q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache,

@@ -14,15 +14,12 @@
 namespace q4 {
 
 constexpr int kMaskTokens = 64;   // tokens that a mask can name
-constexpr int kPartSlots = 512;   // workgroups wanted per launch at most
-static_assert(2 * kPartSlots <= kAttnCounters, "a counter for each sequence of several parts, and for each group");
 
 struct NewArgs {
     AttnArgs a;             // rows: new tokens of all sequences
     const uint64_t* masks;  // [rows], or NULL
     int max_new;            // most new tokens of a sequence
     int target;             // parts wanted per kv head and row block
-    int second;             // parts are joined by a second launch
     int pairs;              // kv heads times row blocks of a sequence
 };
 
@@ -104,13 +101,8 @@ struct NewPart {
     int part;     // of the sequence
     int parts;    // parts of the sequence
     int slot;     // workspace slot of its first part, if it has several
-    int split;    // sequences of several parts before this one
-    int group;    // groups of kJoin parts before this sequence's
     int t_begin, t_end;
 };
-
-// Parts of a sequence beyond which groups of kJoin are joined first.
-constexpr int kNewGroups = 2 * kJoin;
 
 // Tiles of a part: the total over `target`, rounded up, so that there are at most
 // target + (sequences of several parts) parts of such sequences; at least `least`.
@@ -131,7 +123,7 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
     const int lane = threadIdx.x & 63;
     NewPart r;
     r.q.s = -1;
-    r.part = r.parts = r.slot = r.split = r.group = r.t_begin = r.t_end = 0;
+    r.part = r.parts = r.slot = r.t_begin = r.t_end = 0;
     if (a.count == 1) {
         const auto of = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
@@ -163,8 +155,6 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
         const int tiles = new_tiles(x, q, t0);
         const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
         const LaneScan s = lane_scan(n), several = lane_scan(n > 1 ? n : 0);
-        const int groups = n > kNewGroups ? (n + kJoin - 1) / kJoin : 0;
-        const LaneScan gs = lane_scan(groups);
         const uint64_t hit = __ballot(n > 0 && item < before + s.upto && item >= before + s.upto - n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
@@ -177,8 +167,6 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
             r.parts = of(n);
             r.part = item - (before + of(s.upto) - r.parts);
             r.slot += of(several.upto - (n > 1 ? n : 0));
-            r.split += bits_of(__ballot(n > 1 && lane < l));
-            r.group += of(gs.upto - groups);
             // Alike parts: the last one is no shorter than it has to be.
             const int per = (of(tiles) + r.parts - 1) / r.parts;
             r.t_begin = of(t0) + r.part * per;
@@ -186,8 +174,6 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
             return r;
         }
         r.slot += several.last;
-        r.split += bits_of(__ballot(n > 1));
-        r.group += gs.last;
         before += s.last;
     }
     return r;
@@ -237,21 +223,19 @@ __device__ __forceinline__ NewParts new_parts(const NewArgs& x, int s, int least
     }
 }
 
-// Partial results: counters of finished parts, outputs [slots][pairs][R][dim], their
-// maxima and sums [slots][pairs][R][2], R rows of a workgroup.  There are fewer
-// than 2 target slots, and target * pairs is at most kPartSlots: where that leaves a
+// Partial results: outputs [slots][pairs][R][dim], their maxima and sums
+// [slots][pairs][R][2], R rows of a workgroup, behind the counters of the decode call
+// (so that both can share a workspace).  There are fewer than 2 target slots; with a
 // target of one nothing is split.
 struct NewWorkspace {
     float* o;
     float* ml;
-    int* counters;
 };
 
 __host__ __device__ inline long new_slots(int target) { return target > 1 ? 2 * (long)target : 0; }
 
 __device__ __forceinline__ NewWorkspace new_workspace(const NewArgs& x, int pairs, int rows, int dim) {
     NewWorkspace w;
-    w.counters = reinterpret_cast<int*>(x.a.workspace);
     w.o = x.a.workspace + kAttnCounters;
     w.ml = w.o + new_slots(x.target) * pairs * rows * dim;
     return w;
@@ -261,41 +245,7 @@ inline int64_t new_workspace_bytes(int target, long pairs, int rows, int dim) {
     return (new_slots(target) * pairs * rows * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
 
-// The last workgroup of a sequence and row block to finish joins its parts, in
-// order, whichever it is, and gives row r to store(r, joined) from one wave.  The
-// counters are zero again afterwards.  Called by every thread of a workgroup after
-// its last share_store; `nrows` rows from the workgroup's own slot on.
-template <int D, class Store>
-__device__ __forceinline__ void join_new_parts(const NewPart& it, const NewWorkspace& ws, int pairs, int pair, int rows,
-                                               int nrows, Store store) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    const long row_at = ((long)it.slot * pairs + pair) * rows;  // of the first part
-    int parts = it.parts;
-    long stride = (long)pairs * rows;  // rows from part to part
-    if (parts > kNewGroups) {
-        // Many parts: groups of kJoin are joined first, each by its last workgroup,
-        // into the place of the group's first part.
-        const int first = it.part / kJoin * kJoin, members = min(kJoin, parts - first);
-        if (!parts_done(ws.counters + kPartSlots + (it.group + it.part / kJoin) * pairs + pair, members)) return;
-        for (int r = wave; r < nrows; r += waves) {
-            const long at = row_at + first * stride + r;
-            const JoinedRow<D> j = join_parts<D, true>(ws.o + at * D, ws.ml + at * 2, stride, members);
-#pragma unroll
-            for (int i = 0; i < JoinedRow<D>::PER; ++i) {
-                const int d = 2 * (lane + 64 * i);
-                if (d < D) share_store(ws.o + at * D + d, j.o[i].x, j.o[i].y);
-            }
-            if (lane == 0) share_store(ws.ml + at * 2, j.m, j.l);
-        }
-        parts = (parts + kJoin - 1) / kJoin;
-        stride *= kJoin;
-    }
-    if (!parts_done(ws.counters + it.split * pairs + pair, parts)) return;
-    for (int r = wave; r < nrows; r += waves)
-        store(r, join_parts<D, true>(ws.o + (row_at + r) * D, ws.ml + (row_at + r) * 2, stride, parts));
-}
-
-// Join by a second launch: a workgroup for RW rows of one sequence, of `rows_of(q)`
+// Join, by a second launch: a workgroup for RW rows of one sequence, of `rows_of(q)`
 // rows in all.  Weights first, a thread for each row and part, then four columns of a
 // row for each thread, all of its parts' requested together; where that leaves
 // threads, several take parts of one four.

@@ -86,9 +86,8 @@ struct JoinedRow {
 // together, lane p holding part p's statistics; part after part waited for each
 // time took 3.3 us for 8 parts.  AGENT: the parts come from workgroups of the
 // same launch.
-// WIDE: columns of an output row, of which the D from po on are joined.
 constexpr int kJoin = 16;
-template <int D, bool AGENT, int WIDE = D>
+template <int D, bool AGENT>
 __device__ __forceinline__ JoinedRow<D> join_parts(const float* po, const float* ml, long stride, int parts) {
     const int lane = threadIdx.x & 63;
     auto get = [](const float* p) { return AGENT ? share_load(p) : *reinterpret_cast<const float2*>(p); };
@@ -108,7 +107,7 @@ __device__ __forceinline__ JoinedRow<D> join_parts(const float* po, const float*
             for (int i = 0; i < PER; ++i) {
                 const int d = 2 * (lane + 64 * i);
                 v[p][i] = {0.0f, 0.0f};
-                if (p0 + p < parts && d < D) v[p][i] = get(po + (long)(p0 + p) * stride * WIDE + d);
+                if (p0 + p < parts && d < D) v[p][i] = get(po + (long)(p0 + p) * stride * D + d);
             }
         }
         float t = st.x;

@@ -22,15 +22,15 @@
 // hold drafted positions or a window's edge.
 //
 // The visible tiles of all sequences are cut into parts of one length, computed on
-// the device from the lengths; the last part of a sequence to finish joins them in
-// order.
+// the device from the lengths; a second launch joins them in order.
 #include "attn_new.hpp"
 
 namespace q4 {
 
 constexpr int kTreeWaves = 4;
 constexpr int kTreeThreads = 64 * kTreeWaves;
-constexpr int kTreeGridY = 32768;  // parts per layer of the grid
+constexpr int kTreeGridY = 32768;  // parts, or sequences, per layer of the grid
+constexpr int kTreeTarget = 512;   // most workgroups wanted per launch: two per CU
 
 // Workgroups per CU that registers and LDS leave room for.
 __host__ __device__ constexpr int tree_per_cu(int dim, int rb) { return dim <= 128 && rb == 1 ? 2 : 1; }
@@ -44,7 +44,7 @@ __host__ __device__ constexpr int tree_halves(int dim, int rb) { return dim * rb
 static int tree_row_blocks(int rows, int dim) { return rows <= 16 ? 1 : rows <= 32 || dim > 128 ? 2 : 4; }
 
 static int tree_target(long pairs, int dim, int rb) {
-    const long t = 256 * tree_per_cu(dim, rb) / pairs;
+    const long t = kTreeTarget / 2 * tree_per_cu(dim, rb) / pairs;
     return t > 0 ? (int)t : 1;
 }
 
@@ -410,15 +410,28 @@ __global__ void __launch_bounds__(kTreeThreads, tree_per_cu(D, RB)) attn_tree_ke
             w.y = as_u32((h2){(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)});
             *reinterpret_cast<uint2*>(a.out + out_row(r) * D + d) = w;
         } else {
-            float* wo = ws.o + (slot + r) * D + d;
-            share_store(wo, o[0], o[1]);
-            share_store(wo + 2, o[2], o[3]);
-            if (d == 0) share_store(ws.ml + (slot + r) * 2, top, sum);
+            *reinterpret_cast<f4*>(ws.o + (slot + r) * D + d) = o;
+            if (d == 0) *reinterpret_cast<float2*>(ws.ml + (slot + r) * 2) = {top, sum};
         }
     }
-    if (it.parts == 1) return;
-    join_new_parts<D>(it, ws, pairs, pair, R, nrows,
-                      [&](int r, const JoinedRow<D>& j) { store_joined(j, a.out + out_row(r) * D); });
+}
+
+// Row `row` of a sequence is token row / heads, head row % heads.
+template <int D, int RW>
+__global__ void __launch_bounds__(kJoinThreads) attn_tree_join_kernel(NewArgs x, int least, int rows) {
+    __shared__ JoinShared<D, RW, kTreeTarget + 1> sh;
+    const AttnArgs& a = x.a;
+    const NewParts p = new_parts(x, blockIdx.y + blockIdx.z * kTreeGridY, least);
+    const int row0 = blockIdx.x * RW, all = min(p.q.n, x.max_new) * a.heads;
+    if (p.parts < 2 || row0 >= all) return;
+    join_rows(
+        sh, new_workspace(x, x.pairs, rows, D), p, row0, all, (long)x.pairs * rows,
+        [&](int slot, int row) {
+            const int token = row / a.heads, head = row - token * a.heads, kvh = head / a.group;
+            const int r = token * a.group + head - kvh * a.group;  // of the kv head's
+            return ((long)slot * x.pairs + r / rows * a.c.kv_heads + kvh) * rows + r % rows;
+        },
+        [&](const NewSeq& q, int row) { return a.out + ((size_t)q.row * a.heads + row) * D; });
 }
 
 static int tree_blocks(int kv_heads, int group, int max_new, int dim, int* rb) {
@@ -436,7 +449,7 @@ int64_t attn_tree_workspace(int heads, int kv_heads, int dim, int max_new) {
 template <int D, int RB>
 static hipError_t launch_tree_rows(NewArgs x, int pairs, hipStream_t st) {
     x.target = tree_target(pairs, D, RB);
-    x.second = 0;
+    x.pairs = pairs;
     const int least = D <= 128 ? 2 : 1;
     const long tiles = ((long)x.a.max_length + kTileKeys - 1) / kTileKeys, most = (tiles + least - 1) / least * x.a.count;
     const long grid = (long)x.target + x.a.count < most ? (long)x.target + x.a.count : most;
@@ -446,6 +459,16 @@ static hipError_t launch_tree_rows(NewArgs x, int pairs, hipStream_t st) {
                   : options == kOptions ? &attn_tree_kernel<D, kOptions, RB>
                                         : &attn_tree_kernel<D, kLargeCapOptions, RB>;
     hipLaunchKernelGGL(kernel, blocks, dim3(kTreeThreads), 0, st, x, least);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !new_second(x, tiles)) return e;
+    const int rw = join_rows_per_group((long)x.a.rows * x.a.heads);
+    const dim3 groups((unsigned)(((long)x.max_new * x.a.heads + rw - 1) / rw),
+                      (unsigned)(x.a.count < kTreeGridY ? x.a.count : kTreeGridY),
+                      (unsigned)((x.a.count + kTreeGridY - 1) / kTreeGridY));
+    auto join = rw == 16  ? &attn_tree_join_kernel<D, 16>
+                : rw == 4 ? &attn_tree_join_kernel<D, 4>
+                          : &attn_tree_join_kernel<D, 1>;
+    hipLaunchKernelGGL(join, groups, dim3(kJoinThreads), 0, st, x, least, 16 * RB);
     return hipGetLastError();
 }
 

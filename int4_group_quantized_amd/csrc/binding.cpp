@@ -230,7 +230,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // one stream run one after the other), grown as needed, counters zeroed once.
 // A call in a graph capture gets memory of its own, since a graph may be
 // replayed on any stream.  Never destroyed: at exit the device may be gone.
-at::Tensor kept_workspace(int64_t need, const at::Device& d, hipStream_t stream) {
+// counted: whether the call uses the counters.
+at::Tensor kept_workspace(int64_t need, const at::Device& d, hipStream_t stream, bool counted) {
     static auto* kept = new std::map<std::pair<int, hipStream_t>, at::Tensor>;
     hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &status) != hipSuccess) {
@@ -242,13 +243,14 @@ at::Tensor kept_workspace(int64_t need, const at::Device& d, hipStream_t stream)
     at::Tensor& t = capturing ? fresh : (*kept)[{d.index(), stream}];
     if (!t.defined() || t.numel() < need) {
         t = empty({need}, at::kByte, d);
+        if (capturing && !counted) return t;
         t.narrow(0, 0, Q4G128_ATTN_COUNTER_BYTES).zero_();
     }
     return t;
 }
 
-at::Tensor workspace_of(PyObject* o, int64_t need, const SameDevice& dev, hipStream_t stream) {
-    if (o == Py_None) return need > 0 ? kept_workspace(need, dev.device, stream) : at::Tensor();
+at::Tensor workspace_of(PyObject* o, int64_t need, const SameDevice& dev, hipStream_t stream, bool counted = false) {
+    if (o == Py_None) return need > 0 ? kept_workspace(need, dev.device, stream, counted) : at::Tensor();
     const at::Tensor& t = tensor(o, "workspace");
     on_gpu(t, "workspace");
     dev.add(t);
@@ -304,7 +306,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::DeviceGuard guard(t.dev.device);
     const hipStream_t stream = current_stream(t.dev.device);
     const at::Tensor out = output(a[10], "out", t.q.sizes(), t.dev);
-    const at::Tensor ws = workspace_of(a[11], need, t.dev, stream);
+    const at::Tensor ws = workspace_of(a[11], need, t.dev, stream, true);
     return answer(q4g128_attn_decode(t.qp(), &t.c, t.lp(), t.max_length, t.rows, t.heads, &t.o,
                                      static_cast<uint16_t*>(out.data_ptr()), ws.data_ptr(), ws.numel(), stream),
                   out);

@@ -740,7 +740,6 @@ static hipError_t launch_latent_rows(NewArgs x, const DeviceInfo& dev, hipStream
     x.target = latent_target(pairs);
     const long tiles = ((long)x.a.max_length + kTileKeys - 1) / kTileKeys;
     const long grid = (long)x.target + x.a.count < tiles * x.a.count ? (long)x.target + x.a.count : tiles * x.a.count;
-    x.second = new_second(x, tiles);
     std::atomic<int>& ready = PerDevice<Kernel>::value[dev.device];
     if (!ready.load(std::memory_order_acquire)) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -755,7 +754,7 @@ static hipError_t launch_latent_rows(NewArgs x, const DeviceInfo& dev, hipStream
                       (unsigned)((pairs + kLatentGridY - 1) / kLatentGridY));
     hipLaunchKernelGGL(Kernel, blocks, dim3(kLatentThreads), bytes, st, x);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !x.second) return e;
+    if (e != hipSuccess || !new_second(x, tiles)) return e;
     const int rw = join_rows_per_group((long)x.a.rows * x.a.heads);
     const dim3 groups((unsigned)((rows + rw - 1) / rw), (unsigned)(x.a.count < kLatentGridY ? x.a.count : kLatentGridY),
                       (unsigned)((x.a.count + kLatentGridY - 1) / kLatentGridY));

@@ -15,6 +15,8 @@
 #include "latent.hpp"
 #include "lds_loads.hpp"
 
+#include <type_traits>
+
 namespace q4 {
 
 typedef float f16r __attribute__((ext_vector_type(16)));
@@ -82,21 +84,29 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(Expand
         }
     };
 
-    // Weights: rows of the head's 2 V, 32 a block.
+    // Weights: rows of the head's 2 V, 32 a block.  A lane reads 32 codes at a time, the
+    // upper half of the wave those behind the lower half's; of every two dwords (a
+    // step's codes) they then swap the one that belongs to the other.
     h8 w[NB][STEPS];
     {
         const DequantConsts kc = make_dequant_consts();
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const size_t row = (size_t)head * (2 * V) + (wave * NB + b) * 32 + n;
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.packed + row * (L / 2)) + h;
+            const u4* q = reinterpret_cast<const u4*>(a.packed + row * (L / 2)) + h;
             const _Float16* sp = reinterpret_cast<const _Float16*>(a.scales) + row * (L / 128);
             const _Float16* mp = reinterpret_cast<const _Float16*>(a.mins) + row * (L / 128);
 #pragma unroll
-            for (int g = 0; g < L / 128; ++g) {
-                const h2 s = {sp[g], sp[g]}, m = {mp[g], mp[g]};
+            for (int c = 0; c < L / 64; ++c) {
+                const u4 v = q[2 * c];
+                const h2 s = {sp[c / 2], sp[c / 2]}, m = {mp[c / 2], mp[c / 2]};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[b][8 * g + i] = weights_of(q[2 * (8 * g + i)], s, m, kc);
+                for (int i = 0; i < 2; ++i) {
+                    // Lower half: dwords 2i, 2i + 1 of the first 32 codes; upper: of the second.
+                    const auto r = __builtin_amdgcn_permlane32_swap(v[2 * i], v[2 * i + 1], false, false);
+                    w[b][4 * c + i] = weights_of(r[0], s, m, kc);
+                    w[b][4 * c + 2 + i] = weights_of(r[1], s, m, kc);
+                }
             }
         }
     }
@@ -104,71 +114,59 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(Expand
     const uint32_t lds_at =
         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u4*)lds + 32 * D * wave);
     constexpr uint32_t IMAGE = 2 * kTileKeys * D;
+    // The tile requested: where it lies, and where its keys and values go.  Lane i
+    // holds the pages of the tile's quarter i % 4.
     const uint16_t* source = a.c.k;
-    int gone_next = 0;  // bit i: quarter i has no latent page
+    int page_to = -1;
+    // Table entries [first, first + 64) of either cache, one per lane: an entry read for
+    // its tile alone would hold up every tile.
+    int ids = -1, ids_first = 0, to_ids = -1, to_first = 0;
+    const auto refill = [&](const KvCache& c, int entry, int& first) {
+        first = entry;
+        const int e = entry + lane, id = e < c.cols ? c.table[(size_t)next_s * c.cols + e] : -1;
+        return (unsigned)id < (unsigned)c.pages ? id : -1;
+    };
     auto aim = [&](int64_t item) {
-        find(item);
-        const int* row = a.c.table + (size_t)next_s * a.c.cols;
-        const int last = next_to - 1, kb = next_tile * kTileKeys;
-        const int page = page_of(a.c, row, min(kb + 16 * (lane & 3), last));
-        gone_next = (int)(__ballot(page < 0) & 15);
-        const int mine = max(__builtin_amdgcn_readlane(page, wave), 0);
-        source = uniform(a.c.k + (size_t)mine * a.c.k_stride + (size_t)((kb + 16 * wave) & pmask) * D);
+        const bool same = item > begin && (next_tile + 1) * kTileKeys < next_to;
+        if (same) ++next_tile;
+        else find(item);
+        const int kb = next_tile * kTileKeys;
+        if (!same || ((kb + 63) >> a.c.shift) >= ids_first + 64) ids = refill(a.c, kb >> a.c.shift, ids_first);
+        if (!same || ((kb + 63) >> a.to.shift) >= to_first + 64) to_ids = refill(a.to, kb >> a.to.shift, to_first);
+        page_to = -1;
+        int mine = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = kb + 16 * i;
+            const int page = __builtin_amdgcn_readlane(ids, (at >> a.c.shift) - ids_first);
+            const int to = __builtin_amdgcn_readlane(to_ids, (at >> a.to.shift) - to_first);
+            if (i == wave) mine = page;
+            if ((lane & 3) == i && page >= 0) page_to = to;
+        }
+        source = uniform(a.c.k + (size_t)max(mine, 0) * a.c.k_stride + (size_t)((kb + 16 * wave) & pmask) * D);
     };
-    auto load_piece = [&](int slot, int j) {
-        const int place = 64 * j + lane;
-        load_lds(source, 16 * (place ^ expand_swizzle(place / C)), lds_at + slot * IMAGE + 1024 * j);
-    };
+    uint32_t at[LOADS];
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) at[j] = 16 * ((64 * j + lane) ^ expand_swizzle((64 * j + lane) / C));
+    auto load_piece = [&](int slot, int j) { load_lds(source, at[j], lds_at + slot * IMAGE + 1024 * j); };
 
     const bool keys = wave < 2;
     const int d0 = (wave & 1) * (32 * NB);  // first of the wave's dims
-    aim(begin);
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) load_piece(0, j);
-    int slot = 0;
-    for (int64_t item = begin; item < end; ++item, slot ^= 1) {
-        const int seq = next_s, kb = next_tile * kTileKeys, from = next_from, upto = next_to, gone = gone_next;
-        wait_for_loads<0>();
-        lds_meet();  // all waves' loads are there, and the other image has been read
-        const bool more = item + 1 < end;
-        // Where this tile's keys and values go: pages by quarter.
-        int to_page;
-        {
-            const int* row = a.to.table + (size_t)seq * a.to.cols;
-            const int at = kb + 16 * (lane & 3);
-            const bool in = (at >> a.to.shift) < a.to.cols;
-            to_page = in ? page_of(a.to, row, at) : -1;
-            if (gone >> (lane & 3) & 1) to_page = -1;
-        }
-        const auto page_to = [&](int quarter) { return __shfl(to_page, quarter, 64); };
-        if (more) aim(item + 1);
-        const uint8_t* image = reinterpret_cast<const uint8_t*>(lds) + slot * IMAGE;
-        f16r acc[2][NB];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc[p][b] = (f16r)0.0f;
-        const auto row_of = [&](int p, int s) {
-            const int row = 32 * p + n;
-            return *reinterpret_cast<const h8*>(image + row * (2 * D) + 16 * ((2 * s + h) ^ expand_swizzle(row)));
-        };
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const h8 c[2] = {row_of(0, s), row_of(1, s)};
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    acc[p][b] = keys ? __builtin_amdgcn_mfma_f32_32x32x16_f16(w[b][s], c[p], acc[p][b], 0, 0, 0)
-                                     : __builtin_amdgcn_mfma_f32_32x32x16_f16(c[p], w[b][s], acc[p][b], 0, 0, 0);
-            if (more && s < LOADS) load_piece(slot ^ 1, s);
-        }
-        const int tp = (1 << a.to.shift) - 1;
+    const int tp = (1 << a.to.shift) - 1;
+    constexpr int ROT_CHUNKS = kTileKeys * (kRot / 8) / kExpandThreads;
+    // A tile's results, kept until the next one's loads have been waited for, so that
+    // the stores have a whole tile's time before anything waits for them.
+    f16r acc[2][NB];
+    u4 rot[ROT_CHUNKS];
+    struct Done {
+        int kb, from, to, page;
+    } done = {0, 0, 0, -1};
+    auto store = [&] {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             if (keys) {
-                const int pos = kb + 32 * p + n, page = page_to(2 * p + (n >> 4));
-                if (page >= 0 && pos >= from && pos < upto) {
+                const int pos = done.kb + 32 * p + n, page = __shfl(done.page, 2 * p + (n >> 4), 64);
+                if (page >= 0 && pos >= done.from && pos < done.to) {
                     uint16_t* to = a.to.k + (size_t)page * a.to.k_stride + (((size_t)head << a.to.shift) + (pos & tp)) * K + d0;
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
@@ -183,8 +181,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(Expand
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int pos = kb + 32 * p + 8 * i + 4 * h, page = __builtin_amdgcn_readlane(to_page, 2 * p + (i >> 1));
-                    if (page < 0 || pos + 3 < from || pos >= upto) continue;
+                    const int pos = done.kb + 32 * p + 8 * i + 4 * h, page = __builtin_amdgcn_readlane(done.page, 2 * p + (i >> 1));
+                    if (page < 0 || pos + 3 < done.from || pos >= done.to) continue;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         uint16_t* to = a.to.v + (size_t)page * a.to.v_stride +
@@ -192,12 +190,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(Expand
                         uint16_t v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(uint16_t, (_Float16)acc[p][b][4 * i + e]);
-                        if (pos >= from && pos + 3 < upto) {
+                        if (pos >= done.from && pos + 3 < done.to) {
                             *reinterpret_cast<uint2*>(to) = {(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (pos + e >= from && pos + e < upto) to[e] = v[e];
+                                if (pos + e >= done.from && pos + e < done.to) to[e] = v[e];
                         }
                     }
                 }
@@ -205,15 +203,71 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(Expand
         }
         // The rotary part of the keys.
 #pragma unroll
-        for (int i = tid; i < kTileKeys * (kRot / 8); i += kExpandThreads) {
-            const int row = i >> 3, c = i & 7, pos = kb + row, page = page_to(row >> 4);
-            if (page >= 0 && pos >= from && pos < upto) {
-                const u4 v = *reinterpret_cast<const u4*>(image + row * (2 * D) + 16 * ((L / 8 + c) ^ expand_swizzle(row)));
+        for (int i = 0; i < ROT_CHUNKS; ++i) {
+            const int row = (tid + i * kExpandThreads) >> 3, c = tid & 7, pos = done.kb + row, page = __shfl(done.page, row >> 4, 64);
+            if (page >= 0 && pos >= done.from && pos < done.to)
                 *reinterpret_cast<u4*>(a.to.k + (size_t)page * a.to.k_stride +
-                                       (((size_t)head << a.to.shift) + (pos & tp)) * K + V + 8 * c) = v;
+                                       (((size_t)head << a.to.shift) + (pos & tp)) * K + V + 8 * c) = rot[i];
+        }
+    };
+    aim(begin);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) load_piece(0, j);
+    int slot = 0;
+    for (int64_t item = begin; item < end; ++item, slot ^= 1) {
+        wait_for_loads<0>();
+        lds_meet();  // all waves' loads are there, and the other image has been read
+        const int kb = next_tile * kTileKeys, from = next_from, upto = next_to, page = page_to;
+        const bool more = item + 1 < end;
+        if (more) aim(item + 1);
+        if (item > begin) store();
+        done = {kb, from, upto, page};
+        const uint8_t* image = reinterpret_cast<const uint8_t*>(lds) + slot * IMAGE;
+#pragma unroll
+        for (int i = 0; i < ROT_CHUNKS; ++i) {
+            const int row = (tid + i * kExpandThreads) >> 3, c = tid & 7;
+            rot[i] = *reinterpret_cast<const u4*>(image + row * (2 * D) + 16 * ((L / 8 + c) ^ expand_swizzle(row)));
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[p][b] = (f16r)0.0f;
+        constexpr int AHEAD = 3;  // operands read ahead of the products
+        h8 c[AHEAD][2];
+        const auto row_of = [&](int p, int s) {
+            const int row = 32 * p + n;
+            return *reinterpret_cast<const h8*>(image + row * (2 * D) + 16 * ((2 * s + h) ^ expand_swizzle(row)));
+        };
+        const auto products = [&](auto load, auto of_keys) {
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) c[s][p] = row_of(p, s);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        acc[p][b] = decltype(of_keys)::value
+                                        ? __builtin_amdgcn_mfma_f32_32x32x16_f16(w[b][s], c[s % AHEAD][p], acc[p][b], 0, 0, 0)
+                                        : __builtin_amdgcn_mfma_f32_32x32x16_f16(c[s % AHEAD][p], w[b][s], acc[p][b], 0, 0, 0);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    if (s + AHEAD < STEPS) c[s % AHEAD][p] = row_of(p, s + AHEAD);
+                if (decltype(load)::value && s < LOADS) load_piece(slot ^ 1, s);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        if (more) {
+            if (keys) products(std::true_type{}, std::true_type{});
+            else products(std::true_type{}, std::false_type{});
+        } else {
+            if (keys) products(std::false_type{}, std::true_type{});
+            else products(std::false_type{}, std::false_type{});
         }
     }
+    store();
 }
 
 template <int L, int V>
