@@ -397,7 +397,8 @@ Q4_API q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* c
  *   Q4G128_ATTN_COUNTER_BYTES are left alone, the rest may hold anything, so that the
  *   calls of one stream can share one with q4g128_attn_decode.
  */
-Q4_API int64_t q4g128_attn_tree_workspace(int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_new);
+Q4_API int64_t q4g128_attn_tree_workspace(int64_t tokens, int64_t count, int32_t heads,
+                             int32_t kv_heads, int32_t dim, int64_t max_new, int64_t max_length);
 Q4_API q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache,
                              const int32_t* q_starts, const int32_t* lengths,
                              const uint64_t* masks, int64_t max_new, int64_t max_length,

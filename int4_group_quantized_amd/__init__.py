@@ -123,7 +123,7 @@ def _load():
     lib.q4g128_rope_append_slots.argtypes = [vp, i64, i64, i32, cache, vp, vp, vp, vp, i32, i32, f32, vp, vp, f32, vp,
                                              vp]
     lib.q4g128_cache_keep.argtypes = [cache, vp, vp, vp, i64, i64, vp]
-    lib.q4g128_attn_tree_workspace.argtypes = [i32, i32, i32, i64]
+    lib.q4g128_attn_tree_workspace.argtypes = [i64, i64, i32, i32, i32, i64, i64]
     lib.q4g128_attn_tree.argtypes = [vp, cache, vp, vp, vp, i64, i64, i64, i64, i32, options, vp, vp, i64, vp]
     latent = ctypes.POINTER(LatentCache)
     lib.q4g128_latent_append.argtypes = [vp, i64, i64, latent, vp, vp, vp, vp, i32, f32, vp, f32, vp, i64, i64, i32, vp,
@@ -450,9 +450,9 @@ def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=Non
                                          prefix, max_length, out, workspace), "q4g128_attn_prefill")
 
 
-def q4g128_attn_tree_workspace(heads, kv_heads, dim, max_new) -> int:
+def q4g128_attn_tree_workspace(tokens, count, heads, kv_heads, dim, max_new, max_length) -> int:
     """Bytes of workspace that q4g128_attn_tree needs."""
-    return _lib.q4g128_attn_tree_workspace(heads, kv_heads, dim, max_new)
+    return _lib.q4g128_attn_tree_workspace(tokens, count, heads, kv_heads, dim, max_new, max_length)
 
 
 def q4g128_attn_tree(q, k_cache, v_cache, table, q_starts, lengths, masks=None, scale=None, softcap=0.0, window=0,

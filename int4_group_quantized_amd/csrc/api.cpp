@@ -239,6 +239,8 @@ q4_status check_attention(const uint16_t* q, const q4g128_kv_cache* cache, const
     a->out = out;
     a->workspace = (float*)workspace;
     a->q_starts = nullptr;
+    a->masks = nullptr;
+    a->max_new = (int)rows;
     a->count = (int)sequences;
     return Q4_OK;
 }
@@ -565,12 +567,13 @@ q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* cache, c
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 
-int64_t q4g128_attn_tree_workspace(int32_t heads, int32_t kv_heads, int32_t dim, int64_t max_new) {
-    if (heads < 1 || kv_heads < 1 || max_new < 1) return Q4_EINVAL;
-    if (heads > Q4G128_MAX_HEADS || heads % kv_heads != 0 || heads / kv_heads > Q4G128_MAX_GROUP ||
+int64_t q4g128_attn_tree_workspace(int64_t tokens, int64_t count, int32_t heads, int32_t kv_heads, int32_t dim,
+                                   int64_t max_new, int64_t max_length) {
+    if (tokens < 1 || count < 1 || heads < 1 || kv_heads < 1 || max_new < 1 || max_length < 1) return Q4_EINVAL;
+    if (tokens > Q4G128_MAX_TOKENS || count > Q4G128_MAX_SEQUENCES || max_length > Q4G128_MAX_N || heads > Q4G128_MAX_HEADS || heads % kv_heads != 0 || heads / kv_heads > Q4G128_MAX_GROUP ||
         !q4::attn_dim_supported(dim) || max_new > Q4G128_MAX_DRAFT)
         return Q4_ESHAPE;
-    return q4::attn_tree_workspace(heads, kv_heads, dim, (int)max_new);
+    return q4::attn_tree_workspace(tokens, count, heads, kv_heads, dim, (int)max_new, max_length);
 }
 
 q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* q_starts,
@@ -579,7 +582,9 @@ q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, cons
                            uint16_t* out, void* workspace, int64_t workspace_bytes, void* stream) {
     q4::NewArgs x;
     if (!q_starts) return Q4_EINVAL;
-    const int64_t need = cache ? q4g128_attn_tree_workspace(heads, cache->kv_heads, cache->dim, max_new) : Q4_EINVAL;
+    const int64_t need = cache ? q4g128_attn_tree_workspace(tokens, count, heads, cache->kv_heads, cache->dim, max_new,
+                                                            max_length)
+                               : Q4_EINVAL;
     if (need < 0) return (q4_status)need;
     if (options && options->prefix) return Q4_EINVAL;
     q4_status s = check_attention(q, cache, lengths, max_length, tokens, count, heads, options, out, workspace,
@@ -591,7 +596,10 @@ q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, cons
     x.a.q_starts = q_starts;
     x.masks = masks;
     x.max_new = (int)max_new;
-    hipError_t e = q4::launch_attn_tree(x, (hipStream_t)stream);
+    q4::DeviceInfo dev;
+    s = current_device(&dev);
+    if (s != Q4_OK) return s;
+    hipError_t e = q4::launch_attn_tree(x, dev, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

@@ -64,6 +64,8 @@ struct AttnArgs {
     // prompt only
     const int* q_starts;
     const int* prefix;     // or NULL
+    const uint64_t* masks; // of drafted tokens, or NULL
+    int max_new;           // most tokens of a sequence that are served
     int count;             // sequences
     int tile;              // tokens of a workgroup
     float inv_tile;        // 1 / tile
@@ -91,11 +93,14 @@ hipError_t launch_cache_keep(const KeepArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t st);
 int64_t attn_decode_workspace(int64_t batch, int heads, int dim);
 hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
+// Drafted tokens without options by the prompt kernel; its workspace.
+hipError_t launch_prefill_tree(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int dim_v,
                                int64_t max_length);
 struct NewArgs;  // attn_new.hpp
-hipError_t launch_attn_tree(const NewArgs& x, hipStream_t st);
-int64_t attn_tree_workspace(int heads, int kv_heads, int dim, int max_new);
+hipError_t launch_attn_tree(const NewArgs& x, const DeviceInfo& dev, hipStream_t st);
+int64_t attn_tree_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int max_new,
+                            int64_t max_length);
 
 // The table's page for a position of sequence `row`, or -1 when the page is
 // absent.  pos must lie below cols << shift.

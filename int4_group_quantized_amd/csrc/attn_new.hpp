@@ -18,7 +18,7 @@ constexpr int kMaskTokens = 64;   // tokens that a mask can name
 struct NewArgs {
     AttnArgs a;             // rows: new tokens of all sequences
     const uint64_t* masks;  // [rows], or NULL
-    int max_new;            // most new tokens of a sequence
+    int max_new;            // most new tokens of a sequence that are served
     int target;             // parts wanted per kv head and row block
     int pairs;              // kv heads times row blocks of a sequence
 };

@@ -45,7 +45,7 @@
 //
 // Few tokens on a long cache leave most CUs idle, so the visible tiles are
 // then cut into equal splits joined by a second launch (prefill_split).
-#include "attn_softmax.hpp"
+#include "attn_new.hpp"
 #include "lds_loads.hpp"
 
 #include <cmath>
@@ -56,8 +56,8 @@ namespace q4 {
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 // Waves that share 32 of a workgroup's rows, and threads of a workgroup.
-__host__ __device__ constexpr int prefill_share(int dim, int rows) { return dim > 128 || rows == 64 ? 2 : 1; }
-__host__ __device__ constexpr int prefill_threads(int dim, int rows) { return 2 * rows * prefill_share(dim, rows); }
+__host__ __device__ constexpr int prefill_share(int dim_v, int rows) { return dim_v > 128 || rows == 64 ? 2 : 1; }
+__host__ __device__ constexpr int prefill_threads(int dim_v, int rows) { return 2 * rows * prefill_share(dim_v, rows); }
 constexpr int kPrefillAlone = 256;      // workgroups that have a CU to themselves
 constexpr double kSecondLaunch = 4.0;   // us, launch and join of short partial results
 constexpr double kJoinRound = 1.0;      // us, each further kJoin of them
@@ -91,8 +91,8 @@ struct PrefillPlan {
 static PrefillPlan prefill_split(int rows, long blocks, long length, long tokens, int heads, int dim, int dim_v) {
     // Beyond dim 128 a CU's LDS holds one workgroup: 128 tokens of 16 heads of 256 on
     // 4,000 positions take 33 us in 256 workgroups, 44 in 512.
-    const long room = (dim > 128 ? 1 : 2) * kPrefillAlone / blocks, most = room < length ? room : length;
-    const double c = (0.6 + dim / 150.0) * (rows == 64 ? 0.85 : 1.0), v = 8e-6 / 4.0 * (double)tokens * heads * dim_v;
+    const long room = (dim_v > 128 ? 1 : 2) * kPrefillAlone / blocks, most = room < length ? room : length;
+    const double c = (0.6 + (dim + dim_v) / 300.0) * (rows == 64 ? 0.85 : 1.0), v = 8e-6 / 4.0 * (double)tokens * heads * dim_v;
     PrefillPlan plan = {rows, 1, c * (double)length};
     if (most < 2) return plan;
     long n = (long)(std::sqrt(c * (double)length / v) + 0.5);
@@ -140,6 +140,8 @@ struct PrefillTile {
     int pos;     // position of the first token (may be negative)
     int len;     // positions of the sequence
     int prefix;  // positions that all of its tokens see
+    int base;    // position of the sequence's first token
+    int total;   // tokens of the sequence
 };
 
 // x / a.tile rounded up, x < 2^21: the quotient of x - 1/2 keeps 1 / 256 from
@@ -156,9 +158,11 @@ __device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s,
     PrefillTile r;
     r.s = s;
     r.token = first + at;
-    r.n = min(a.tile, last - r.token);
+    r.n = min(a.tile, min(last - first, a.max_new) - at);
     r.len = min(max(len, 0), a.max_length);
-    r.pos = r.len - (last - first) + at;
+    r.total = last - first;
+    r.base = r.len - r.total;
+    r.pos = r.base + at;
     r.prefix = prefix;
     return r;
 }
@@ -170,13 +174,13 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
     const int lane = threadIdx.x & 63;
     PrefillTile none;
     none.s = -1;
-    none.token = none.n = none.pos = none.len = none.prefix = 0;
+    none.token = none.n = none.pos = none.len = none.prefix = none.base = none.total = 0;
     if (a.count == 1) {
         const auto of = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
         const int prefix = a.prefix ? of(a.prefix[0]) : 0;
         const int st = min(max(first, 0), a.rows), en = min(max(last, st), a.rows);
-        const int n = prefill_tiles_of(a, en - st);
+        const int n = prefill_tiles_of(a, min(en - st, a.max_new));
         return item < n ? prefill_tile_of(a, 0, st, en, len, prefix, n, item) : none;
     }
     int before = 0;
@@ -191,7 +195,7 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
         asm volatile("" : "+v"(st), "+v"(en), "+v"(len), "+v"(prefix));
         st = min(max(st, 0), a.rows);
         en = min(max(en, st), a.rows);
-        const int n = prefill_tiles_of(a, en - st);
+        const int n = prefill_tiles_of(a, min(en - st, a.max_new));
         const LaneScan c = lane_scan(n);
         const uint64_t hit = __ballot(n > 0 && item < before + c.upto && item >= before + c.upto - n);
         if (hit) {
@@ -230,12 +234,15 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
     return (((w & 0x7C007C00u) + 0x04000400u) >> 15) & 0x00010001u;
 }
 
-// Token `tok` of a tile sees positions lo <= j < hi.
+// Token `tok` of a tile sees positions lo <= j < hi (with masks, those that all of the
+// sequence's tokens see).
 struct Seen {
     int lo, hi;
 };
+template <bool TREE>
 __device__ __forceinline__ Seen prefill_sees(const AttnArgs& a, const PrefillTile& it, int prefix, int tok) {
     const int pos = it.pos + tok;
+    if (TREE) return {0, tok < it.n ? max(it.base, 0) : 0};
     if (tok >= it.n || pos < 0) return {0, 0};
     return {a.window > 0 ? max(pos + 1 - a.window, 0) : 0, min(max(pos + 1, prefix), it.len)};
 }
@@ -244,6 +251,7 @@ __device__ __forceinline__ Seen prefill_sees(const AttnArgs& a, const PrefillTil
 struct PrefillRow {
     int token, head, pos;
     Seen see;
+    uint64_t mask;  // drafted tokens seen
     bool live;
 };
 
@@ -252,6 +260,7 @@ __device__ __forceinline__ int prefill_token_of(const AttnArgs& a, int r) {
     return (int)(((float)r + 0.5f) * a.inv_group);
 }
 
+template <bool TREE>
 __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const PrefillTile& it, int prefix, int kvh, int r) {
     PrefillRow q;
     const int tok = prefill_token_of(a, r);
@@ -259,7 +268,13 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
     q.head = kvh * a.group + (q.live ? r - tok * a.group : 0);
     q.token = it.token + (q.live ? tok : 0);
     q.pos = it.pos + tok;
-    q.see = prefill_sees(a, it, prefix, tok);
+    q.see = prefill_sees<TREE>(a, it, prefix, tok);
+    q.mask = 0;
+    if (TREE && q.live) {
+        // Without masks a chain: token i of the sequence sees the tokens up to itself.
+        const int i = q.pos - it.base;
+        q.mask = (a.masks ? a.masks[q.token] : low_bits(i + 1)) & low_bits(it.total);
+    }
     return q;
 }
 
@@ -271,13 +286,13 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // has met such a tile start their rows again here, after the fast loop and with
 // nothing of it live, because the same handling inside that loop cost it 100
 // registers (8,192 tokens of 32 heads: 865 us with it inside, 740 us with it here).
-template <int D, int DV, int OPTIONS, int SHARE>
+template <int D, int DV, int OPTIONS, int SHARE, bool TREE>
 __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const PrefillTile& it, int prefix,
                                                         int split, int kvh, int wave, int k_begin, int k_end) {
     constexpr int OUT = DV / (2 * SHARE);  // output dimensions of a lane
     const int lane = threadIdx.x & 63, n = lane & 31, d0 = (lane >> 5) * (D / 2);
     const int o0 = (2 * (wave % SHARE) + (lane >> 5)) * OUT;
-    const PrefillRow q = prefill_row(a, it, prefix, kvh, wave / SHARE * 32 + n);
+    const PrefillRow q = prefill_row<TREE>(a, it, prefix, kvh, wave / SHARE * 32 + n);
     const ScoreParams sp = score_params<OPTIONS>(a, q.head);
     const _Float16* qp = reinterpret_cast<const _Float16*>(a.q) + ((size_t)q.token * a.heads + q.head) * D + d0;
     const int* row = a.c.table + (size_t)it.s * a.c.cols;
@@ -297,7 +312,11 @@ __device__ __forceinline__ void prefill_rows_one_by_one(const AttnArgs& a, const
 #pragma unroll 4
         for (int i = 0; i < D / 2; ++i) dot = __builtin_fmaf((float)qp[i], (float)kp[i], dot);
         dot += __shfl_xor(dot, 32, 64);
-        if (key < q.see.lo || key >= q.see.hi) continue;
+        if (TREE) {
+            if (!q.live || !(seen_word({q.mask, 0, q.see.hi, 0}, key, it.base) & 1)) continue;
+        } else if (key < q.see.lo || key >= q.see.hi) {
+            continue;
+        }
         const float s = score<OPTIONS>(dot, sp, key - q.pos);
         const float m_new = fmaxf(m, s), base = m_new == Q4_NEG_INF ? 0.0f : m_new;
         const float f = exp2_hw(m - base), p = exp2_hw(s - base);
@@ -333,10 +352,12 @@ struct PrefillShared {
     int found[WAVES];                       // a wave has seen infinities or NaN where a row is masked
 };
 
-template <int D, int DV, int OPTIONS, int ROWS>
-__global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 64 ? 1 : 2)
+// TREE: drafted tokens, which see the positions before them all and those of each other
+// that their masks name.
+template <int D, int DV, int OPTIONS, int ROWS, bool TREE>
+__global__ void __launch_bounds__(prefill_threads(DV, ROWS), D > 128 && ROWS == 64 ? 1 : 2)
     attn_prefill_kernel(AttnArgs a, int tile0) {
-    constexpr int SHARE = prefill_share(D, ROWS), THREADS = prefill_threads(D, ROWS), WAVES = THREADS / 64;
+    constexpr int SHARE = prefill_share(DV, ROWS), THREADS = prefill_threads(DV, ROWS), WAVES = THREADS / 64;
     constexpr bool EXTRA = OPTIONS != kNoOptions;
     constexpr int KEYS = 2 / SHARE;                 // blocks of 32 keys of a wave
     constexpr int DIMS = DV / (32 * SHARE);         // and of 32 output dimensions
@@ -359,27 +380,30 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
     const int part = wave % SHARE, rows0 = wave / SHARE * 32;
-    auto& shared = *reinterpret_cast<PrefillShared<WAVES, (SHARE > 1)>*>(lds + a.images * IMAGE);
+    // Two images of keys wider than values fill half of a CU's LDS to the last byte:
+    // what is behind them elsewhere is used after the tiles only, and lies in the first.
+    constexpr bool WITHIN = D != DV && SHARE == 1;
+    auto& shared = *reinterpret_cast<PrefillShared<WAVES, (SHARE > 1)>*>(lds + (WITHIN ? 0 : a.images * IMAGE));
 
     const int prefix = it.prefix;
-    const PrefillRow q = prefill_row(a, it, prefix, kvh, rows0 + n);
+    const PrefillRow q = prefill_row<TREE>(a, it, prefix, kvh, rows0 + n);
     const int head = q.head, token = q.token, qpos = q.pos, hi = q.see.hi, lo = q.see.lo;
     const bool live = q.live;
     // What a token sees starts and ends no earlier than what the one before it
     // sees: all of the wave's rows see [all_lo, all_hi), none sees from any_hi on.
     const int tok0 = __builtin_amdgcn_readfirstlane(prefill_token_of(a, rows0));
     const int tok1 = min(__builtin_amdgcn_readfirstlane(prefill_token_of(a, rows0 + 31)), it.n - 1);
-    const int all_hi = prefill_sees(a, it, prefix, tok0).hi;
-    const Seen most = prefill_sees(a, it, prefix, tok1);
-    const int any_hi = tok0 < it.n ? most.hi : 0, all_lo = most.lo;
+    const int all_hi = prefill_sees<TREE>(a, it, prefix, tok0).hi;
+    const Seen most = prefill_sees<TREE>(a, it, prefix, tok1);
+    const int any_hi = tok0 < it.n ? (TREE ? it.len : most.hi) : 0, all_lo = most.lo;
 
     // All of the workgroup's rows see [seen_lo, seen_hi).
-    const int seen_hi = prefill_sees(a, it, prefix, 0).hi, seen_lo = prefill_sees(a, it, prefix, it.n - 1).lo;
+    const int seen_hi = prefill_sees<TREE>(a, it, prefix, 0).hi, seen_lo = prefill_sees<TREE>(a, it, prefix, it.n - 1).lo;
 
     // Tiles of the workgroup: the first token sees the lowest position, the last
     // (or the prefix) the highest.
     const int last = it.pos + it.n - 1;
-    const int wg_hi = last >= 0 ? min(max(last + 1, prefix), it.len) : 0;
+    const int wg_hi = TREE ? it.len : last >= 0 ? min(max(last + 1, prefix), it.len) : 0;
     const int wg_lo = a.window > 0 ? max(it.pos + 1 - a.window, 0) : 0;
     const int first_tile = wg_lo / kTileKeys;
     const int tiles = max((wg_hi + kTileKeys - 1) / kTileKeys - first_tile, 0);
@@ -580,7 +604,8 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
             // Operand reads run ahead of the products: KW steps of K, and VW of V before
             // the softmax, as many as registers hold without spilling (a spilled
             // register's reload would wait for the tiles under way).
-            constexpr int STEPS = D / 16, KW = STEPS == 4 || (D > 192 && EXTRA) ? 2 : STEPS == 6 ? 3 : 4;
+            constexpr int STEPS = D / 16;
+            constexpr int KW = STEPS == 4 || (D > 192 && EXTRA) || (D > DV && D > 128 && SHARE == 1) ? 2 : STEPS == 6 ? 3 : 4;
             constexpr int VW = (SHARE > 1 ? D <= 192 : !EXTRA) ? 2 : 1;
             u4 kf[KW][KEYS];
 #pragma unroll
@@ -640,7 +665,15 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                             s[b][i] += __builtin_fmaf(sp.slope2, (float)(32 * b + 16 * (i >> 3) + (i & 7)), bias);
                 }
             }
-            if (masked) {
+            if (TREE && masked) {
+                const uint64_t word = seen_word({q.mask, 0, hi, 0}, kb, it.base);
+#pragma unroll
+                for (int b = 0; b < KEYS; ++b) {
+                    const uint32_t bits = (uint32_t)(word >> (32 * (KEYS * part + b))) >> (8 * h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[b][i] = bits >> (16 * (i >> 3) + (i & 7)) & 1 ? s[b][i] : Q4_NEG_INF;
+                }
+            } else if (masked) {
                 // seen: lo <= key < hi, as one unsigned comparison
                 const int from = kw + 8 * h - lo;
                 const unsigned count = (unsigned)max(hi - lo, 0);
@@ -650,6 +683,8 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
                     for (int i = 0; i < 16; ++i)
                         s[b][i] = (unsigned)(from + 32 * b + 16 * (i >> 3) + (i & 7)) < count ? s[b][i] : Q4_NEG_INF;
                 }
+            }
+            if (masked) {
                 if (gone) {
 #pragma unroll
                     for (int b = 0; b < KEYS; ++b) {
@@ -739,6 +774,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
         while (t_load < t_end) tile(std::true_type{});
     while (t_use < t_end) tile(std::false_type{});
     l += __shfl_xor(l, 32, 64);
+    if constexpr (WITHIN) lds_meet();
     const bool found = __any(bad != 0);
     if (lane == 0) shared.found[wave] = found;
     if constexpr (SHARE > 1) {
@@ -749,7 +785,7 @@ __global__ void __launch_bounds__(prefill_threads(D, ROWS), D > 128 && ROWS == 6
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) any_found |= shared.found[w];
     if (any_found) {
-        prefill_rows_one_by_one<D, DV, OPTIONS, SHARE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
+        prefill_rows_one_by_one<D, DV, OPTIONS, SHARE, TREE>(a, it, prefix, split, kvh, wave, t_begin * kTileKeys, t_end * kTileKeys);
         return;
     }
     if constexpr (SHARE > 1) l += shared.sum[wave ^ 1][n];
@@ -796,23 +832,32 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a) {
     // Tokens outside every sequence have no parts.
     const int token = (int)(r / a.heads);
     if (token < a.q_starts[0] || token >= a.q_starts[a.count]) return;
+    if (a.max_new < a.rows) {
+        // Nor have those past the most of a sequence.
+        for (int s0 = 0; s0 < a.count; s0 += 64) {
+            const int s = min(s0 + (int)(threadIdx.x & 63), a.count - 1), first = a.q_starts[s];
+            if (__any(token >= first + a.max_new && token < a.q_starts[s + 1])) return;
+        }
+    }
     const float* part = a.workspace + kAttnCounters;
     store_joined(join_parts<D, false>(part + r * D, part + (long)splits * rows * D + r * 2, rows, splits), a.out + r * D);
 }
 
-template <int D, int DV, int OPTIONS, int ROWS>
+template <int D, int DV, int OPTIONS, int ROWS, bool TREE>
 static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     constexpr size_t image = kTileKeys * (D + DV) * sizeof(uint16_t);
-    constexpr size_t behind = sizeof(PrefillShared<prefill_threads(D, ROWS) / 64, (prefill_share(D, ROWS) > 1)>);
+    constexpr bool within = D != DV && prefill_share(DV, ROWS) == 1;
+    constexpr size_t behind =
+        within ? 0 : sizeof(PrefillShared<prefill_threads(DV, ROWS) / 64, (prefill_share(DV, ROWS) > 1)>);
     // Two workgroups of four waves per CU hide each other's waits where there are
     // enough of them; fewer workgroups, and those of eight waves, get as many
     // images as a CU's LDS holds, up to four (three tiles ahead).
     const long tiles = prefill_tiles(a.rows, a.count, ROWS, a.group);
-    const bool two = prefill_threads(D, ROWS) == 256 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
+    const bool two = prefill_threads(DV, ROWS) == 256 && tiles * a.c.kv_heads * a.splits > dev.num_cu;
     const int fit = (int)(((two ? dev.max_lds / 2 : dev.max_lds) - behind) / image);
     a.images = fit < 2 ? 2 : fit > 4 ? 4 : fit;
-    auto kernel = &attn_prefill_kernel<D, DV, OPTIONS, ROWS>;
-    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, DV, OPTIONS, ROWS>>::value[dev.device];
+    auto kernel = &attn_prefill_kernel<D, DV, OPTIONS, ROWS, TREE>;
+    std::atomic<int>& ready = PerDevice<&attn_prefill_kernel<D, DV, OPTIONS, ROWS, TREE>>::value[dev.device];
     if (!ready.load(std::memory_order_acquire)) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
@@ -824,7 +869,7 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     const long most = 65535;  // of a grid's third dimension
     for (long t = 0; t < tiles; t += most) {
         const dim3 grid(a.c.kv_heads, a.splits, (unsigned)(tiles - t < most ? tiles - t : most));
-        hipLaunchKernelGGL((attn_prefill_kernel<D, DV, OPTIONS, ROWS>), grid, dim3(prefill_threads(D, ROWS)), a.images * image + behind,
+        hipLaunchKernelGGL((attn_prefill_kernel<D, DV, OPTIONS, ROWS, TREE>), grid, dim3(prefill_threads(DV, ROWS)), a.images * image + behind,
                            st, a, (int)t);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -832,15 +877,15 @@ static hipError_t launch_tiles(AttnArgs a, const DeviceInfo& dev, hipStream_t st
     return hipSuccess;
 }
 
-template <int D, int DV, int OPTIONS>
+template <int D, int DV, int OPTIONS, bool TREE = false>
 static hipError_t launch_rows(const AttnArgs& a, int rows, const DeviceInfo& dev, hipStream_t st) {
     if constexpr (D != 96) {  // three blocks of 32 dimensions do not share out
-        if (rows == 64) return launch_tiles<D, DV, OPTIONS, 64>(a, dev, st);
+        if (rows == 64) return launch_tiles<D, DV, OPTIONS, 64, TREE>(a, dev, st);
     }
-    return launch_tiles<D, DV, OPTIONS, 128>(a, dev, st);
+    return launch_tiles<D, DV, OPTIONS, 128, TREE>(a, dev, st);
 }
 
-template <int D, int DV = D>
+template <int D, int DV = D, bool TREE = false>
 static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStream_t st) {
     a.inv_group = 1.0f / (float)a.group;
     PrefillPlan plan = prefill_plan(a.rows, a.count, a.heads, a.c.kv_heads, D, DV, a.max_length);
@@ -856,8 +901,8 @@ static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStre
     a.tile = prefill_tokens(plan.rows, a.group);
     a.inv_tile = 1.0f / (float)a.tile;
     hipError_t e = hipSuccess;
-    if constexpr (DV != D) {
-        e = launch_rows<D, DV, kNoOptions>(a, plan.rows, dev, st);
+    if constexpr (DV != D || TREE) {
+        e = launch_rows<D, DV, kNoOptions, TREE>(a, plan.rows, dev, st);
     } else {
         switch (attn_options(a)) {
             case kNoOptions: e = launch_rows<D, DV, kNoOptions>(a, plan.rows, dev, st); break;
@@ -869,6 +914,17 @@ static hipError_t launch_prefill_attn(AttnArgs a, const DeviceInfo& dev, hipStre
     const long rows = (long)a.rows * a.heads;
     hipLaunchKernelGGL((attn_prefill_join_kernel<DV>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
     return hipGetLastError();
+}
+
+hipError_t launch_prefill_tree(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st) {
+    switch (a.c.dim) {
+        case 64: return launch_prefill_attn<64, 64, true>(a, dev, st);
+        case 96: return launch_prefill_attn<96, 96, true>(a, dev, st);
+        case 128: return launch_prefill_attn<128, 128, true>(a, dev, st);
+        case 192: return launch_prefill_attn<192, 192, true>(a, dev, st);
+        case 256: return launch_prefill_attn<256, 256, true>(a, dev, st);
+    }
+    return hipErrorInvalidValue;  // widths are validated before
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st) {

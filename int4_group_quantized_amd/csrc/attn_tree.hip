@@ -440,10 +440,20 @@ static int tree_blocks(int kv_heads, int group, int max_new, int dim, int* rb) {
     return (int)((rows + 16 * *rb - 1) / (16 * *rb)) * kv_heads;
 }
 
-int64_t attn_tree_workspace(int heads, int kv_heads, int dim, int max_new) {
+// Whether the prompt kernel serves a call: from this many rows of a sequence and kv
+// head on, where its tiles, which all waves of a workgroup share, cost less than
+// every wave's own loads; options are this file's.
+constexpr int kPromptRows = 64;
+static bool by_prompt(int max_new, int group) { return max_new * group >= kPromptRows; }
+
+int64_t attn_tree_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int max_new,
+                            int64_t max_length) {
     int rb;
     const int pairs = tree_blocks(kv_heads, heads / kv_heads, max_new, dim, &rb);
-    return new_workspace_bytes(tree_target(pairs, dim, rb), pairs, 16 * rb, dim);
+    const int64_t own = new_workspace_bytes(tree_target(pairs, dim, rb), pairs, 16 * rb, dim);
+    if (!by_prompt(max_new, heads / kv_heads)) return own;
+    const int64_t prompt = attn_prefill_workspace(tokens, count, heads, kv_heads, dim, dim, max_length);
+    return prompt > own ? prompt : own;
 }
 
 template <int D, int RB>
@@ -483,7 +493,13 @@ static hipError_t launch_tree(const NewArgs& x, hipStream_t st) {
     return launch_tree_rows<D, 2>(x, pairs, st);
 }
 
-hipError_t launch_attn_tree(const NewArgs& x, hipStream_t st) {
+hipError_t launch_attn_tree(const NewArgs& x, const DeviceInfo& dev, hipStream_t st) {
+    if (by_prompt(x.max_new, x.a.group) && attn_options(x.a) == kNoOptions && x.a.window == 0) {
+        AttnArgs a = x.a;
+        a.masks = x.masks;
+        a.max_new = x.max_new;
+        return launch_prefill_tree(a, dev, st);
+    }
     switch (x.a.c.dim) {
         case 64: return launch_tree<64>(x, st);
         case 96: return launch_tree<96>(x, st);

@@ -352,7 +352,7 @@ PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     t.dev.add(starts);
     const uint64_t* masks = optional<uint64_t>(a[6], "masks", at::kLong, {t.rows}, t.dev);
     const int64_t max_new = a[11] == Py_None ? std::min<int64_t>(t.rows, Q4G128_MAX_DRAFT) : integer(a[11]);
-    const int64_t need = q4g128_attn_tree_workspace(t.heads, t.c.kv_heads, t.c.dim, max_new);
+    const int64_t need = q4g128_attn_tree_workspace(t.rows, t.count, t.heads, t.c.kv_heads, t.c.dim, max_new, t.max_length);
     if (need < 0) return PyLong_FromLongLong(need);
     const c10::DeviceGuard guard(t.dev.device);
     const hipStream_t stream = current_stream(t.dev.device);

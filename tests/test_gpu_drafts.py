@@ -217,7 +217,7 @@ def test_tree_repeats_on_other_streams_and_in_graphs(dev):
     got = q4.q4g128_attn_tree(*args, **options, stream=other)
     other.synchronize()
     assert torch.equal(out, got)
-    ws = torch.zeros(max(q4.q4g128_attn_tree_workspace(8, 2, 128, 22), q4.q4g128_attn_decode_workspace(3, 8, 128)),
+    ws = torch.zeros(max(q4.q4g128_attn_tree_workspace(22, 3, 8, 2, 128, 22, 5056), q4.q4g128_attn_decode_workspace(3, 8, 128)),
                      dtype=torch.uint8, device=dev)
     for _ in range(2):
         assert torch.equal(out, q4.q4g128_attn_tree(*args, **options, workspace=ws))
