@@ -392,10 +392,8 @@ Q4_API q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* c
  *   q4g128_attn_prefill.  No token sees the 65th or a later drafted token of a mask.
  *   max_new: an upper bound on a sequence's drafted tokens, 1 to Q4G128_MAX_DRAFT;
  *   it sizes the launch, and rows of later tokens are left as they were.
- *   options->prefix must be NULL.  max_length as in q4g128_attn_decode.  workspace:
- *   q4g128_attn_tree_workspace() bytes, 16-byte aligned; its first
- *   Q4G128_ATTN_COUNTER_BYTES are left alone, the rest may hold anything, so that the
- *   calls of one stream can share one with q4g128_attn_decode.
+ *   options->prefix must be NULL.  max_length as in q4g128_attn_decode, workspace
+ *   (q4g128_attn_tree_workspace() bytes) as in q4g128_attn_prefill.
  */
 Q4_API int64_t q4g128_attn_tree_workspace(int64_t tokens, int64_t count, int32_t heads,
                              int32_t kv_heads, int32_t dim, int64_t max_new, int64_t max_length);
@@ -476,8 +474,8 @@ Q4_API q4_status q4g128_latent_keep(const q4g128_latent_cache* cache, const int3
  * q4g128_latent_attn -- attention over the rows themselves (absorbed form):
  *     out[t][h] = sum_j softmax_j(scale * q[t][h] . c_j) c_j[:latent]
  *   q [tokens][heads][latent + 64], out [tokens][heads][latent] fp16; q_starts,
- *   lengths, masks, max_new, max_length and workspace (q4g128_latent_attn_workspace()
- *   bytes) as in q4g128_attn_tree; a head's value weights are applied to out by the
+ *   lengths, masks, max_new and max_length as in q4g128_attn_tree, workspace
+ *   (q4g128_latent_attn_workspace() bytes) as in q4g128_attn_prefill; a head's value weights are applied to out by the
  *   caller.  max_new is at most Q4G128_MAX_DRAFT with masks and at most
  *   Q4G128_MAX_TOKENS without.  Numerics as stated for the attention calls.
  *   heads at most Q4G128_MAX_HEADS; scale > 0, finite.

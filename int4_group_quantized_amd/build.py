@@ -30,7 +30,7 @@ DIAG_SOURCES = ["diag.hip"]
 
 SOURCES = ["api.cpp", "gemv.hip", "gemv_group.hip", "gemv_seg.hip", "prefill.hip", "prefill_split.hip", "prefill_pair.hip", "prefill_epilogue.hip", "pack.hip",
            "quantize.hip", "head_int8.hip", "rope_append.hip", "attn_decode.hip", "attn_prefill.hip", "attn_tree.hip", "cache_keep.hip",
-           "latent_append.hip", "latent_attn.hip", "latent_expand.hip"]
+           "latent_append.hip", "latent_attn.hip", "latent_expand.hip", "latent_prefill.hip"]
 # Python binding of the cache and attention calls: an extension module against
 # the torch and Python that run this script.
 BINDING_SOURCE = "binding.cpp"

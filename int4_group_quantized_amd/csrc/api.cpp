@@ -573,14 +573,14 @@ int64_t q4g128_attn_tree_workspace(int64_t tokens, int64_t count, int32_t heads,
     if (tokens > Q4G128_MAX_TOKENS || count > Q4G128_MAX_SEQUENCES || max_length > Q4G128_MAX_N || heads > Q4G128_MAX_HEADS || heads % kv_heads != 0 || heads / kv_heads > Q4G128_MAX_GROUP ||
         !q4::attn_dim_supported(dim) || max_new > Q4G128_MAX_DRAFT)
         return Q4_ESHAPE;
-    return q4::attn_tree_workspace(tokens, count, heads, kv_heads, dim, (int)max_new, max_length);
+    return q4::attn_prefill_workspace(tokens, count, heads, kv_heads, dim, dim, max_length, max_new);
 }
 
 q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, const int32_t* q_starts,
                            const int32_t* lengths, const uint64_t* masks, int64_t max_new, int64_t max_length,
                            int64_t tokens, int64_t count, int32_t heads, const q4g128_attn_options* options,
                            uint16_t* out, void* workspace, int64_t workspace_bytes, void* stream) {
-    q4::NewArgs x;
+    q4::AttnArgs a;
     if (!q_starts) return Q4_EINVAL;
     const int64_t need = cache ? q4g128_attn_tree_workspace(tokens, count, heads, cache->kv_heads, cache->dim, max_new,
                                                             max_length)
@@ -588,18 +588,18 @@ q4_status q4g128_attn_tree(const uint16_t* q, const q4g128_kv_cache* cache, cons
     if (need < 0) return (q4_status)need;
     if (options && options->prefix) return Q4_EINVAL;
     q4_status s = check_attention(q, cache, lengths, max_length, tokens, count, heads, options, out, workspace,
-                                  workspace_bytes, need, &x.a);
+                                  workspace_bytes, need, &a);
     if (s != Q4_OK) return s;
     s = check_new(q_starts, masks, tokens, count, out, (size_t)tokens * (size_t)heads * (size_t)cache->dim * 2,
                   workspace, (size_t)need);
     if (s != Q4_OK) return s;
-    x.a.q_starts = q_starts;
-    x.masks = masks;
-    x.max_new = (int)max_new;
+    a.q_starts = q_starts;
+    a.masks = masks;
+    a.max_new = (int)max_new;
     q4::DeviceInfo dev;
     s = current_device(&dev);
     if (s != Q4_OK) return s;
-    hipError_t e = q4::launch_attn_tree(x, dev, (hipStream_t)stream);
+    hipError_t e = q4::launch_attn_tree(a, dev, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 
@@ -795,7 +795,7 @@ q4_status q4g128_latent_prefill(const uint16_t* q, const q4g128_kv_cache* expand
     q4::DeviceInfo dev;
     s = current_device(&dev);
     if (s != Q4_OK) return s;
-    hipError_t e = q4::launch_attn_prefill(a, dev, (hipStream_t)stream);
+    hipError_t e = q4::launch_latent_prefill(a, dev, (hipStream_t)stream);
     return e == hipSuccess ? Q4_OK : device_error(e);
 }
 

@@ -93,14 +93,11 @@ hipError_t launch_cache_keep(const KeepArgs& a, hipStream_t st);
 hipError_t launch_attn_decode(const AttnArgs& a, hipStream_t st);
 int64_t attn_decode_workspace(int64_t batch, int heads, int dim);
 hipError_t launch_attn_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
-// Drafted tokens without options by the prompt kernel; its workspace.
-hipError_t launch_prefill_tree(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
+hipError_t launch_attn_tree(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
+hipError_t launch_latent_prefill(const AttnArgs& a, const DeviceInfo& dev, hipStream_t st);
+// max_new: most tokens of a sequence, for drafted ones.
 int64_t attn_prefill_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int dim_v,
-                               int64_t max_length);
-struct NewArgs;  // attn_new.hpp
-hipError_t launch_attn_tree(const NewArgs& x, const DeviceInfo& dev, hipStream_t st);
-int64_t attn_tree_workspace(int64_t tokens, int64_t count, int heads, int kv_heads, int dim, int max_new,
-                            int64_t max_length);
+                               int64_t max_length, int64_t max_new = 0);
 
 // The table's page for a position of sequence `row`, or -1 when the page is
 // absent.  pos must lie below cols << shift.

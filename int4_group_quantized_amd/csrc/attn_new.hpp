@@ -1,6 +1,6 @@
 // New tokens over a cache: what they see, and how the cached positions are shared
-// out to workgroups.  Used by the attention of drafted tokens (attn_tree.hip) and
-// the latent attention (latent_attn.hip).
+// out to workgroups.  Used by the latent attention (latent_attn.hip); what they see also
+// by the attention of drafted tokens (attn_tree.hip).
 //
 // The n new tokens of a sequence are its last n cached positions, base .. base +
 // n - 1.  Without masks token i sees every position up to base + i.  With masks it
@@ -41,11 +41,8 @@ __device__ __forceinline__ NewSeq new_seq(const NewArgs& x, int s, int first, in
     return r;
 }
 
-// First tile that any of its tokens may see, and the number of tiles.
-__device__ __forceinline__ int new_tiles(const NewArgs& x, const NewSeq& q, int& first) {
-    first = x.a.window > 0 ? max(q.base + 1 - x.a.window, 0) / kTileKeys : 0;
-    return q.n > 0 ? (q.len + kTileKeys - 1) / kTileKeys - first : 0;
-}
+// Its tiles of positions.
+__device__ __forceinline__ int new_tiles(const NewSeq& q) { return q.n > 0 ? (q.len + kTileKeys - 1) / kTileKeys : 0; }
 
 __device__ __forceinline__ int bits_of(uint64_t v) { return __builtin_popcountll(v); }
 
@@ -64,25 +61,25 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
     return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
 }
 
-__device__ __forceinline__ SeenRow seen_row(const NewArgs& x, const NewSeq& q, int token) {
+__device__ __forceinline__ SeenRow seen_row(const uint64_t* masks, int window, const NewSeq& q, int token) {
     SeenRow r = {0, 0, 0, 0};
     if (token >= q.n) return r;
-    if (x.masks) {
-        const uint64_t* mine = x.masks + q.row;
+    if (masks) {
+        const uint64_t* mine = masks + q.row;
         const uint64_t valid = low_bits(q.n);
         r.mask = mine[token] & valid;
         r.place = place_of(q, r.mask);
         r.hi = max(q.base, 0);
-        if (x.a.window > 0 && x.a.window <= kMaskTokens) {
+        if (window > 0 && window <= kMaskTokens) {
             // places differ by 63 at most
             for (int k = 0; k < min(q.n, kMaskTokens); ++k)
-                if (place_of(q, mine[k] & valid) <= r.place - x.a.window) r.mask &= ~((uint64_t)1 << k);
+                if (place_of(q, mine[k] & valid) <= r.place - window) r.mask &= ~((uint64_t)1 << k);
         }
     } else {
         r.place = q.base + token;
         r.hi = max(r.place + 1, 0);
     }
-    r.lo = x.a.window > 0 ? max(r.place + 1 - x.a.window, 0) : 0;
+    r.lo = window > 0 ? max(r.place + 1 - window, 0) : 0;
     return r;
 }
 
@@ -105,11 +102,11 @@ struct NewPart {
 };
 
 // Tiles of a part: the total over `target`, rounded up, so that there are at most
-// target + (sequences of several parts) parts of such sequences; at least `least`.
-__device__ __forceinline__ int new_chunk(int64_t total, int target, int least) {
+// target + (sequences of several parts) parts of such sequences.
+__device__ __forceinline__ int new_chunk(int64_t total, int target) {
     const float quotient = (float)total / (float)target;
     if (quotient > (float)(1 << 22)) return 1 << 26;  // more than any sequence has
-    int c = max((int)quotient - 1, least);            // at most two below
+    int c = max((int)quotient - 1, 1);                // at most two below
     while ((int64_t)c * target < total) ++c;
     return c;
 }
@@ -118,7 +115,7 @@ __device__ __forceinline__ int new_chunk(int64_t total, int target, int least) {
 // computes it for itself.  A sequence with new tokens but no positions has a part,
 // which writes zeros.  A sequence of several parts has more than total / target
 // tiles, so there are fewer than `target` of them, with fewer than 2 target parts.
-__device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int least) {
+__device__ __forceinline__ NewPart new_part(const NewArgs& x, int item) {
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 63;
     NewPart r;
@@ -128,12 +125,11 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
         const auto of = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
         const NewSeq q = new_seq(x, 0, first, last, len);
-        int t0;
-        const int n = new_tiles(x, q, t0), chunk = new_chunk(n, x.target, least);
+        const int n = new_tiles(q), chunk = new_chunk(n, x.target);
         r.parts = q.n == 0 ? 0 : n > chunk ? (n + chunk - 1) / chunk : 1;
         r.part = item;
-        r.t_begin = t0 + item * chunk;
-        r.t_end = min(t0 + n, r.t_begin + chunk);
+        r.t_begin = item * chunk;
+        r.t_end = min(n, r.t_begin + chunk);
         if (item < r.parts) r.q = q;
         return r;
     }
@@ -144,15 +140,13 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
     };
     int64_t total = 0;
     for (int s0 = 0; s0 < a.count; s0 += 64) {
-        int t0;
-        total += lane_scan(new_tiles(x, seq_of(s0 + lane), t0)).last;
+        total += lane_scan(new_tiles(seq_of(s0 + lane))).last;
     }
-    const int chunk = new_chunk(total, x.target, least);
+    const int chunk = new_chunk(total, x.target);
     int before = 0;  // parts of earlier sequences
     for (int s0 = 0; s0 < a.count; s0 += 64) {
         const NewSeq q = seq_of(s0 + lane);
-        int t0;
-        const int tiles = new_tiles(x, q, t0);
+        const int tiles = new_tiles(q);
         const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
         const LaneScan s = lane_scan(n), several = lane_scan(n > 1 ? n : 0);
         const uint64_t hit = __ballot(n > 0 && item < before + s.upto && item >= before + s.upto - n);
@@ -169,8 +163,8 @@ __device__ __forceinline__ NewPart new_part(const NewArgs& x, int item, int leas
             r.slot += of(several.upto - (n > 1 ? n : 0));
             // Alike parts: the last one is no shorter than it has to be.
             const int per = (of(tiles) + r.parts - 1) / r.parts;
-            r.t_begin = of(t0) + r.part * per;
-            r.t_end = min(of(t0 + tiles), r.t_begin + per);
+            r.t_begin = r.part * per;
+            r.t_end = min(of(tiles), r.t_begin + per);
             return r;
         }
         r.slot += several.last;
@@ -184,7 +178,7 @@ struct NewParts {
     NewSeq q;
     int parts, slot;
 };
-__device__ __forceinline__ NewParts new_parts(const NewArgs& x, int s, int least) {
+__device__ __forceinline__ NewParts new_parts(const NewArgs& x, int s) {
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 63;
     const auto seq_of = [&](int i) {
@@ -194,16 +188,14 @@ __device__ __forceinline__ NewParts new_parts(const NewArgs& x, int s, int least
     };
     int64_t total = 0;
     for (int s0 = 0; s0 < a.count; s0 += 64) {
-        int t0;
-        total += lane_scan(new_tiles(x, seq_of(s0 + lane), t0)).last;
+        total += lane_scan(new_tiles(seq_of(s0 + lane))).last;
     }
-    const int chunk = new_chunk(total, x.target, least);
+    const int chunk = new_chunk(total, x.target);
     NewParts r;
     r.slot = 0;
     for (int s0 = 0;; s0 += 64) {
         const NewSeq q = seq_of(s0 + lane);
-        int t0;
-        const int tiles = new_tiles(x, q, t0);
+        const int tiles = new_tiles(q);
         const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
         const LaneScan several = lane_scan(n > 1 ? n : 0);
         if (s >= s0 + 64) {

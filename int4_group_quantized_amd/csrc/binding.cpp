@@ -360,7 +360,8 @@ PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor ws = workspace_of(a[14], need, t.dev, stream);
     return answer(q4g128_attn_tree(t.qp(), &t.c, static_cast<const int32_t*>(starts.data_ptr()), t.lp(), masks, max_new,
                                    t.max_length, t.rows, t.count, t.heads, &t.o,
-                                   static_cast<uint16_t*>(out.data_ptr()), ws.data_ptr(), ws.numel(), stream),
+                                   static_cast<uint16_t*>(out.data_ptr()), ws.defined() ? ws.data_ptr() : nullptr,
+                                   ws.defined() ? ws.numel() : 0, stream),
                   out);
     END_HANDLE_TH_ERRORS
 }

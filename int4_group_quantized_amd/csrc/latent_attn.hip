@@ -28,7 +28,7 @@
 // chunk numbers are exclusive-ored with some of the row's (swizzle) so that the 16
 // rows of a key operand and the rows of a transposed read fall on different banks.
 //
-// The positions are cut into parts as for drafted tokens (attn_new.hpp).
+// The positions are cut into parts (attn_new.hpp), which a second launch joins.
 #include "latent.hpp"
 #include "lds_loads.hpp"
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ void latent_row_one_by_one(const NewArgs& x, const Ne
     constexpr int D = L + kRot, PER = L / 64;
     const AttnArgs& a = x.a;
     const int lane = threadIdx.x & 63, end = min(kb + kTileKeys, q.len), pmask = (1 << a.c.shift) - 1;
-    const SeenRow see = seen_row(x, q, token);
+    const SeenRow see = seen_row(x.masks, 0, q, token);
     const _Float16* qp = reinterpret_cast<const _Float16*>(a.q) + ((size_t)(q.row + token) * a.heads + head) * D;
     float acc[PER];
 #pragma unroll
@@ -128,7 +128,7 @@ __device__ __forceinline__ LatentWork latent_work(const NewArgs& x, int rows) {
     w.it.q.s = -1;
     w.nrows = 0;
     if (w.pair >= w.pairs) return w;
-    w.it = new_part(x, blockIdx.x, 1);
+    w.it = new_part(x, blockIdx.x);
     w.nrows = w.it.q.s < 0 ? 0 : min(rows, min(w.it.q.n, x.max_new) * x.a.heads - w.r0);
     if (w.nrows <= 0) return w;
     const int base = w.it.q.base;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs 
                 // Formed again for each such tile: kept, it would take 20 registers.
 #pragma unroll 1
                 for (int b = 0; b < RB; ++b) {
-                    const SeenRow see = seen_row(x, work.it.q, (r0 + min(16 * b + n, nrows - 1)) / a.heads);
+                    const SeenRow see = seen_row(x.masks, 0, work.it.q, (r0 + min(16 * b + n, nrows - 1)) / a.heads);
                     seen |= ((uint32_t)(seen_word(see, kb, base) >> (16 * wave + 4 * g)) & 15) << (4 * b);
                 }
             }
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_wide_kernel(New
                 left_from = min(left_from, t);
                 left_to = t + 1;
             } else {
-                const SeenRow see = seen_row(x, work.it.q, (r0 + min(32 * rh + n, nrows - 1)) / a.heads);
+                const SeenRow see = seen_row(x.masks, 0, work.it.q, (r0 + min(32 * rh + n, nrows - 1)) / a.heads);
                 uint32_t word = (uint32_t)(seen_word(see, kb, base) >> (32 * kh));
                 if (gone >> (2 * kh) & 1) word &= 0xFFFF0000u;
                 if (gone >> (2 * kh) & 2) word &= 0x0000FFFFu;
@@ -722,7 +722,7 @@ template <int L, int RW>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(NewArgs x, int rows) {
     __shared__ JoinShared<L, RW, kLatentTarget + 1> sh;
     const AttnArgs& a = x.a;
-    const NewParts p = new_parts(x, blockIdx.y + blockIdx.z * kLatentGridY, 1);
+    const NewParts p = new_parts(x, blockIdx.y + blockIdx.z * kLatentGridY);
     const int row0 = blockIdx.x * RW, all = min(p.q.n, x.max_new) * a.heads;
     if (p.parts < 2 || row0 >= all) return;
     join_rows(
