@@ -161,41 +161,52 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(Expand
     struct Done {
         int kb, from, to, page;
     } done = {0, 0, 0, -1};
+    // Eight neighbours of one row of results: registers 8 j .. 8 j + 7 of a block hold,
+    // in a lane's lower and upper partner, two runs of eight by halves; of each pair of
+    // dwords the partners swap the one that belongs to the other.  The lane's run is
+    // number 2 j + h.
+    const auto run_of = [&](const f16r& x, int j) {
+        uint32_t lo[2], hi[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            lo[e] = as_u32((h2){(_Float16)x[8 * j + 2 * e], (_Float16)x[8 * j + 2 * e + 1]});
+            hi[e] = as_u32((h2){(_Float16)x[8 * j + 4 + 2 * e], (_Float16)x[8 * j + 5 + 2 * e]});
+        }
+        const auto r0 = __builtin_amdgcn_permlane32_swap(lo[0], hi[0], false, false);
+        const auto r1 = __builtin_amdgcn_permlane32_swap(lo[1], hi[1], false, false);
+        return (u4){r0[0], r1[0], r0[1], r1[1]};
+    };
     auto store = [&] {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             if (keys) {
                 const int pos = done.kb + 32 * p + n, page = __shfl(done.page, 2 * p + (n >> 4), 64);
-                if (page >= 0 && pos >= done.from && pos < done.to) {
-                    uint16_t* to = a.to.k + (size_t)page * a.to.k_stride + (((size_t)head << a.to.shift) + (pos & tp)) * K + d0;
+                const bool live = page >= 0 && pos >= done.from && pos < done.to;
+                uint16_t* to = a.to.k + (size_t)max(page, 0) * a.to.k_stride + (((size_t)head << a.to.shift) + (pos & tp)) * K + d0;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint2 v;
-                            v.x = as_u32((h2){(_Float16)acc[p][b][4 * i], (_Float16)acc[p][b][4 * i + 1]});
-                            v.y = as_u32((h2){(_Float16)acc[p][b][4 * i + 2], (_Float16)acc[p][b][4 * i + 3]});
-                            *reinterpret_cast<uint2*>(to + 32 * b + 8 * i + 4 * h) = v;
-                        }
-                }
+                    for (int j = 0; j < 2; ++j) {
+                        const u4 v = run_of(acc[p][b], j);
+                        if (live) *reinterpret_cast<u4*>(to + 32 * b + 16 * j + 8 * h) = v;
+                    }
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = done.kb + 32 * p + 8 * i + 4 * h, page = __builtin_amdgcn_readlane(done.page, 2 * p + (i >> 1));
-                    if (page < 0 || pos + 3 < done.from || pos >= done.to) continue;
+                for (int j = 0; j < 2; ++j) {
+                    const int pos = done.kb + 32 * p + 16 * j + 8 * h, page = __builtin_amdgcn_readlane(done.page, 2 * p + j);
+                    const bool all = pos >= done.from && pos + 7 < done.to;
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
+                        const u4 v = run_of(acc[p][b], j);
+                        if (page < 0) continue;
                         uint16_t* to = a.to.v + (size_t)page * a.to.v_stride +
                                        ((size_t)(head * V + d0 + 32 * b + n) << a.to.shift) + (pos & tp);
-                        uint16_t v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(uint16_t, (_Float16)acc[p][b][4 * i + e]);
-                        if (pos >= done.from && pos + 3 < done.to) {
-                            *reinterpret_cast<uint2*>(to) = {(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
+                        if (all) {
+                            *reinterpret_cast<u4*>(to) = v;
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (pos + e >= done.from && pos + e < done.to) to[e] = v[e];
+                            for (int e = 0; e < 8; ++e)
+                                if (pos + e >= done.from && pos + e < done.to) to[e] = (uint16_t)(v[e >> 1] >> 16 * (e & 1));
                         }
                     }
                 }
