@@ -19,8 +19,8 @@ struct NewArgs {
     AttnArgs a;             // rows: new tokens of all sequences
     const uint64_t* masks;  // [rows], or NULL
     int max_new;            // most new tokens of a sequence that are served
-    int target;             // parts wanted per kv head and row block
-    int pairs;              // kv heads times row blocks of a sequence
+    int target;             // parts wanted per row block
+    int pairs;              // row blocks of a sequence, at most
 };
 
 struct NewSeq {
@@ -92,12 +92,13 @@ __device__ __forceinline__ uint64_t seen_word(const SeenRow& r, int kb, int base
     return w;
 }
 
-// A workgroup's part of one sequence's tiles.
+// A workgroup's part of one sequence's tiles, for one block of its rows.
 struct NewPart {
     NewSeq q;
     int part;     // of the sequence
     int parts;    // parts of the sequence
     int slot;     // workspace slot of its first part, if it has several
+    int block;    // of the sequence's rows
     int t_begin, t_end;
 };
 
@@ -111,108 +112,159 @@ __device__ __forceinline__ int new_chunk(int64_t total, int target) {
     return c;
 }
 
-// The part with number `item`; parts are numbered sequence by sequence.  Each wave
-// computes it for itself.  A sequence with new tokens but no positions has a part,
-// which writes zeros.  A sequence of several parts has more than total / target
-// tiles, so there are fewer than `target` of them, with fewer than 2 target parts.
-__device__ __forceinline__ NewPart new_part(const NewArgs& x, int item) {
+// Parts and row blocks of a sequence.  One with new tokens but no positions has a part,
+// which writes zeros.  A sequence of several parts has more than total / target tiles,
+// so there are fewer than `target` of them, with fewer than 2 target parts.
+struct NewShare {
+    int parts, blocks;
+};
+__device__ __forceinline__ NewShare new_share(const NewArgs& x, const NewSeq& q, int chunk, int rows) {
+    NewShare r;
+    r.parts = q.n == 0 ? 0 : max((new_tiles(q) + chunk - 1) / chunk, 1);
+    r.blocks = (min(q.n, x.max_new) * x.a.heads + rows - 1) / rows;
+    return r;
+}
+
+// Workgroups are dealt to the eight XCDs in turn.  Of `total` items each XCD takes a
+// run, so that neighbours, the row blocks of one part, share an L2.  -1: none left.
+__device__ __forceinline__ int new_item(int total) {
+    const int g = (int)(blockIdx.x + blockIdx.y * gridDim.x), per = (total + 7) / 8, item = (g & 7) * per + (g >> 3);
+    return (g >> 3) < per && item < total ? item : -1;
+}
+
+// The sequences of a call, 64 at a time, one per lane; the first 64 are read once.
+struct NewSeqs {
+    const NewArgs& x;
+    NewSeq first;
+    __device__ __forceinline__ NewSeq read(int s) const {
+        NewSeq q = {-1, 0, 0, 0, 0};
+        if (s < x.a.count) q = new_seq(x, s, x.a.q_starts[s], x.a.q_starts[s + 1], x.a.lengths[s]);
+        return q;
+    }
+    __device__ __forceinline__ explicit NewSeqs(const NewArgs& args) : x(args), first(read(threadIdx.x & 63)) {}
+    __device__ __forceinline__ NewSeq operator()(int s0) const { return s0 == 0 ? first : read(s0 + (int)(threadIdx.x & 63)); }
+    // Tiles of a part.
+    __device__ __forceinline__ int chunk() const {
+        int64_t total = 0;
+        for (int s0 = 0; s0 < x.a.count; s0 += 64) total += lane_scan(new_tiles((*this)(s0))).last;
+        return new_chunk(total, x.target);
+    }
+};
+
+__device__ __forceinline__ NewSeq new_seq_of(const NewSeq& q, int l) {
+    const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+    return {of(q.s), of(q.row), of(q.n), of(q.len), of(q.base)};
+}
+
+// What the workgroup does, in blocks of `rows` rows; each wave computes it for itself.
+// Items are numbered sequence by sequence, part by part, row block by row block.
+__device__ __forceinline__ NewPart new_part(const NewArgs& x, int rows) {
     const AttnArgs& a = x.a;
-    const int lane = threadIdx.x & 63;
     NewPart r;
     r.q.s = -1;
-    r.part = r.parts = r.slot = r.t_begin = r.t_end = 0;
+    r.part = r.parts = r.slot = r.block = r.t_begin = r.t_end = 0;
+    const auto set = [&](const NewSeq& q, const NewShare& s, int number) {
+        r.q = q;
+        r.parts = s.parts;
+        r.part = number / s.blocks;
+        r.block = number - r.part * s.blocks;
+        // Alike parts: the last one is no shorter than it has to be.
+        const int tiles = new_tiles(q), per = (tiles + r.parts - 1) / r.parts;
+        r.t_begin = r.part * per;
+        r.t_end = min(tiles, r.t_begin + per);
+    };
     if (a.count == 1) {
         const auto of = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
         const NewSeq q = new_seq(x, 0, first, last, len);
-        const int n = new_tiles(q), chunk = new_chunk(n, x.target);
-        r.parts = q.n == 0 ? 0 : n > chunk ? (n + chunk - 1) / chunk : 1;
-        r.part = item;
-        r.t_begin = item * chunk;
-        r.t_end = min(n, r.t_begin + chunk);
-        if (item < r.parts) r.q = q;
+        const NewShare s = new_share(x, q, new_chunk(new_tiles(q), x.target), rows);
+        const int item = new_item(s.parts * s.blocks);
+        if (item >= 0) set(q, s, item);
         return r;
     }
-    const auto seq_of = [&](int s) {
-        NewSeq q = {-1, 0, 0, 0, 0};
-        if (s < a.count) q = new_seq(x, s, a.q_starts[s], a.q_starts[s + 1], a.lengths[s]);
-        return q;
+    const NewSeqs seqs(x);
+    const int chunk = seqs.chunk();
+    const auto items_of = [&](const NewSeq& q) {
+        const NewShare s = new_share(x, q, chunk, rows);
+        return s.parts * s.blocks;
     };
-    int64_t total = 0;
+    const LaneScan scan0 = lane_scan(items_of(seqs.first));
+    int total = scan0.last;
+    for (int s0 = 64; s0 < a.count; s0 += 64) total += lane_scan(items_of(seqs(s0))).last;
+    const int item = new_item(total);
+    if (item < 0) return r;
+    int before = 0;  // items of earlier sequences
     for (int s0 = 0; s0 < a.count; s0 += 64) {
-        total += lane_scan(new_tiles(seq_of(s0 + lane))).last;
-    }
-    const int chunk = new_chunk(total, x.target);
-    int before = 0;  // parts of earlier sequences
-    for (int s0 = 0; s0 < a.count; s0 += 64) {
-        const NewSeq q = seq_of(s0 + lane);
-        const int tiles = new_tiles(q);
-        const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
-        const LaneScan s = lane_scan(n), several = lane_scan(n > 1 ? n : 0);
-        const uint64_t hit = __ballot(n > 0 && item < before + s.upto && item >= before + s.upto - n);
+        const NewSeq q = seqs(s0);
+        const NewShare s = new_share(x, q, chunk, rows);
+        const int n = s.parts * s.blocks;
+        const LaneScan scan = s0 == 0 ? scan0 : lane_scan(n), several = lane_scan(s.parts > 1 ? s.parts : 0);
+        const uint64_t hit = __ballot(n > 0 && item < before + scan.upto && item >= before + scan.upto - n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
             const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-            r.q.s = s0 + l;
-            r.q.row = of(q.row);
-            r.q.n = of(q.n);
-            r.q.len = of(q.len);
-            r.q.base = of(q.base);
-            r.parts = of(n);
-            r.part = item - (before + of(s.upto) - r.parts);
-            r.slot += of(several.upto - (n > 1 ? n : 0));
-            // Alike parts: the last one is no shorter than it has to be.
-            const int per = (of(tiles) + r.parts - 1) / r.parts;
-            r.t_begin = r.part * per;
-            r.t_end = min(of(tiles), r.t_begin + per);
+            r.slot += of(several.upto - (s.parts > 1 ? s.parts : 0));
+            set(new_seq_of(q, l), {of(s.parts), of(s.blocks)}, item - (before + of(scan.upto - n)));
             return r;
         }
         r.slot += several.last;
-        before += s.last;
+        before += scan.last;
     }
     return r;
 }
 
-// A sequence's parts, for the second launch.
+// For the second launch: a sequence of several parts, and the workgroup's first row of
+// it, `each` rows a workgroup.  q.s is -1 where there is nothing to do.
 struct NewParts {
     NewSeq q;
-    int parts, slot;
+    int parts, slot, row0;
 };
-__device__ __forceinline__ NewParts new_parts(const NewArgs& x, int s) {
+__device__ __forceinline__ NewParts new_parts(const NewArgs& x, int each) {
     const AttnArgs& a = x.a;
-    const int lane = threadIdx.x & 63;
-    const auto seq_of = [&](int i) {
-        NewSeq q = {-1, 0, 0, 0, 0};
-        if (i < a.count) q = new_seq(x, i, a.q_starts[i], a.q_starts[i + 1], a.lengths[i]);
-        return q;
-    };
-    int64_t total = 0;
-    for (int s0 = 0; s0 < a.count; s0 += 64) {
-        total += lane_scan(new_tiles(seq_of(s0 + lane))).last;
-    }
-    const int chunk = new_chunk(total, x.target);
     NewParts r;
-    r.slot = 0;
-    for (int s0 = 0;; s0 += 64) {
-        const NewSeq q = seq_of(s0 + lane);
-        const int tiles = new_tiles(q);
-        const int n = q.n == 0 ? 0 : max((tiles + chunk - 1) / chunk, 1);
-        const LaneScan several = lane_scan(n > 1 ? n : 0);
-        if (s >= s0 + 64) {
-            r.slot += several.last;
-            continue;
+    r.q.s = -1;
+    r.parts = r.slot = r.row0 = 0;
+    const int item = (int)(blockIdx.x + blockIdx.y * gridDim.x);
+    const NewSeqs seqs(x);
+    const int chunk = seqs.chunk();
+    int before = 0;
+    for (int s0 = 0; s0 < a.count; s0 += 64) {
+        const NewSeq q = seqs(s0);
+        const NewShare s = new_share(x, q, chunk, each);
+        const int n = s.parts > 1 ? s.blocks : 0;
+        const LaneScan scan = lane_scan(n), several = lane_scan(s.parts > 1 ? s.parts : 0);
+        const uint64_t hit = __ballot(n > 0 && item < before + scan.upto && item >= before + scan.upto - n);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            r.q = new_seq_of(q, l);
+            r.parts = of(s.parts);
+            r.slot += of(several.upto - (s.parts > 1 ? s.parts : 0));
+            r.row0 = (item - (before + of(scan.upto - n))) * each;
+            return r;
         }
-        const int l = s - s0;
-        const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-        r.parts = of(n);
-        r.slot += of(several.upto - (n > 1 ? n : 0));
-        r.q.s = s;
-        r.q.row = of(q.row);
-        r.q.n = of(q.n);
-        r.q.len = of(q.len);
-        r.q.base = of(q.base);
-        return r;
+        r.slot += several.last;
+        before += scan.last;
     }
+    return r;
+}
+
+// Workgroups of the two launches, at most: row blocks of all sequences, and of those in
+// several parts for each part.
+inline long new_blocks(const NewArgs& x, int rows) {
+    const long most = ((long)x.max_new * x.a.heads + rows - 1) / rows * x.a.count;  // every sequence as long as it may be
+    const long all = (long)x.a.rows * x.a.heads / rows + x.a.count;
+    return most < all ? most : all;
+}
+inline long new_items(const NewArgs& x, int rows, long tiles) {
+    const long most = ((long)x.target + x.a.count < tiles * x.a.count ? (long)x.target + x.a.count : tiles * x.a.count) * x.pairs;
+    const long all = new_blocks(x, rows) + (x.target > 1 ? 2L * x.target * x.pairs : 0);
+    return most < all ? most : all;
+}
+inline dim3 new_grid(long n) {
+    constexpr long X = 1 << 20;
+    n = (n + 7) / 8 * 8;
+    return dim3((unsigned)(n < X ? n : X), (unsigned)((n + X - 1) / X));
 }
 
 // Partial results: outputs [slots][pairs][R][dim], their maxima and sums
@@ -237,8 +289,7 @@ inline int64_t new_workspace_bytes(int target, long pairs, int rows, int dim) {
     return (new_slots(target) * pairs * rows * (dim + 2) + kAttnCounters) * (int64_t)sizeof(float);
 }
 
-// Join, by a second launch: a workgroup for RW rows of one sequence, of `rows_of(q)`
-// rows in all.  Weights first, a thread for each row and part, then four columns of a
+// Join, by a second launch: a workgroup for RW rows of one sequence, of `rows` in all.  Weights first, a thread for each row and part, then four columns of a
 // row for each thread, all of its parts' requested together; where that leaves
 // threads, several take parts of one four.
 //   at(slot, row): place of the row in part `slot`; stride: from part to part, rows
@@ -254,11 +305,11 @@ struct JoinShared {
     f4 part[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? ITEMS : 1];
 };
 template <int D, int RW, int PARTS, class At, class Out>
-__device__ __forceinline__ void join_rows(JoinShared<D, RW, PARTS>& sh, const NewWorkspace& ws, const NewParts& p, int row0, int rows,
-                                          long stride, At at, Out out) {
+__device__ __forceinline__ void join_rows(JoinShared<D, RW, PARTS>& sh, const NewWorkspace& ws, const NewParts& p, int rows, long stride,
+                                          At at, Out out) {
     using Shared = JoinShared<D, RW, PARTS>;
     constexpr int ITEMS = Shared::ITEMS, GROUPS = Shared::GROUPS, PER = (ITEMS + kJoinThreads - 1) / kJoinThreads;
-    const int tid = threadIdx.x, parts = p.parts;
+    const int tid = threadIdx.x, parts = p.parts, row0 = p.row0;
     const int n = min(RW, rows - row0);
     for (int i = tid; i < n * parts; i += kJoinThreads) {
         const int r = i / parts, k = i % parts;

@@ -40,7 +40,6 @@ typedef float f16s __attribute__((ext_vector_type(16)));
 
 constexpr int kLatentThreads = 256;
 constexpr int kLatentTarget = 256;    // workgroups wanted per launch: one per CU
-constexpr int kLatentGridY = 32768;   // row blocks, or sequences, per layer of the grid
 constexpr int kWeightPitch = 72;      // halves of a row of weights in LDS: 9 chunks, so 16 rows differ in banks
 
 template <int L, int R>
@@ -114,7 +113,6 @@ __device__ __forceinline__ void latent_row_one_by_one(const NewArgs& x, const Ne
 // What a workgroup works on.
 struct LatentWork {
     NewPart it;
-    int pairs, pair;
     int r0, nrows;  // first row of the sequence's, rows
     int t_end;      // tiles end
     int all_hi;     // every row sees [0, all_hi)
@@ -122,13 +120,8 @@ struct LatentWork {
 
 __device__ __forceinline__ LatentWork latent_work(const NewArgs& x, int rows) {
     LatentWork w;
-    w.pairs = x.pairs;
-    w.pair = blockIdx.y + blockIdx.z * kLatentGridY;
-    w.r0 = w.pair * rows;
-    w.it.q.s = -1;
-    w.nrows = 0;
-    if (w.pair >= w.pairs) return w;
-    w.it = new_part(x, blockIdx.x);
+    w.it = new_part(x, rows);
+    w.r0 = w.it.block * rows;
     w.nrows = w.it.q.s < 0 ? 0 : min(rows, min(w.it.q.n, x.max_new) * x.a.heads - w.r0);
     if (w.nrows <= 0) return w;
     const int base = w.it.q.base;
@@ -270,8 +263,8 @@ __device__ __forceinline__ void latent_finish(const NewArgs& x, const LatentWork
         }
         __syncthreads();
     }
-    const NewWorkspace ws = new_workspace(x, w.pairs, R, L);
-    const long first = ((long)(w.it.slot + w.it.part) * w.pairs + w.pair) * R;
+    const NewWorkspace ws = new_workspace(x, x.pairs, R, L);
+    const long first = ((long)(w.it.slot + w.it.part) * x.pairs + w.it.block) * R;
     for (int i = tid; i < w.nrows * (L / 4); i += kLatentThreads) {
         const int r = i / (L / 4), d = i % (L / 4) * 4;
         const f4 o = *reinterpret_cast<const f4*>(&res.o[r][d]);
@@ -722,11 +715,10 @@ template <int L, int RW>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(NewArgs x, int rows) {
     __shared__ JoinShared<L, RW, kLatentTarget + 1> sh;
     const AttnArgs& a = x.a;
-    const NewParts p = new_parts(x, blockIdx.y + blockIdx.z * kLatentGridY);
-    const int row0 = blockIdx.x * RW, all = min(p.q.n, x.max_new) * a.heads;
-    if (p.parts < 2 || row0 >= all) return;
+    const NewParts p = new_parts(x, RW);
+    if (p.q.s < 0) return;
     join_rows(
-        sh, new_workspace(x, x.pairs, rows, L), p, row0, all, (long)x.pairs * rows,
+        sh, new_workspace(x, x.pairs, rows, L), p, min(p.q.n, x.max_new) * a.heads, (long)x.pairs * rows,
         [&](int slot, int row) { return ((long)slot * x.pairs + row / rows) * rows + row % rows; },
         [&](const NewSeq& q, int row) { return a.out + ((size_t)q.row * a.heads + row) * L; });
 }
@@ -739,7 +731,7 @@ static hipError_t launch_latent_rows(NewArgs x, const DeviceInfo& dev, hipStream
     const long rows = (long)x.max_new * x.a.heads, pairs = (rows + R - 1) / R;
     x.target = latent_target(pairs);
     const long tiles = ((long)x.a.max_length + kTileKeys - 1) / kTileKeys;
-    const long grid = (long)x.target + x.a.count < tiles * x.a.count ? (long)x.target + x.a.count : tiles * x.a.count;
+    x.pairs = (int)pairs;
     std::atomic<int>& ready = PerDevice<Kernel>::value[dev.device];
     if (!ready.load(std::memory_order_acquire)) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -747,19 +739,12 @@ static hipError_t launch_latent_rows(NewArgs x, const DeviceInfo& dev, hipStream
         if (e != hipSuccess) return e;
         ready.store(1, std::memory_order_release);
     }
-    x.pairs = (int)pairs;
-    // Workgroups are dealt to the eight XCDs in turn: with a multiple of eight parts the
-    // row blocks of one part are on the same, and its L2 serves all but the first.
-    const dim3 blocks((unsigned)((grid + 7) / 8 * 8), (unsigned)(pairs < kLatentGridY ? pairs : kLatentGridY),
-                      (unsigned)((pairs + kLatentGridY - 1) / kLatentGridY));
-    hipLaunchKernelGGL(Kernel, blocks, dim3(kLatentThreads), bytes, st, x);
+    hipLaunchKernelGGL(Kernel, new_grid(new_items(x, R, tiles)), dim3(kLatentThreads), bytes, st, x);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !new_second(x, tiles)) return e;
     const int rw = join_rows_per_group((long)x.a.rows * x.a.heads);
-    const dim3 groups((unsigned)((rows + rw - 1) / rw), (unsigned)(x.a.count < kLatentGridY ? x.a.count : kLatentGridY),
-                      (unsigned)((x.a.count + kLatentGridY - 1) / kLatentGridY));
     auto join = rw == 16 ? &latent_join_kernel<L, 16> : rw == 4 ? &latent_join_kernel<L, 4> : &latent_join_kernel<L, 1>;
-    hipLaunchKernelGGL(join, groups, dim3(kJoinThreads), 0, st, x, R);
+    hipLaunchKernelGGL(join, new_grid(new_blocks(x, rw)), dim3(kJoinThreads), 0, st, x, R);
     return hipGetLastError();
 }
 

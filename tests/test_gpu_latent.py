@@ -156,6 +156,16 @@ def test_attn_long_and_split(dev, heads):
     attn_case(dev, 13, [1 + i % 3 for i in range(70)], [3 + 37 * i % 400 for i in range(70)], heads, 128, 16)
 
 
+@pytest.mark.parametrize("heads", [3, 20, 40])
+@pytest.mark.parametrize("kind", ["any", None])
+def test_attn_many_sequences_below_a_loose_bound(dev, heads, kind):
+    """Far fewer rows than max_new would allow, sequences without any, one in many parts."""
+    new = [i % 4 for i in range(150)]
+    lengths = [n + 29 * i % 90 for i, n in enumerate(new)]
+    lengths[77] = 3000
+    attn_case(dev, 33, new, lengths, heads, 128, 16, kind, max_new=64)
+
+
 @pytest.mark.parametrize("heads", [3, 30, 64])
 @pytest.mark.parametrize("rising", [0.05, 2.0])
 def test_attn_moving_maximum(dev, heads, rising):
@@ -362,3 +372,49 @@ def test_one_token_through_the_absorbed_products(dev):
         ds = H * scale * (np.abs(weights(*quantized[0][h]) @ x[:own]) @ np.abs(c[:, :latent]).T).max()
         bound = (2 * ds * (1 + ds) + 2 * H) * (w @ (np.abs(c[:, :latent]) @ np.abs(wv).T)) + 1e-4
         assert np.all(np.abs(out[h] - w @ v) <= bound), h
+
+
+def test_binding_refusals(dev):
+    f16, i = dict(dtype=torch.float16, device=dev), dict(dtype=torch.int32, device=dev)
+    rows, table, n, starts = torch.zeros(4, 16, 192, **f16), torch.zeros(3, 4, **i), torch.ones(3, **i), torch.arange(4, **i)
+    pos, kv = torch.zeros(3, **i), torch.zeros(3, 192, device=dev)
+    kc, vc = torch.zeros(4, 2, 16, 128, **f16), torch.zeros(4, 2, 64, 16, **f16)
+    packed, sm = torch.zeros(256, 64, dtype=torch.uint8, device=dev), torch.zeros(256, 1, **f16)
+    calls = {
+        "append": (q4.q4g128_latent_append, dict(kv=kv, cache=rows, table=table, positions=pos, inv_freq=None)),
+        "keep": (q4.q4g128_latent_keep, dict(cache=rows, table=table, starts=n, keep_starts=starts, keep=pos)),
+        "attn": (q4.q4g128_latent_attn, dict(q=torch.zeros(3, 2, 192, **f16), cache=rows, table=table, q_starts=starts,
+                                             lengths=n, scale=0.1)),
+        "expand": (q4.q4g128_latent_expand, dict(cache=rows, table=table, lengths=n, packed=packed, scales=sm, mins=sm.clone(),
+                                                 k_cache=kc, v_cache=vc, expanded_table=table.clone())),
+        "prefill": (q4.q4g128_latent_prefill, dict(q=torch.zeros(3, 2, 128, **f16), k_cache=kc, v_cache=vc, table=table,
+                                                   q_starts=starts, lengths=n, scale=0.1)),
+        "tree": (q4.q4g128_attn_tree, dict(q=torch.zeros(3, 2, 64, **f16), k_cache=torch.zeros(4, 2, 16, 64, **f16),
+                                           v_cache=vc, table=table, q_starts=starts, lengths=n)),
+    }
+    for call, good in calls.values():
+        call(**good)
+        for name, x in good.items():
+            if not isinstance(x, torch.Tensor):
+                continue
+            for bad, error in ((x.cpu(), (ValueError,)), (x.double(), (TypeError,)), (x[None], (ValueError, q4.Q4Error)),
+                               ("x", (TypeError,))):
+                with pytest.raises(error):
+                    call(**dict(good, **{name: bad}))
+    for name, bad, error in (("append", dict(kv=kv[:, :191]), ValueError), ("append", dict(kv=kv.t()), ValueError),
+                             ("append", dict(q_main=torch.zeros(3, 2, 64, device=dev)), ValueError),
+                             ("append", dict(norm=torch.zeros(64, **f16)), ValueError),
+                             ("append", dict(inv_freq=torch.zeros(16, device=dev)), ValueError),
+                             ("attn", dict(masks=pos), TypeError), ("attn", dict(lengths=n[:2]), ValueError),
+                             ("attn", dict(max_new=0), q4.Q4Error), ("attn", dict(scale=0.0), q4.Q4Error),
+                             ("attn", dict(max_length=65), q4.Q4Error), ("attn", dict(workspace=pos), ValueError),
+                             ("attn", dict(cache=rows.transpose(1, 2)), ValueError),
+                             ("attn", dict(masks=pos.long(), max_new=65), q4.Q4Error),
+                             ("keep", dict(keep_starts=starts[:3]), ValueError),
+                             ("expand", dict(packed=packed[:128]), ValueError),
+                             ("expand", dict(expanded_table=table[:2]), (ValueError, q4.Q4Error)),
+                             ("expand", dict(v_cache=kc), ValueError), ("prefill", dict(k_cache=vc), ValueError),
+                             ("tree", dict(masks=pos.long()[:2]), ValueError), ("tree", dict(max_new=65), q4.Q4Error)):
+        with pytest.raises(error):
+            calls[name][0](**dict(calls[name][1], **bad))
+    torch.cuda.synchronize()
