@@ -31,7 +31,8 @@
  *   - `stream` is a hipStream_t (NULL = the null stream).  Calls only enqueue
  *     work; they never synchronise the host.  Buffers must stay alive until
  *     the enqueued work completes.
- *   - Outputs are fully overwritten and must not overlap any input.
+ *   - Outputs are fully overwritten, but for caches and rows that a call is said to
+ *     leave alone, and must not overlap any input.
  *   - Arguments are validated on the host before any HIP call; an invalid
  *     call enqueues nothing.
  *   - Results are deterministic: fixed reduction orders; the only atomics
@@ -65,8 +66,8 @@ typedef int32_t q4_status;
 #define Q4_ESHAPE (-2)
 /* codes / packed / x / X / W not 16-byte aligned; scales / mins not 2-byte
    aligned; y / Y not 4-byte aligned.  For the cache and attention calls: qkv, k,
-   v, q, out and workspace not 16-byte, q_norm / k_norm not 2-byte, other arrays
-   not 4-byte aligned. */
+   v, latent rows, kv, q, q_main, q_rot, out and workspace not 16-byte, norms not
+   2-byte, masks not 8-byte, other arrays not 4-byte aligned. */
 #define Q4_EALIGN (-3)
 /* The HIP runtime reported an error while querying the device or launching;
    q4g128_last_hip_error() returns the hipError_t of the calling thread. */
@@ -320,11 +321,10 @@ Q4_API q4_status q4g128_rope_append_slots(const float* qkv, int64_t ld, int64_t 
  *     out = sum_j softmax(s)_j v_j
  * It sees j <= p, with window > 0 only j > p - window, and in the prompt call
  * also every j < prefix[s]; the tree call says what drafted tokens see.  Scores,
- * softmax statistics and sums are fp32.  The
- * weights enter the second product rounded to fp16, in units of 2 to a running
- * maximum of the base-2 scores: at most 1 in the decode call, at most 2^8 in the
- * others, whose maximum may lag; they are summed as rounded.  out is rounded
- * once to fp16.  A query that sees nothing gives zeros.  What a masked
+ * softmax statistics and sums are fp32.  The weights enter the second product
+ * rounded to fp16, in units of 2 to a running maximum of the base-2 scores: at most
+ * 1 in the decode call, at most 2^8 in the others, whose maximum may lag; they are
+ * summed as rounded.  out is rounded once to fp16.  A query that sees nothing gives zeros.  What a masked
  * position or an absent page holds never reaches a result, NaN included.
  *   scale > 0; softcap >= 0 (0: none); both finite; window >= 0 (0: none).
  */
@@ -387,8 +387,8 @@ Q4_API q4_status q4g128_attn_prefill(const uint16_t* q, const q4g128_kv_cache* c
  *   drafted token k of its sequence where bit k of its mask is set (its own bit
  *   like any other).  Windows and slopes go by a token's place, base + max(bits set
  *   among its sequence's tokens, 1) - 1: for a tree's masks (a token's ancestors and
- *   itself) base + its depth, the position that it is to be turned by; positions below base
- *   are their own places.  NULL: each token sees those before it, as in
+ *   itself) base + its depth, the position that it is to be turned by; positions below
+ *   base are their own places.  NULL: each token sees those before it, as in
  *   q4g128_attn_prefill.  No token sees the 65th or a later drafted token of a mask.
  *   max_new: an upper bound on a sequence's drafted tokens, 1 to Q4G128_MAX_DRAFT;
  *   it sizes the launch, and rows of later tokens are left as they were.
@@ -475,8 +475,8 @@ Q4_API q4_status q4g128_latent_keep(const q4g128_latent_cache* cache, const int3
  *     out[t][h] = sum_j softmax_j(scale * q[t][h] . c_j) c_j[:latent]
  *   q [tokens][heads][latent + 64], out [tokens][heads][latent] fp16; q_starts,
  *   lengths, masks, max_new and max_length as in q4g128_attn_tree, workspace
- *   (q4g128_latent_attn_workspace() bytes) as in q4g128_attn_prefill; a head's value weights are applied to out by the
- *   caller.  max_new is at most Q4G128_MAX_DRAFT with masks and at most
+ *   (q4g128_latent_attn_workspace() bytes) as in q4g128_attn_prefill; a head's value
+ *   weights are applied to out by the caller.  max_new is at most Q4G128_MAX_DRAFT with masks and at most
  *   Q4G128_MAX_TOKENS without.  Numerics as stated for the attention calls.
  *   heads at most Q4G128_MAX_HEADS; scale > 0, finite.
  */

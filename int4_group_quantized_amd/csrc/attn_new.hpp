@@ -1,6 +1,6 @@
-// New tokens over a cache: what they see, and how the cached positions are shared
-// out to workgroups.  Used by the latent attention (latent_attn.hip); what they see also
-// by the attention of drafted tokens (attn_tree.hip).
+// New tokens over a cache: what they see, for the latent attention (latent_attn.hip)
+// and that of drafted tokens (attn_tree.hip), and how the cached positions are shared
+// out to the workgroups of the former.
 //
 // The n new tokens of a sequence are its last n cached positions, base .. base +
 // n - 1.  Without masks token i sees every position up to base + i.  With masks it

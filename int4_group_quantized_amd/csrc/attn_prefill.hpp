@@ -2,7 +2,8 @@
 //
 //   out[t][h] = sum_j softmax_j(s(q[t][h] . k_j)) v_j  over the positions j that
 //   token t sees: causal, its own sequence only, optionally within a window or
-//   with a prefix that every token sees.
+//   with a prefix that every token sees; drafted tokens (TREE) see each other by masks.
+//   Keys of D columns, values of DV: those expanded from latent rows have wider keys.
 //
 // A workgroup of four or eight waves serves 128 query rows of one kv head, or 64
 // where that leaves CUs idle: the tokens of one tile times the heads of the group

