@@ -9,9 +9,9 @@
 // they share memory lines.
 //
 // Bound by the launch and a chain of three reads (bounds, pages, rows): one sequence
-// with 5 kept tokens (8 kv heads of 128) takes 3.9 us, 256 sequences with 12 each
-// 10.7 us for 25 MB read and written (the values in two to three times as much, whole
-// lines).  Numbering the values over the tokens
+// with 5 kept tokens (8 kv heads of 128) takes 3.9 us, 256 sequences with up to
+// 12 each 10.7 to 11.8 us for 14 MB read and written (the values in two to three times
+// as much, whole lines).  Numbering the values over the tokens
 // that there are, not over 32 with most lanes idle, took the latter from 20 us.
 #include "attn.hpp"
 
