@@ -11,7 +11,7 @@
 // own straight from memory into registers, for 16, 32 or 64 rows, was slower in all but
 // the largest calls: 16 sequences of 8 tokens of 16 heads (4 kv heads of 128) on up
 // to 4,000 positions 36 us, 21 here; one of 16 tokens on 8,000 24 and 16; 16 of 64 on
-// 16,384 (32 heads on 8) 574 and 383; 64 sequences of 16 tokens on 8,192 196 and 206.
+// 16,384 (32 heads on 8) 574 and 352; 64 sequences of 16 tokens on 8,192 196 and 206.
 #include "attn_prefill.hpp"
 
 namespace q4 {

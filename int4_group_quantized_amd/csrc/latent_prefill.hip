@@ -1,7 +1,7 @@
 // Attention of prompt tokens over keys and values expanded from latent rows: the
 // kernels of attn_prefill.hpp with keys wider than values, by their rotary part.
 //
-// 4,096 tokens of 64 heads (192 and 128 columns, 344 GFLOP): 378 us, 910 TFLOP/s.  Two
+// 4,096 tokens of 64 heads (192 and 128 columns, 344 GFLOP): 370 us, 930 TFLOP/s.  Two
 // waves for 32 rows, as at dim 192 with values as wide, took 470.
 #include "attn_prefill.hpp"
 

@@ -324,7 +324,9 @@ def test_drafting_step(dev):
     qc = q4.q4g128_rope_append(picked, *chain, i32(range(base, base + m), dev), freq, heads, seq=i32([0] * m, dev))
     want = q4.q4g128_attn_prefill(qc, *chain, i32([0, m], dev), i32([base + m], dev))
     assert torch.equal(q[path], qc)
-    assert torch.allclose(got[path], want, rtol=2e-3, atol=2e-3)
+    # Either call errs by 2^-11 of the result for its last rounding and by 2^-11 of sum w |v| for its weights', both at
+    # most 2^-11 max |v|; sums of these few positions add less than a hundredth of that.
+    assert (got[path].float() - want.float()).abs().max() <= 4.04 * H * tree[1].abs().max()
     q4.q4g128_cache_keep(*tree, i32([base], dev), i32([0, m], dev), i32(path, dev))
     outs = []
     for c in (tree, chain):

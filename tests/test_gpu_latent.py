@@ -367,10 +367,13 @@ def test_one_token_through_the_absorbed_products(dev):
         x = np.concatenate([q_own[h].cpu().numpy().astype(np.float64), turned[h]])
         w = heads_ref.weights(x, k, length - 1, np.ones(length, dtype=bool), scale)
         wv = weights(*quantized[1][h])
-        # The query in the latent space is rounded to fp16: scores err by ds, weights by 2 ds and their own rounding;
-        # so is the mixed row before its product with the value weights.
-        ds = H * scale * (np.abs(weights(*quantized[0][h]) @ x[:own]) @ np.abs(c[:, :latent]).T).max()
-        bound = (2 * ds * (1 + ds) + 2 * H) * (w @ (np.abs(c[:, :latent]) @ np.abs(wv).T)) + 1e-4
+        # The query in the latent space is rounded to fp16: scores err by ds, normalised weights by a factor within
+        # e^(2 ds) and their own rounding; so is the mixed row before its product with the value weights (fp32 sums,
+        # as the query's); below fp16's normal range weights and mixed row err by 2^-25 of the largest value each.
+        ds = (H + (own + latent + 72) * U32) * scale * (np.abs(weights(*quantized[0][h]) @ x[:own]) @ np.abs(c[:, :latent]).T).max()
+        far = np.abs(c[:, :latent]) @ np.abs(wv).T
+        bound = ((np.expm1(2 * ds) + 2 * H + 2 * (latent + 72) * U32) * (1 + 2 * H) * (w @ far)
+                 + TINY * (length * far.max(0) + np.abs(wv).sum(1)))
         assert np.all(np.abs(out[h] - w @ v) <= bound), h
 
 
