@@ -161,8 +161,13 @@ struct LatentLoads {
     int page_next = 0;   // of the wave's rows of the tile aimed at
     int gone_next = 0;   // bit i: quarter i of it has no page
 
-    __device__ __forceinline__ LatentLoads(const KvCache& cache, const NewSeq& q, int w, int l, const u4* lds)
+    // first: latent_entry's.
+    __device__ __forceinline__ LatentLoads(const KvCache& cache, const NewSeq& q, int w, int l, const u4* lds, bool one, int first)
         : c(cache), table(cache.table + (size_t)q.s * cache.cols), len(q.len), wave(w), lane(l), source(cache.k) {
+        if (one) {
+            ids = (unsigned)first < (unsigned)c.pages ? first : -1;
+            ids_first = 0;
+        }
         to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u4*)lds + 32 * D * wave);
     }
     __device__ __forceinline__ void aim(int t) {
@@ -290,6 +295,11 @@ __device__ __forceinline__ void latent_finish(const NewArgs& x, const LatentWork
     }
 }
 
+// One sequence's first table entries, requested before anything else is known.
+__device__ __forceinline__ int latent_entry(const AttnArgs& a) {
+    return a.count == 1 ? a.c.table[min((int)(threadIdx.x & 63), a.c.cols - 1)] : -1;
+}
+
 // 16 RB rows.
 template <int L, int RB>
 __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs x) {
@@ -301,6 +311,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs 
     extern __shared__ u4 lds[];
     auto& sh = *reinterpret_cast<LatentShared<L, R>*>(lds);
     const AttnArgs& a = x.a;
+    const int entry = latent_entry(a);
     const LatentWork work = latent_work(x, R);
     if (work.nrows <= 0) return;
     const int nrows = work.nrows, r0 = work.r0, t_end = work.t_end, base = work.it.q.base;
@@ -319,7 +330,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs 
         }
     }
     const float scale2 = a.scale * kLog2e;
-    Loads loads(a.c, work.it.q, wave, lane, lds);
+    Loads loads(a.c, work.it.q, wave, lane, lds, a.count == 1, entry);
     // Byte offsets in an image of the lane's operands: of step 0's keys, and of dims
     // 0's values, the first 4 of the 8 keys.  Further ones differ by whole rows and
     // 128 bytes, and by exclusive-ors below that.
@@ -503,6 +514,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_wide_kernel(New
     extern __shared__ u4 lds[];
     auto& sh = *reinterpret_cast<LatentShared<L, R>*>(lds);
     const AttnArgs& a = x.a;
+    const int entry = latent_entry(a);
     const LatentWork work = latent_work(x, R);
     if (work.nrows <= 0) return;
     const int nrows = work.nrows, r0 = work.r0, t_end = work.t_end, base = work.it.q.base;
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_wide_kernel(New
         }
     }
     const float scale2 = a.scale * kLog2e;
-    Loads loads(a.c, work.it.q, wave, lane, lds);
+    Loads loads(a.c, work.it.q, wave, lane, lds, a.count == 1, entry);
     const int k_row = 32 * kh + 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
     const uint32_t k_at = k_row * (2 * D) + 16 * (h ^ latent_swizzle<true>(k_row));
     // Values: 16 lanes take 16 dims of 4 keys; lanes 16 and up the next 16 dims, 32 and
