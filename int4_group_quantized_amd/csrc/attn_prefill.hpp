@@ -702,26 +702,26 @@ __global__ void __launch_bounds__(prefill_threads(DV, ROWS), D > 128 && ROWS == 
                     }
                 }
             }
-            if (TREE && masked) {
-                const uint64_t word = seen_word({q.mask, lo, hi, 0}, kb, it.base);
-#pragma unroll
-                for (int b = 0; b < KEYS; ++b) {
-                    const uint32_t bits = (uint32_t)(word >> (32 * (KEYS * part + b))) >> (8 * h);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[b][i] = bits >> (16 * (i >> 3) + (i & 7)) & 1 ? s[b][i] : Q4_NEG_INF;
-                }
-            } else if (masked) {
-                // seen: lo <= key < hi, as one unsigned comparison
-                const int from = kw + 8 * h - lo;
-                const unsigned count = (unsigned)max(hi - lo, 0);
-#pragma unroll
-                for (int b = 0; b < KEYS; ++b) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[b][i] = (unsigned)(from + 32 * b + 16 * (i >> 3) + (i & 7)) < count ? s[b][i] : Q4_NEG_INF;
-                }
-            }
             if (masked) {
+                if constexpr (TREE) {
+                    const uint64_t word = seen_word({q.mask, lo, hi, 0}, kb, it.base);
+#pragma unroll
+                    for (int b = 0; b < KEYS; ++b) {
+                        const uint32_t bits = (uint32_t)(word >> (32 * (KEYS * part + b))) >> (8 * h);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[b][i] = bits >> (16 * (i >> 3) + (i & 7)) & 1 ? s[b][i] : Q4_NEG_INF;
+                    }
+                } else {
+                    // seen: lo <= key < hi, as one unsigned comparison
+                    const int from = kw + 8 * h - lo;
+                    const unsigned count = (unsigned)max(hi - lo, 0);
+#pragma unroll
+                    for (int b = 0; b < KEYS; ++b) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            s[b][i] = (unsigned)(from + 32 * b + 16 * (i >> 3) + (i & 7)) < count ? s[b][i] : Q4_NEG_INF;
+                    }
+                }
                 if (gone) {
 #pragma unroll
                     for (int b = 0; b < KEYS; ++b) {
