@@ -150,15 +150,22 @@ __device__ __forceinline__ int prefill_tiles_of(const AttnArgs& a, int x) {
     return (int)(((float)(x + a.tile) - 0.5f) * a.inv_tile);
 }
 
+// Of a sequence's tokens, those that are served: of drafted ones the first max_new.
+template <bool TREE>
+__device__ __forceinline__ int prefill_served(const AttnArgs& a, int tokens) {
+    return TREE ? min(tokens, a.max_new) : tokens;
+}
+
 // Tile t of the `tiles` of sequence s, whose rows are first .. last - 1.  A
 // sequence's last tokens, which see the most positions, come first.
+template <bool TREE>
 __device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s, int first, int last, int len,
                                                        int prefix, int tiles, int t) {
     const int at = (tiles - 1 - t) * a.tile;
     PrefillTile r;
     r.s = s;
     r.token = first + at;
-    r.n = min(a.tile, min(last - first, a.max_new) - at);
+    r.n = min(a.tile, prefill_served<TREE>(a, last - first) - at);
     r.len = min(max(len, 0), a.max_length);
     r.total = last - first;
     r.base = r.len - r.total;
@@ -170,6 +177,7 @@ __device__ __forceinline__ PrefillTile prefill_tile_of(const AttnArgs& a, int s,
 // Tile number `item`.  A sequence's length and prefix are read with its rows,
 // not after them (readfirstlane and the empty assembly keep the compiler from
 // moving the reads to where they are needed: 0.1 to 0.3 us).
+template <bool TREE>
 __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item) {
     const int lane = threadIdx.x & 63;
     PrefillTile none;
@@ -180,8 +188,8 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
         const int first = of(a.q_starts[0]), last = of(a.q_starts[1]), len = of(a.lengths[0]);
         const int prefix = a.prefix ? of(a.prefix[0]) : 0;
         const int st = min(max(first, 0), a.rows), en = min(max(last, st), a.rows);
-        const int n = prefill_tiles_of(a, min(en - st, a.max_new));
-        return item < n ? prefill_tile_of(a, 0, st, en, len, prefix, n, item) : none;
+        const int n = prefill_tiles_of(a, prefill_served<TREE>(a, en - st));
+        return item < n ? prefill_tile_of<TREE>(a, 0, st, en, len, prefix, n, item) : none;
     }
     int before = 0;
     for (int s0 = 0; s0 < a.count; s0 += 64) {
@@ -195,13 +203,13 @@ __device__ __forceinline__ PrefillTile prefill_tile(const AttnArgs& a, int item)
         asm volatile("" : "+v"(st), "+v"(en), "+v"(len), "+v"(prefix));
         st = min(max(st, 0), a.rows);
         en = min(max(en, st), a.rows);
-        const int n = prefill_tiles_of(a, min(en - st, a.max_new));
+        const int n = prefill_tiles_of(a, prefill_served<TREE>(a, en - st));
         const LaneScan c = lane_scan(n);
         const uint64_t hit = __ballot(n > 0 && item < before + c.upto && item >= before + c.upto - n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
             const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-            return prefill_tile_of(a, s0 + l, of(st), of(en), of(len), of(prefix), of(n),
+            return prefill_tile_of<TREE>(a, s0 + l, of(st), of(en), of(len), of(prefix), of(n),
                                    item - (before + of(c.upto) - of(n)));
         }
         before += c.last;
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(prefill_threads(DV, ROWS), D > 128 && ROWS == 
         ids = a.c.table[min((int)(threadIdx.x & 63), a.c.cols - 1)];
         ids_first = 0;
     }
-    const PrefillTile it = prefill_tile(a, tile0 + blockIdx.z);
+    const PrefillTile it = prefill_tile<TREE>(a, tile0 + blockIdx.z);
     if (it.s < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int n = lane & 31, h = lane >> 5;
