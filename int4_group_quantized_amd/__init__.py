@@ -451,7 +451,7 @@ def q4g128_attn_prefill(q, k_cache, v_cache, table, q_starts, lengths, scale=Non
 
 
 def q4g128_attn_tree_workspace(tokens, count, heads, kv_heads, dim, max_new, max_length) -> int:
-    """Bytes of workspace that q4g128_attn_tree needs."""
+    """Bytes of workspace that q4g128_attn_tree needs (0: none)."""
     return _lib.q4g128_attn_tree_workspace(tokens, count, heads, kv_heads, dim, max_new, max_length)
 
 
