@@ -193,6 +193,30 @@ def test_tree_max_new_and_rows_of_no_sequence(dev):
             assert torch.equal(out[t], torch.full_like(out[t], 7.0) if kept else whole[t]), t
 
 
+@pytest.mark.parametrize("options", [dict(), dict(softcap=30.0, slopes=True), dict(window=300), dict(window=40, slopes=True)])
+def test_tree_options_in_parts(dev, options):
+    """Windows, caps and biases where the positions are split, and many sequences beside a long one."""
+    tree_case(dev, 18, [20, 3], [6000, 900], 4, 2, 128, 64, "any", **options)
+    tree_case(dev, 19, [i % 4 for i in range(70)], [3000 if i == 33 else 4 + 11 * i % 90 for i in range(70)], 2, 1, 64, 16, "any",
+              **options)
+
+
+def test_tree_max_new_in_parts(dev):
+    """The join leaves rows past max_new and rows of no sequence as they were."""
+    rng = np.random.default_rng(20)
+    lengths, starts = [5000, 2500] + [40] * 68, [2, 10, 15] + list(range(16, 84))
+    pool = Pool(rng, lengths, 1, 64, 64)
+    q = rng.standard_normal((90, 2, 64)).astype(np.float16)
+    args = (torch.from_numpy(q).to(dev), *pool.on(dev), i32(starts, dev), i32(lengths, dev))
+    out = torch.full((90, 2, 64), 7.0, dtype=torch.float16, device=dev)
+    q4.q4g128_attn_tree(*args, scale=0.1, max_new=6, out=out)
+    left = [0, 1, 8, 9] + list(range(83, 90))
+    assert torch.all(out[left] == 7.0)
+    whole = q4.q4g128_attn_tree(*args, scale=0.1, out=torch.zeros_like(out))
+    out[left] = whole[left]
+    check(out, q, pool, starts, lengths, 0.1, None, "max_new in parts", 0.0, 0, None)
+
+
 def test_tree_is_decode_for_one_token_and_prompt_for_a_chain(dev):
     """Within the two calls' bounds of each other, from the same definition."""
     rng = np.random.default_rng(18)

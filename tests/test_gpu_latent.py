@@ -205,6 +205,22 @@ def test_attn_max_new_and_rows_of_no_sequence(dev):
             assert torch.equal(out[t], torch.full_like(out[t], 7.0) if kept else whole[t]), t
 
 
+@pytest.mark.parametrize("heads", [2, 5, 20])
+def test_attn_max_new_in_parts(dev, heads):
+    rng = np.random.default_rng(34)
+    lengths, starts = [5000, 2500] + [40] * 68, [2, 10, 15] + list(range(16, 84))
+    pool = Rows(rng, lengths, 128, 64)
+    q = rng.standard_normal((90, heads, 128 + ROT)).astype(np.float16)
+    args = (torch.from_numpy(q).to(dev), *pool.on(dev), i32(starts, dev), i32(lengths, dev), 0.06)
+    out = torch.full((90, heads, 128), 7.0, dtype=torch.float16, device=dev)
+    q4.q4g128_latent_attn(*args, max_new=6, out=out)
+    left = [0, 1, 8, 9] + list(range(83, 90))
+    assert torch.all(out[left] == 7.0)
+    whole = q4.q4g128_latent_attn(*args, out=torch.zeros_like(out))
+    out[left] = whole[left]
+    check(out, q, pool, starts, lengths, 0.06, None, "max_new in parts")
+
+
 def test_attn_cache_in_a_larger_pool(dev):
     rng = np.random.default_rng(18)
     pool = Rows(rng, [300], 256, 32)
