@@ -501,7 +501,8 @@ Q4_API q4_status q4g128_latent_attn(const uint16_t* q, const q4g128_latent_cache
  *   expanded: a q4g128_kv_cache with a kv head for every head and dim = value (64 or
  *   128), whose keys are value + 64 wide: k [pages][heads][page][value + 64] (k_stride
  *   at least heads*page*(value+64)), v [pages][heads][value][page].  Its table may be
- *   the latent cache's, if their pages are alike.  heads at most
+ *   the latent cache's, if their pages are alike, and with equal strides (in bytes) the
+ *   pages of all three pools may interleave in one allocation.  heads at most
  *   Q4G128_MAX_HEADS.  Positions without a page in either cache are not written, and
  *   nothing but the positions named above is.  No two sequences may share a page of
  *   `expanded` that both write.

@@ -174,17 +174,29 @@ size_t k_bytes(const q4::KvCache& c) { return pool_bytes(c, c.k_stride, c.dim); 
 size_t v_bytes(const q4::KvCache& c) { return c.v ? pool_bytes(c, c.v_stride, c.dim_v) : 0; }
 size_t table_bytes(const q4::KvCache& c) { return (size_t)c.sequences * (size_t)c.cols * 4; }
 
-// Whether the two pools share an element.  Pools whose pages interleave (parts
-// of one larger pool) overlap as ranges without sharing any.
-bool pools_meet(const q4::KvCache& c) {
-    if (!overlaps(c.k, k_bytes(c), c.v, v_bytes(c))) return false;
-    if (c.k_stride != c.v_stride) return true;
-    const uintptr_t k = (uintptr_t)c.k, v = (uintptr_t)c.v;
-    const uintptr_t stride = (uintptr_t)c.k_stride * 2, cell = ((uintptr_t)c.kv_heads << c.shift) * 2;
-    // How far a page of V begins behind one of K.
-    const uintptr_t behind = v >= k ? (v - k) % stride : (stride - (k - v) % stride) % stride;
-    return behind < cell * c.dim || behind > stride - cell * c.dim_v;
+// Pages of one pool: `cell` bytes each, `stride` bytes from one to the next, `bytes` in all.
+struct Pool {
+    const void* p;
+    size_t stride, cell, bytes;
+};
+Pool k_pool(const q4::KvCache& c) {
+    return {c.k, (size_t)c.k_stride * 2, ((size_t)c.kv_heads * (size_t)c.dim << c.shift) * 2, k_bytes(c)};
 }
+Pool v_pool(const q4::KvCache& c) {
+    return {c.v, (size_t)c.v_stride * 2, ((size_t)c.kv_heads * (size_t)c.dim_v << c.shift) * 2, v_bytes(c)};
+}
+
+// Whether two pools share an element.  Pools whose pages interleave (parts of one
+// larger pool) overlap as ranges without sharing any.
+bool pools_meet(const Pool& a, const Pool& b) {
+    if (!overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
+    if (a.stride != b.stride) return true;
+    const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p, stride = a.stride;
+    // How far a page of b begins behind one of a.
+    const uintptr_t behind = q >= p ? (q - p) % stride : (stride - (p - q) % stride) % stride;
+    return behind < a.cell || behind > stride - b.cell;
+}
+bool pools_meet(const q4::KvCache& c) { return pools_meet(k_pool(c), v_pool(c)); }
 
 // Whether [p, p + bytes) meets one of the cache's pools or its table.
 bool hits_cache(const q4::KvCache& c, const void* p, size_t bytes) {
@@ -746,13 +758,14 @@ q4_status q4g128_latent_expand(const q4g128_latent_cache* cache, const int32_t* 
         return Q4_EALIGN;
     const size_t n = (size_t)expanded->kv_heads * 2 * (size_t)expanded->dim, l = (size_t)cache->latent;
     const size_t kbytes = k_bytes(a.to), vbytes = v_bytes(a.to);
-    const void* in[] = {lengths, firsts, packed, scales, mins, a.c.k, a.c.table, a.to.table};
+    const void* in[] = {lengths, firsts, packed, scales, mins, a.c.table, a.to.table};
     const size_t inbytes[] = {(size_t)count * 4, (size_t)count * 4, n * l / 2, n * (l / 128) * 2, n * (l / 128) * 2,
-                              k_bytes(a.c), table_bytes(a.c), table_bytes(a.to)};
-    for (int i = 0; i < 8; ++i)
+                              table_bytes(a.c), table_bytes(a.to)};
+    for (int i = 0; i < 7; ++i)
         if (in[i] && (overlaps(a.to.k, kbytes, in[i], inbytes[i]) || overlaps(a.to.v, vbytes, in[i], inbytes[i])))
             return Q4_EINVAL;
-    if (pools_meet(a.to)) return Q4_EINVAL;
+    const Pool rows = k_pool(a.c);
+    if (pools_meet(a.to) || pools_meet(rows, k_pool(a.to)) || pools_meet(rows, v_pool(a.to))) return Q4_EINVAL;
     a.lengths = lengths;
     a.firsts = firsts;
     a.max_length = (int)max_length;
