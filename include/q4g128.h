@@ -477,7 +477,9 @@ Q4_API q4_status q4g128_latent_keep(const q4g128_latent_cache* cache, const int3
  *   lengths, masks, max_new and max_length as in q4g128_attn_tree, workspace
  *   (q4g128_latent_attn_workspace() bytes) as in q4g128_attn_prefill; a head's value
  *   weights are applied to out by the caller.  max_new is at most Q4G128_MAX_DRAFT with masks and at most
- *   Q4G128_MAX_TOKENS without.  Numerics as stated for the attention calls.
+ *   Q4G128_MAX_TOKENS without; rows of a workgroup and parts of the positions follow it, so it should be
+ *   no larger than the longest sequence's rows: 1 for single tokens.  Numerics as stated for the
+ *   attention calls.
  *   heads at most Q4G128_MAX_HEADS; scale > 0, finite.
  */
 Q4_API int64_t q4g128_latent_attn_workspace(int32_t heads, int32_t latent, int64_t max_new);

@@ -2,10 +2,12 @@
 // (attn_prefill.hpp) with masks, which say what the last positions of a sequence see
 // of each other.
 //
-// Memory bound: every cached position costs 4 * dim bytes per kv head, once for all of
-// a tree's tokens and all heads of the group (up to 128 rows of a workgroup).  What a row
-// sees of a tile is one 64-bit word (seen_word), formed only for tiles that hold
-// drafted positions or a window's edge.
+// A cached position costs 4 * dim bytes per kv head for every 128 rows (a tree's tokens
+// times the heads of the group); the workgroups of further rows find it in L2 (16 trees of
+// 64 tokens, 256 rows each, fetch 1.08 GB of a cache of 1.07).  Few rows are bound by
+// latency, many by the matrix cores and the softmax, as prompts are.  What a row sees of
+// a tile is one 64-bit word (seen_word), formed only for tiles that hold drafted
+// positions or a window's edge.
 //
 // A kernel of its own after the decode call's, every wave with keys and values of its
 // own straight from memory into registers, for 16, 32 or 64 rows, was slower in all but

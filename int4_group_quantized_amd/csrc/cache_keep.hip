@@ -9,10 +9,11 @@
 // they share memory lines.
 //
 // Bound by the launch and a chain of three reads (bounds, pages, rows): one sequence
-// with 5 kept tokens (8 kv heads of 128) takes 3.9 us, 256 sequences with up to
-// 12 each 10.7 to 11.8 us for 14 MB read and written (the values in two to three times
-// as much, whole lines).  Numbering the values over the tokens
-// that there are, not over 32 with most lanes idle, took the latter from 20 us.
+// with 5 kept tokens takes 3.7 us (4 kv heads of 128; 3.9 with 8), 256 sequences of 8 kv
+// heads with up to 12 each 10.7 to 12.4 us for 14 MB read and written (the values in two
+// to three times as much, whole lines), with 12 each 18.5.  Numbering the values over
+// the tokens that there are, not over 32 with most lanes idle, took the call with up to
+// 12 from 20 us.
 #include "attn.hpp"
 
 namespace q4 {

@@ -18,15 +18,17 @@
 // with v_mfma_f32_16x16x32_f16, 64 rows with v_mfma_f32_32x32x16_f16.  Queries and
 // outputs stay in registers, the weights pass through LDS.
 //
-// 64 sequences of 8,192 positions (0.6 GB): 16 heads 115 us (5.1 TB/s), 64 heads 139,
-// 128 heads 208 (146 GFLOP, 700 TFLOP/s; the join 12 of it).  The last has its matrix
-// cores busy 35 to 40% of the cycles: one wave per SIMD, whose registers hold queries
-// and outputs, goes through products, softmax and barriers in turn; without the loads
-// of the next tile it would be 150, with every row from L2 187 to 209.  64 rows by
-// eight waves of 32 each, whose registers leave no room for reading operands ahead,
-// took 262; a tile's first product beside the last one's second, in tiles of 32
-// positions, 214.  Few rows are bound by latency: one sequence of 2,000 positions and
-// 16 heads takes 16 us, 5 of them the join.
+// 64 sequences of 8,192 positions (0.6 GB): 16 heads 115 us (5.2 TB/s), 64 heads 139,
+// 128 heads 205 to 211 (146 GFLOP, 690 to 710 TFLOP/s; the join 12 to 14 of it).  The
+// last has its matrix cores busy 35 to 40% of the cycles: one wave per SIMD, whose
+// registers hold queries and outputs, goes through products, softmax and barriers in
+// turn.  64 rows by eight waves of 32 each, whose registers leave no room for reading
+// operands ahead, took 262; a tile's first product beside the last one's second, in
+// tiles of 32 positions, 214.  Few rows are bound by latency: one sequence of 2,000
+// positions and 16 heads takes 16 us, 5 of them the join.
+//
+// R and the number of parts follow max_new, not the rows that there are: the first and
+// the last of the 64-sequence calls take 290 and 296 us when it is 64 instead of 1.
 //
 // A wave takes its weights from the maximum that all had after the last tile, or from
 // its own where that is 2^8 above; the waves' maxima meet with the weights.  Whole

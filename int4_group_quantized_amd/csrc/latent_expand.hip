@@ -13,12 +13,14 @@
 // [dim][position] and values as [position][dim], so that a lane holds neighbours of
 // what it stores, eight once the halves of the wave have swapped theirs.
 //
-// 4,096 positions of 64 heads of 128 (latent 512, 69 GFLOP, 168 MB written) take 84 us,
-// 1,000 of 128 heads 47, 1,900 of 16 heads 18.  Products and stores add up: without the
-// stores the first would be 63, with 12 of the 32 product steps 67; stored in halves as
-// the products leave them, 8 bytes at a time, 92; stored between the next tile's
-// products 90.  The weights are read and turned to fp16 once per workgroup: codes and
-// the fp16 results leave no other rounding than theirs and the sums' own.
+// 4,096 positions of 64 heads of 128 (latent 512, 69 GFLOP, 168 MB written) take 84 to
+// 94 us, 1,000 of 128 heads 47 to 50, 1,900 of 16 heads 18 to 20, 4,096 of 96 heads, which
+// leave 64 of 256 CUs without work, 140 to 144.  Matrix cores are busy 36% of the first
+// one's cycles: one wave per SIMD, whose registers hold the weights, goes through
+// products and stores in turn.  Where it took 84, results stored in halves as the
+// products leave them, 8 bytes at a time, took 92, stored between the next tile's products
+// 90.  The weights are read and turned to fp16 once per workgroup: codes and the fp16
+// results leave no other rounding than theirs and the sums' own.
 #include "latent.hpp"
 #include "lds_loads.hpp"
 
