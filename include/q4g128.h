@@ -323,7 +323,8 @@ Q4_API q4_status q4g128_rope_append_slots(const float* qkv, int64_t ld, int64_t 
  * also every j < prefix[s]; the tree call says what drafted tokens see.  Scores,
  * softmax statistics and sums are fp32.  The weights enter the second product
  * rounded to fp16, in units of 2 to a running maximum of the base-2 scores: at most
- * 1 in the decode call, at most 2^8 in the others, whose maximum may lag; they are
+ * 1 in the decode call, at most 2^8 in the others, whose maximum may lag (2^10 for
+ * scores of 2^24 to 2^26; rows with scores beyond that are computed far more slowly); they are
  * summed as rounded.  out is rounded once to fp16.  A query that sees nothing gives zeros.  What a masked
  * position or an absent page holds never reaches a result, NaN included.
  *   scale > 0; softcap >= 0 (0: none); both finite; window >= 0 (0: none).

@@ -290,7 +290,7 @@ __device__ __forceinline__ PrefillRow prefill_row(const AttnArgs& a, const Prefi
 // A wave's 32 rows over positions [k_begin, k_end), one position after the
 // other, never touching what a row does not see: for tiles that hold infinities
 // or NaN in masked places, where the matrix products would multiply them by
-// zero.  Lanes n and n + 32 share row n, half the dimensions each (waves that share
+// zero, and for scores far from zero (far_base).  Lanes n and n + 32 share row n, half the dimensions each (waves that share
 // it split the output dimensions too).  Far slower; all waves of a workgroup that
 // has met such a tile start their rows again here, after the fast loop and with
 // nothing of it live, because the same handling inside that loop cost it 100
@@ -365,7 +365,7 @@ struct PrefillShared {
     float base[SHARED ? WAVES : 0][32];     // and the maximum that they were taken from
     float sum[SHARED ? WAVES : 0][32];      // a wave's share of the rows' sums
     float apart[TREE ? kMaskTokens : 0];    // places of drafted tokens less their positions
-    int found[WAVES];                       // a wave has seen infinities or NaN where a row is masked
+    int found[WAVES];                       // a wave's rows have to start again
 };
 
 // TREE: drafted tokens, which see the positions before them all and those of each other
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(prefill_threads(DV, ROWS), D > 128 && ROWS == 
     const int ahead = a.images - 1;  // tiles requested ahead
     // Bit i of pages.gone() for the tiles under way, four bits each, oldest first.
     uint32_t gone_bits = 0;
-    uint32_t bad = 0;  // nonzero: a tile with masked positions holds infinities or NaN
+    uint32_t bad = 0;  // nonzero: a tile with masked positions holds infinities or NaN, or a maximum is far
     Pages pg = {};
     if (t_begin < t_end) pg = pages_of(t_begin);
     int t_load = t_begin, slot_load = 0;  // next tile to request, and its image
@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(prefill_threads(DV, ROWS), D > 128 && ROWS == 
 #pragma unroll
         for (int d = 0; d < DIMS; ++d) acc[d] *= f;
         m = m_new;
+        if constexpr (!EXTRA) bad |= far_base(m);
     };
     int slot = 0;
     // SPREAD: another tile, in one page, is requested piece by piece during the

@@ -84,8 +84,8 @@ __device__ __forceinline__ uint32_t odd_halves_in(uint32_t w) {
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 
-// A row of the workgroup over one tile that the fast loop has left out, one
-// position after the other, on top of its results in LDS.
+// A row of the workgroup over one tile that the fast loop has left out, or has scores far
+// from zero in, one position after the other, on top of its results in LDS.
 template <int L>
 __device__ __forceinline__ void latent_row_one_by_one(const NewArgs& x, const NewSeq& q, int token, int head, int kb, float* o, float& m,
                                       float& sum) {
@@ -240,26 +240,33 @@ __device__ __forceinline__ void latent_scale(float& x, float f) {
     asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1" : "+a"(x), "=&v"(v) : "v"(f));
 }
 
-// From the results in LDS (o, m, sum) to the outputs, or the parts' places.
+// From the results in LDS (o, m, sum) to the outputs, or the parts' places.  far: a base
+// was (far_base), so that all tiles are taken again.
 template <int L, int R>
-__device__ __forceinline__ void latent_finish(const NewArgs& x, const LatentWork& w, int left_from, int left_to,
+__device__ __forceinline__ void latent_finish(const NewArgs& x, const LatentWork& w, int left_from, int left_to, bool far,
                                               LatentResult<L, R>& res) {
     constexpr int D = L + kRot, WAVES = kLatentThreads / 64;
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, pmask = (1 << a.c.shift) - 1;
     const NewSeq& q = w.it.q;
     const auto out_row = [&](int r) { return (size_t)q.row * a.heads + w.r0 + r; };
+    if (far) {
+        left_from = w.it.t_begin;
+        left_to = w.t_end;
+    }
     if (left_to > 0) {
         // The same tiles in every wave; each takes rows of its own.
         for (int r = wave; r < w.nrows; r += WAVES) {
             const int token = (w.r0 + r) / a.heads, head = w.r0 + r - token * a.heads;
-            float mr = res.m[r], sum = res.sum[r];
+            float mr = far ? Q4_NEG_INF : res.m[r], sum = far ? 0.0f : res.sum[r];
+            if (far)
+                for (int i = lane; i < L; i += 64) res.o[r][i] = 0.0f;
             for (int t = left_from; t < left_to; ++t) {
                 // Whether the fast loop left it out.  It looks at tiles that some row does
                 // not see whole or that lack a page, and finds nothing in rows without one.
                 uint32_t odd = 0;
-                bool whole = t * kTileKeys + kTileKeys <= w.all_hi;
-                for (int key = t * kTileKeys; key < min((t + 1) * kTileKeys, q.len); ++key) {
+                bool whole = !far && t * kTileKeys + kTileKeys <= w.all_hi;
+                for (int key = t * kTileKeys; key < min((t + 1) * kTileKeys, q.len) && !far; ++key) {
                     const int p = page_of(a.c, a.c.table + (size_t)q.s * a.c.cols, key);
                     if (p < 0) {
                         whole = false;
@@ -269,7 +276,7 @@ __device__ __forceinline__ void latent_finish(const NewArgs& x, const LatentWork
                         reinterpret_cast<const uint32_t*>(a.c.k + (size_t)p * a.c.k_stride + (size_t)(key & pmask) * D);
                     for (int i = lane; i < D / 2; i += 64) odd |= odd_halves_in(c[i]);
                 }
-                if (!whole && __any(odd != 0)) latent_row_one_by_one<L>(x, q, token, head, t * kTileKeys, res.o[r], mr, sum);
+                if (far || (!whole && __any(odd != 0))) latent_row_one_by_one<L>(x, q, token, head, t * kTileKeys, res.o[r], mr, sum);
             }
             if (lane == 0) {
                 res.m[r] = mr;
@@ -350,6 +357,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs 
         for (int i = 0; i < DT; ++i) acc[b][i] = (f4){0, 0, 0, 0};
     }
     int left_from = 1 << 30, left_to = 0;  // tiles left for later
+    uint32_t far = 0;                      // nonzero: a base of the lane's rows was, in any wave
     uint32_t at[LOADS];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) at[j] = Loads::offset(64 * j + lane);
@@ -444,9 +452,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs 
         if (moved) {
 #pragma unroll
             for (int b = 0; b < RB; ++b) {
-                float common = sh.base[0][16 * b + n];
+                float common = Q4_NEG_INF;
 #pragma unroll
-                for (int w = 1; w < 4; ++w) common = fmaxf(common, sh.base[w][16 * b + n]);
+                for (int w = 0; w < 4; ++w) {
+                    const float theirs = sh.base[w][16 * b + n];
+                    common = fmaxf(common, theirs);
+                    far |= far_base(theirs);
+                }
                 const float f = part_weight(m[b], common);
                 l[b] *= f;
                 sums[b] *= part_weight(mine[b], common);
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_kernel(NewArgs 
     __syncthreads();
     if (tid < R) res.sum[tid] = (res.l[0][tid] + res.l[1][tid]) + (res.l[2][tid] + res.l[3][tid]);
     __syncthreads();
-    latent_finish<L, R>(x, work, left_from, left_to, res);
+    latent_finish<L, R>(x, work, left_from, left_to, __any(far != 0), res);
 }
 
 // 64 rows.  Matrix row i of 32 keys loads key 16(i/16) + 8(i/4%2) + 4(i/8%2) + i%4,
@@ -551,6 +563,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_wide_kernel(New
 #pragma unroll
         for (int i = 0; i < DT; ++i) acc[b][i] = (f16s)0.0f;
     int left_from = 1 << 30, left_to = 0;  // tiles left for later
+    uint32_t far = 0;                      // nonzero: a base of the lane's rows was, in any wave
     uint32_t at[LOADS];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) at[j] = Loads::offset(64 * j + lane);
@@ -662,6 +675,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_wide_kernel(New
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const float common = fmaxf(theirs[b][0], theirs[b][1]), f = part_weight(m[b], common);
+                far |= far_base(theirs[b][0]) || far_base(theirs[b][1]);
                 if (b == rh) {
                     l *= f;
                     sum *= part_weight(mine, common);
@@ -715,7 +729,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1) latent_attn_wide_kernel(New
     __syncthreads();
     if (tid < R) res.sum[tid] = res.l[0][tid] + res.l[1][tid];
     __syncthreads();
-    latent_finish<L, R>(x, work, left_from, left_to, res);
+    latent_finish<L, R>(x, work, left_from, left_to, __any(far != 0), res);
 }
 
 // Rows of a workgroup for `rows` query rows of a sequence.
