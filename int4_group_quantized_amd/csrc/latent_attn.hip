@@ -19,7 +19,7 @@
 // outputs stay in registers, the weights pass through LDS.
 //
 // 64 sequences of 8,192 positions (0.6 GB): 16 heads 115 us (5.2 TB/s), 64 heads 139,
-// 128 heads 205 to 211 (146 GFLOP, 690 to 710 TFLOP/s; the join 12 to 14 of it).  The
+// 128 heads 203 to 211 (146 GFLOP, 690 to 720 TFLOP/s; the join 12 to 14 of it).  The
 // last has its matrix cores busy 35 to 40% of the cycles: one wave per SIMD, whose
 // registers hold queries and outputs, goes through products, softmax and barriers in
 // turn.  64 rows by eight waves of 32 each, whose registers leave no room for reading
